@@ -5,8 +5,11 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "internal.h"
 
@@ -647,6 +650,329 @@ int decoder_attention_bwd(const void* q, const void* k, const void* v, const voi
   return cuda_status(launch_attention_bwd(q, k, v, o, lse, dout, dq, dk, dv, scratch, T, H, KV,
                                           1.0f / sqrtf(128.0f), static_cast<cudaStream_t>(stream)),
                      "decoder_attention_bwd launch");
+}
+
+// ---------------------------------------------------------------- rotary positions
+
+// A strided matrix of bf16 rows: `rows` rows of `width` elements, `stride`
+// elements apart.
+struct Rows {
+  const void* p;
+  int64_t stride, width, rows;
+  const char* name;
+};
+
+// Whether two of them share a byte.  Rows of one stride may interleave (the
+// columns of a fused tensor); of different strides, meeting byte ranges count
+// as shared.
+static bool rows_meet(const Rows& a, const Rows& b) {
+  if (!a.rows || !b.rows || !a.width || !b.width) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t ea = pa + 2 * static_cast<uintptr_t>((a.rows - 1) * a.stride + a.width);
+  const uintptr_t eb = pb + 2 * static_cast<uintptr_t>((b.rows - 1) * b.stride + b.width);
+  if (ea <= pb || eb <= pa) return false;
+  if (a.rows == 1 || b.rows == 1 || a.stride != b.stride) return true;
+  const uintptr_t pitch = 2 * static_cast<uintptr_t>(a.stride);
+  const uintptr_t off = pa >= pb ? (pa - pb) % pitch : (pitch - (pb - pa) % pitch) % pitch;
+  return off < 2 * static_cast<uintptr_t>(b.width) ||
+         off + 2 * static_cast<uintptr_t>(a.width) > pitch;
+}
+
+static int check_disjoint(const char* fn, const Rows& out, std::initializer_list<Rows> others) {
+  for (const Rows& r : others)
+    if (rows_meet(out, r))
+      return fail(HSNF4_ERR_INVALID, "%s: %s overlaps %s", fn, out.name, r.name);
+  return HSNF4_OK;
+}
+
+// *stride (0: the row itself) of rows of `width` elements
+static int check_stride(const char* fn, const char* name, int64_t* stride, int64_t width) {
+  if (*stride == 0) *stride = width;
+  if (*stride < width || *stride % 8 || *stride > (int64_t(1) << 30))
+    return fail(HSNF4_ERR_INVALID,
+                "%s: %s must be a multiple of 8, at least the row of %lld elements and at most "
+                "2^30 (got %lld)", fn, name, (long long)width, (long long)*stride);
+  return HSNF4_OK;
+}
+
+static int rope_call(const char* fn, bool backward, const hsnf4_rope* R, const int32_t* pos,
+                     int64_t T, int H, int KV, const void* q, int64_t qs, const void* k,
+                     int64_t ks, void* qo, int64_t qos, void* ko, int64_t kos, void* stream) {
+  if (!R) return fail(HSNF4_ERR_INVALID, "%s: rope is NULL", fn);
+  if (R->head_dim < 16 || R->head_dim > 256 || R->head_dim % 8 || R->rot_dim < 16 ||
+      R->rot_dim > R->head_dim || R->rot_dim % 16)
+    return fail(HSNF4_ERR_INVALID, "%s: need head_dim a multiple of 8 in [16, 256] and rot_dim a "
+                "multiple of 16 in [16, head_dim] (got %d, %d)", fn, R->head_dim, R->rot_dim);
+  if (R->n_axes < 1 || R->n_axes > 8)
+    return fail(HSNF4_ERR_INVALID, "%s: n_axes must be in [1, 8] (got %d)", fn, R->n_axes);
+  if (R->pairing != HSNF4_ROPE_HALF && R->pairing != HSNF4_ROPE_ADJACENT)
+    return fail(HSNF4_ERR_INVALID, "%s: unknown pairing %d", fn, R->pairing);
+  if (!isfinite(R->scale)) return fail(HSNF4_ERR_INVALID, "%s: scale is not finite", fn);
+  for (int i = 0; i < R->rot_dim / 2; ++i) {
+    if (!isfinite(R->inv_freq[i]))
+      return fail(HSNF4_ERR_INVALID, "%s: inv_freq[%d] is not finite", fn, i);
+    if (R->axis[i] >= R->n_axes)
+      return fail(HSNF4_ERR_INVALID, "%s: axis[%d] = %d of %d axes", fn, i, R->axis[i], R->n_axes);
+  }
+  if (T < 1 || T > (int64_t(1) << 30) || H < 1 || KV < 0 || H > 1024 || KV > 1024)
+    return fail(HSNF4_ERR_INVALID, "%s: need 1 <= T <= 2^30, 1 <= H <= 1024 and 0 <= KV <= 1024 "
+                "(got T=%lld, H=%d, KV=%d)", fn, (long long)T, H, KV);
+  int rc = check_ptrs(fn, {{q, backward ? "dq" : "q"}, {qo, backward ? "dq_out" : "q_out"}});
+  if (!rc && KV) rc = check_ptrs(fn, {{k, backward ? "dk" : "k"}, {ko, backward ? "dk_out" : "k_out"}});
+  if (!rc && !pos) rc = fail(HSNF4_ERR_INVALID, "%s: pos is NULL", fn);
+  if (!rc && (reinterpret_cast<uintptr_t>(pos) & 3))
+    rc = fail(HSNF4_ERR_INVALID, "%s: pos is not 4-byte aligned", fn);
+  if (!rc && !KV && (k || ko)) rc = fail(HSNF4_ERR_INVALID, "%s: k given with KV = 0", fn);
+  const int64_t wq = static_cast<int64_t>(H) * R->head_dim,
+                wk = static_cast<int64_t>(KV) * R->head_dim;
+  if (!rc) rc = check_stride(fn, backward ? "dq_stride" : "q_stride", &qs, wq);
+  if (!rc) rc = check_stride(fn, backward ? "dq_out_stride" : "q_out_stride", &qos, wq);
+  if (!rc && KV) rc = check_stride(fn, backward ? "dk_stride" : "k_stride", &ks, wk);
+  if (!rc && KV) rc = check_stride(fn, backward ? "dk_out_stride" : "k_out_stride", &kos, wk);
+  if (rc) return rc;
+  const Rows rq = {q, qs, wq, T, backward ? "dq" : "q"};
+  const Rows rk = {k, ks, wk, KV ? T : 0, backward ? "dk" : "k"};
+  const Rows rqo = {qo, qos, wq, T, backward ? "dq_out" : "q_out"};
+  const Rows rko = {ko, kos, wk, KV ? T : 0, backward ? "dk_out" : "k_out"};
+  // pos as one row of 16-bit words
+  const Rows rp = {pos, 0, 2 * R->n_axes * T, 1, "pos"};
+  const bool q_in_place = q == qo && qs == qos, k_in_place = k == ko && ks == kos;
+  if (!q_in_place) rc = check_disjoint(fn, rqo, {rq});
+  if (!rc) rc = check_disjoint(fn, rqo, {rk, rko, rp});
+  if (!rc && !k_in_place) rc = check_disjoint(fn, rko, {rk});
+  if (!rc) rc = check_disjoint(fn, rko, {rq, rp});
+  if (rc) return rc;
+  const RopeTensors t = {{q, k}, {qo, ko}, {qs, ks}, {qos, kos}, pos};
+  return cuda_status(launch_rope(*R, t, T, H, KV, backward, static_cast<cudaStream_t>(stream)),
+                     backward ? "decoder_rope_bwd launch" : "decoder_rope_fwd launch");
+}
+
+int decoder_rope_fwd(const hsnf4_rope* rope, const int32_t* pos, int64_t T, int H, int KV,
+                     const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                     void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                     void* stream) {
+  return rope_call("decoder_rope_fwd", false, rope, pos, T, H, KV, q, q_stride, k, k_stride,
+                   q_out, q_out_stride, k_out, k_out_stride, stream);
+}
+
+int decoder_rope_bwd(const hsnf4_rope* rope, const int32_t* pos, int64_t T, int H, int KV,
+                     const void* dq, int64_t dq_stride, const void* dk, int64_t dk_stride,
+                     void* dq_out, int64_t dq_out_stride, void* dk_out, int64_t dk_out_stride,
+                     void* stream) {
+  return rope_call("decoder_rope_bwd", true, rope, pos, T, H, KV, dq, dq_stride, dk, dk_stride,
+                   dq_out, dq_out_stride, dk_out, dk_out_stride, stream);
+}
+
+// ---------------------------------------------------------------- packed attention
+
+static int check_packed_sizes(const char* fn, int64_t Tq, int64_t Tk, int n_seq, int H, int KV,
+                              int d) {
+  const int64_t most = int64_t(1) << 24;
+  if (Tq < 1 || Tk < 1 || Tq > most || Tk > most || n_seq < 1 || n_seq > 65535 || H < 1 ||
+      H > 1024 || KV < 1 || H % KV)
+    return fail(HSNF4_ERR_INVALID, "%s: need 1 <= Tq, Tk <= 2^24, 1 <= n_seq <= 65535 and H <= "
+                "1024 a multiple of KV (got Tq=%lld, Tk=%lld, n_seq=%d, H=%d, KV=%d)", fn,
+                (long long)Tq, (long long)Tk, n_seq, H, KV);
+  if (d != 64 && d != 128)
+    return fail(HSNF4_ERR_INVALID, "%s: head_dim must be 64 or 128 (got %d)", fn, d);
+  return HSNF4_OK;
+}
+
+// checks *a and fills its zero strides
+static int check_packed(const char* fn, hsnf4_packed_attention* a) {
+  int rc = check_packed_sizes(fn, a->Tq, a->Tk, a->n_seq, a->H, a->KV, a->head_dim);
+  if (!rc) rc = check_ptrs(fn, {{a->q, "q"}, {a->k, "k"}, {a->v, "v"}});
+  if (rc) return rc;
+  const std::pair<const int32_t*, const char*> cus[] = {{a->cu_q, "cu_q"}, {a->cu_k, "cu_k"}};
+  for (auto& c : cus) {
+    if (!c.first) return fail(HSNF4_ERR_INVALID, "%s: %s is NULL", fn, c.second);
+    if (reinterpret_cast<uintptr_t>(c.first) & 3)
+      return fail(HSNF4_ERR_INVALID, "%s: %s is not 4-byte aligned", fn, c.second);
+  }
+  if (a->causal != 0 && a->causal != 1)
+    return fail(HSNF4_ERR_INVALID, "%s: causal must be 0 or 1 (got %d)", fn, a->causal);
+  if (!(isfinite(a->scale) && a->scale > 0.0f))
+    return fail(HSNF4_ERR_INVALID, "%s: scale must be finite and > 0 (got %g)", fn,
+                static_cast<double>(a->scale));
+  const int64_t wq = static_cast<int64_t>(a->H) * a->head_dim,
+                wk = static_cast<int64_t>(a->KV) * a->head_dim;
+  rc = check_stride(fn, "q_stride", &a->q_stride, wq);
+  if (!rc) rc = check_stride(fn, "k_stride", &a->k_stride, wk);
+  if (!rc) rc = check_stride(fn, "v_stride", &a->v_stride, wk);
+  return rc;
+}
+
+int decoder_attention_packed_fwd(const hsnf4_packed_attention* args, void* o, int64_t o_stride,
+                                 float* lse, void* stream) {
+  static const char* fn = "decoder_attention_packed_fwd";
+  if (!args) return fail(HSNF4_ERR_INVALID, "%s: a is NULL", fn);
+  hsnf4_packed_attention a = *args;
+  int rc = check_packed(fn, &a);
+  if (!rc) rc = check_ptrs(fn, {{o, "o"}, {lse, "lse"}});
+  const int64_t wq = static_cast<int64_t>(a.H) * a.head_dim,
+                wk = static_cast<int64_t>(a.KV) * a.head_dim;
+  if (!rc) rc = check_stride(fn, "o_stride", &o_stride, wq);
+  if (rc) return rc;
+  const Rows q = {a.q, a.q_stride, wq, a.Tq, "q"}, k = {a.k, a.k_stride, wk, a.Tk, "k"},
+             v = {a.v, a.v_stride, wk, a.Tk, "v"}, ro = {o, o_stride, wq, a.Tq, "o"},
+             rl = {lse, 0, 2 * a.H * a.Tq, 1, "lse"};
+  rc = check_disjoint(fn, ro, {q, k, v, rl});
+  if (!rc) rc = check_disjoint(fn, rl, {q, k, v});
+  if (rc) return rc;
+  return cuda_status(launch_packed_fwd(a, o, o_stride, lse, static_cast<cudaStream_t>(stream)),
+                     "decoder_attention_packed_fwd launch");
+}
+
+size_t decoder_attention_packed_workspace(int64_t Tq, int64_t Tk, int n_seq, int H, int KV,
+                                          int head_dim) {
+  if (check_packed_sizes("decoder_attention_packed_workspace", Tq, Tk, n_seq, H, KV, head_dim))
+    return 0;
+  return packed_workspace_bytes(Tq, Tk, n_seq, H, KV, head_dim);
+}
+
+int decoder_attention_packed_bwd(const hsnf4_packed_attention* args, const void* o,
+                                 int64_t o_stride, const float* lse, const void* dout,
+                                 int64_t dout_stride, void* dq, int64_t dq_stride, void* dk,
+                                 int64_t dk_stride, void* dv, int64_t dv_stride, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  static const char* fn = "decoder_attention_packed_bwd";
+  if (!args) return fail(HSNF4_ERR_INVALID, "%s: a is NULL", fn);
+  hsnf4_packed_attention a = *args;
+  int rc = check_packed(fn, &a);
+  if (!rc)
+    rc = check_ptrs(fn, {{o, "o"}, {lse, "lse"}, {dout, "dout"}, {dq, "dq"}, {dk, "dk"},
+                         {dv, "dv"}});
+  const int64_t wq = static_cast<int64_t>(a.H) * a.head_dim,
+                wk = static_cast<int64_t>(a.KV) * a.head_dim;
+  if (!rc) rc = check_stride(fn, "o_stride", &o_stride, wq);
+  if (!rc) rc = check_stride(fn, "dout_stride", &dout_stride, wq);
+  if (!rc) rc = check_stride(fn, "dq_stride", &dq_stride, wq);
+  if (!rc) rc = check_stride(fn, "dk_stride", &dk_stride, wk);
+  if (!rc) rc = check_stride(fn, "dv_stride", &dv_stride, wk);
+  if (rc) return rc;
+  const size_t need = packed_workspace_bytes(a.Tq, a.Tk, a.n_seq, a.H, a.KV, a.head_dim);
+  rc = check_workspace(fn, workspace, ws_bytes, need);
+  if (rc) return rc;
+  const Rows in[] = {{a.q, a.q_stride, wq, a.Tq, "q"},
+                     {a.k, a.k_stride, wk, a.Tk, "k"},
+                     {a.v, a.v_stride, wk, a.Tk, "v"},
+                     {o, o_stride, wq, a.Tq, "o"},
+                     {dout, dout_stride, wq, a.Tq, "dout"},
+                     {lse, 0, 2 * a.H * a.Tq, 1, "lse"},
+                     {workspace, 0, static_cast<int64_t>(need / 2), 1, "workspace"}};
+  const Rows out[] = {{dq, dq_stride, wq, a.Tq, "dq"},
+                      {dk, dk_stride, wk, a.Tk, "dk"},
+                      {dv, dv_stride, wk, a.Tk, "dv"}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Rows& r : in)
+      if ((rc = check_disjoint(fn, out[i], {r}))) return rc;
+    for (int j = 0; j < i; ++j)
+      if ((rc = check_disjoint(fn, out[i], {out[j]}))) return rc;
+  }
+  for (int j = 0; j < 6; ++j)
+    if ((rc = check_disjoint(fn, in[6], {in[j]}))) return rc;
+  const PackedBwd b = {o, lse, dout, dq, dk, dv, o_stride, dout_stride, dq_stride, dk_stride,
+                       dv_stride};
+  return cuda_status(launch_packed_bwd(a, b, workspace, static_cast<cudaStream_t>(stream)),
+                     "decoder_attention_packed_bwd launch");
+}
+
+// ---------------------------------------------------------------- gradient norm
+
+size_t lora_grad_table_bytes(int n) { return n < 1 || n > 65536 ? 0 : grad_table_bytes(n); }
+
+int lora_grad_plan(const hsnf4_grad* grads, int n, void* table, size_t table_bytes,
+                   hsnf4_grad_plan* plan, void* stream) {
+  static const char* fn = "lora_grad_plan";
+  if (!grads || !plan) return fail(HSNF4_ERR_INVALID, "%s: %s is NULL", fn, grads ? "plan" : "grads");
+  if (n < 1 || n > 65536)
+    return fail(HSNF4_ERR_INVALID, "%s: 1..65536 tensors (got %d)", fn, n);
+  int rc = check_ptrs(fn, {{table, "table"}});
+  if (rc) return rc;
+  if (table_bytes < grad_table_bytes(n))
+    return fail(HSNF4_ERR_OOM, "%s: table too small: need %zu bytes, given %zu", fn,
+                grad_table_bytes(n), table_bytes);
+  // byte ranges: every out against every other range, but its own g in place
+  struct Range {
+    uintptr_t a, b;
+    int i;
+    bool out;
+  };
+  std::unique_ptr<Range[]> r(new (std::nothrow) Range[2 * static_cast<size_t>(n)]);
+  if (!r) return fail(HSNF4_ERR_OOM, "%s: no host memory", fn);
+  int m = 0;
+  int64_t elements = 0;
+  for (int i = 0; i < n; ++i) {
+    const hsnf4_grad& g = grads[i];
+    if (g.dtype != HSNF4_F32 && g.dtype != HSNF4_BF16 && g.dtype != HSNF4_F16)
+      return fail(HSNF4_ERR_INVALID, "%s: tensor %d has unknown type %d", fn, i, g.dtype);
+    if (g.n < 0 || g.n > (int64_t(1) << 40))
+      return fail(HSNF4_ERR_INVALID, "%s: tensor %d has %lld elements", fn, i, (long long)g.n);
+    if (!g.n) continue;
+    const uintptr_t size = g.dtype == HSNF4_F32 ? 4 : 2;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(g.g), o = reinterpret_cast<uintptr_t>(g.out);
+    if (!a || !o || a % size || o % size)
+      return fail(HSNF4_ERR_INVALID, "%s: tensor %d is NULL or not aligned to its element", fn, i);
+    elements += g.n;
+    r[m++] = {a, a + size * static_cast<uintptr_t>(g.n), i, a == o};
+    if (a != o) r[m++] = {o, o + size * static_cast<uintptr_t>(g.n), i, true};
+  }
+  // in order of their starts, a range that is written meets another exactly
+  // when it meets the furthest-reaching range before it, or the furthest
+  // written one does
+  std::sort(r.get(), r.get() + m, [](const Range& x, const Range& y) {
+    return x.a != y.a ? x.a < y.a : x.i < y.i;
+  });
+  int far = -1, far_out = -1;  // furthest end so far, of any range and of a written one
+  for (int j = 0; j < m; ++j) {
+    const int hit = r[j].out ? far : far_out;
+    if (hit >= 0 && r[hit].b > r[j].a)
+      return fail(HSNF4_ERR_INVALID, "%s: tensors %d and %d overlap where one is written", fn,
+                  r[hit].i, r[j].i);
+    if (far < 0 || r[j].b > r[far].b) far = j;
+    if (r[j].out && (far_out < 0 || r[j].b > r[far_out].b)) far_out = j;
+  }
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  rc = cuda_status(cudaStreamIsCapturing(st, &cap), "lora_grad_plan: cudaStreamIsCapturing");
+  if (rc) return rc;
+  if (cap != cudaStreamCaptureStatusNone)
+    return fail(HSNF4_ERR_STATE, "%s: the table cannot be filled during stream capture", fn);
+  int64_t chunks = 0;
+  rc = cuda_status(fill_grad_table(grads, n, table, &chunks, st), "lora_grad_plan: table copy");
+  if (rc) return rc;
+  *plan = {table, chunks, elements, n, 0};
+  return HSNF4_OK;
+}
+
+size_t lora_grad_workspace(const hsnf4_grad_plan* plan) {
+  return plan ? grad_workspace_bytes(plan->chunks) : 0;
+}
+
+static int grad_call(const char* fn, const hsnf4_grad_plan* plan, float max_norm, bool scale,
+                     float* norm, void* ws, size_t ws_bytes, void* stream) {
+  if (!plan || !plan->table || plan->n < 1 || plan->chunks < 0)
+    return fail(HSNF4_ERR_INVALID, "%s: plan is NULL or was not filled by lora_grad_plan", fn);
+  if (!(max_norm >= 0.0f))
+    return fail(HSNF4_ERR_INVALID, "%s: max_norm must be >= 0 (got %g)", fn,
+                static_cast<double>(max_norm));
+  if (!norm || (reinterpret_cast<uintptr_t>(norm) & 3))
+    return fail(HSNF4_ERR_INVALID, "%s: norm is NULL or not 4-byte aligned", fn);
+  int rc = check_workspace(fn, ws, ws_bytes, grad_workspace_bytes(plan->chunks));
+  if (rc) return rc;
+  return cuda_status(launch_grad_norm(plan->table, plan->n, plan->chunks, max_norm, scale, norm,
+                                      ws, static_cast<cudaStream_t>(stream)),
+                     scale ? "lora_grad_clip launch" : "lora_grad_norm launch");
+}
+
+int lora_grad_norm(const hsnf4_grad_plan* plan, float* norm, void* workspace, size_t ws_bytes,
+                   void* stream) {
+  return grad_call("lora_grad_norm", plan, 0.0f, false, norm, workspace, ws_bytes, stream);
+}
+
+int lora_grad_clip(const hsnf4_grad_plan* plan, float max_norm, float* norm, void* workspace,
+                   size_t ws_bytes, void* stream) {
+  return grad_call("lora_grad_clip", plan, max_norm, true, norm, workspace, ws_bytes, stream);
 }
 
 static hsnf4_lora_fwd_args one_fwd(const hsnf4_nf4_weight* W, const void* X, const void* A,

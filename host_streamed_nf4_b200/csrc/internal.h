@@ -173,6 +173,39 @@ cudaError_t launch_attention_bwd(const void* q, const void* k, const void* v, co
                                  float* D, int64_t T, int H, int KV, float scale,
                                  cudaStream_t st);
 
+// ---- rotary positions (rope.cu): [0] = q, [1] = k (KV heads; 0: none)
+struct RopeTensors {
+  const void* in[2];
+  void* out[2];
+  int64_t in_stride[2], out_stride[2];
+  const int32_t* pos;
+};
+cudaError_t launch_rope(const hsnf4_rope& R, const RopeTensors& t, int64_t T, int H, int KV,
+                        bool backward, cudaStream_t st);
+
+// ---- gradient norm and clipping (grad_norm.cu).  fill_grad_table builds the
+// device table of n tensors and counts their chunks.
+size_t grad_table_bytes(int n);
+size_t grad_workspace_bytes(int64_t chunks);
+cudaError_t fill_grad_table(const hsnf4_grad* grads, int n, void* table, int64_t* chunks,
+                            cudaStream_t st);
+cudaError_t launch_grad_norm(const void* table, int n, int64_t chunks, float max_norm, bool scale,
+                             float* norm, void* ws, cudaStream_t st);
+
+// ---- attention over packed sequences (attention_packed.cu)
+struct PackedBwd {
+  const void* o;
+  const float* lse;
+  const void* dout;
+  void *dq, *dk, *dv;
+  int64_t o_stride, do_stride, dq_stride, dk_stride, dv_stride;
+};
+size_t packed_workspace_bytes(int64_t Tq, int64_t Tk, int n_seq, int H, int KV, int d);
+cudaError_t launch_packed_fwd(const hsnf4_packed_attention& a, void* o, int64_t o_stride,
+                              float* lse, cudaStream_t st);
+cudaError_t launch_packed_bwd(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws,
+                              cudaStream_t st);
+
 // Kernel timing (hsnf4_profile): bracket a launch with prof_begin/prof_end.
 enum ProfKind {
   kProfGemmFwd = 0,

@@ -76,6 +76,35 @@ class GemmPlanInfo(Structure):
                 ("fixup_tiles", ctypes.c_int32)]
 
 
+ROPE_HALF, ROPE_ADJACENT = 0, 1
+ROPE_MAX_PAIRS = 128
+GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class RopeC(Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("pairing", ctypes.c_int32), ("scale", c_float),
+                ("inv_freq", c_float * ROPE_MAX_PAIRS), ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS)]
+
+
+class PackedAttentionC(Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("q_stride", c_int64),
+                ("k_stride", c_int64), ("v_stride", c_int64), ("cu_q", c_void_p),
+                ("cu_k", c_void_p), ("Tq", c_int64), ("Tk", c_int64), ("n_seq", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("KV", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("scale", c_float)]
+
+
+class GradC(Structure):
+    _fields_ = [("g", c_void_p), ("out", c_void_p), ("n", c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class GradPlanC(Structure):
+    _fields_ = [("table", c_void_p), ("chunks", c_int64), ("elements", c_int64),
+                ("n", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class HsNf4Error(RuntimeError):
     def __init__(self, status: int, detail: str):
         super().__init__(f"[{status}] {detail}")
@@ -114,6 +143,24 @@ _SIGS = {
     "decoder_attention_bwd": ([c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int,
                                c_void_p], c_int),
+    "decoder_rope_fwd": ([POINTER(RopeC), c_void_p, c_int64, c_int, c_int] +
+                         [c_void_p, c_int64] * 4 + [c_void_p], c_int),
+    "decoder_rope_bwd": ([POINTER(RopeC), c_void_p, c_int64, c_int, c_int] +
+                         [c_void_p, c_int64] * 4 + [c_void_p], c_int),
+    "decoder_attention_packed_fwd": ([POINTER(PackedAttentionC), c_void_p, c_int64, c_void_p,
+                                      c_void_p], c_int),
+    "decoder_attention_packed_workspace": ([c_int64, c_int64, c_int, c_int, c_int, c_int],
+                                           c_size_t),
+    "decoder_attention_packed_bwd": ([POINTER(PackedAttentionC), c_void_p, c_int64, c_void_p] +
+                                     [c_void_p, c_int64] * 4 + [c_void_p, c_size_t, c_void_p],
+                                     c_int),
+    "lora_grad_table_bytes": ([c_int], c_size_t),
+    "lora_grad_plan": ([POINTER(GradC), c_int, c_void_p, c_size_t, POINTER(GradPlanC), c_void_p],
+                       c_int),
+    "lora_grad_workspace": ([POINTER(GradPlanC)], c_size_t),
+    "lora_grad_norm": ([POINTER(GradPlanC), c_void_p, c_void_p, c_size_t, c_void_p], c_int),
+    "lora_grad_clip": ([POINTER(GradPlanC), c_float, c_void_p, c_void_p, c_size_t, c_void_p],
+                       c_int),
     "lora_dropout_apply": ([c_void_p, c_int64, c_int64, c_float, c_uint64, c_uint64, c_void_p,
                             c_void_p], c_int),
     "lora_linear_fwd_workspace": ([c_int64, c_int64, c_int64, c_int], c_size_t),
@@ -413,6 +460,267 @@ def attention_bwd(q, k, v, o, lse, dout, H, KV, dq=None, dk=None, dv=None, scrat
                                        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(scratch), T, H, KV,
                                        _stream(stream)))
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ rotary positions
+
+def _on(dev: torch.device, stream=None):
+    """(raw stream, guard): the stream a call on device `dev` takes, and the
+    context to make it in (the library launches on the current device)."""
+    guard = _NO_GUARD if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if s.device != dev:
+        raise ValueError(f"the stream is on {s.device}, the tensors on {dev}")
+    return s.cuda_stream, guard
+
+
+class _NoGuard:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_GUARD = _NoGuard()
+
+
+def _rows(t: torch.Tensor, name: str, dev, rows=None, cols=None) -> int:
+    """Row stride of a bf16 [rows, cols] CUDA tensor with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name} must be two-dimensional with contiguous rows")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def rope_inv_freq(rot_dim: int, theta: float) -> torch.Tensor:
+    """theta^(-2i / rot_dim) for i < rot_dim / 2, in 64 bits rounded to fp32."""
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    return (float(theta) ** (-2.0 * i / rot_dim)).to(torch.float32)
+
+
+class Rope:
+    """Rotary positions of a head: the frequencies, and the axis each follows.
+
+    inv_freq: rot_dim / 2 frequencies (rope_inv_freq, or any other table);
+    values of a head past rot_dim are not turned.  sections: how many
+    frequencies each axis has (time, height, width), in order; interleaved
+    deals them out in turn instead (0, 1, 2, 0, 1, 2, ... while an axis has
+    some left).  pairing "half" turns (i, i + rot_dim / 2), "adjacent"
+    (2i, 2i + 1).  scale multiplies the rotation."""
+
+    def __init__(self, head_dim: int, inv_freq, sections=None, interleaved: bool = False,
+                 pairing: str = "half", scale: float = 1.0):
+        f = [float(x) for x in inv_freq]
+        if len(f) > ROPE_MAX_PAIRS:
+            raise ValueError(f"at most {ROPE_MAX_PAIRS} frequencies (got {len(f)})")
+        if pairing not in ("half", "adjacent"):
+            raise ValueError(f"pairing must be 'half' or 'adjacent' (got {pairing!r})")
+        sections = [len(f)] if sections is None else [int(n) for n in sections]
+        if sum(sections) != len(f) or min(sections) < 0:
+            raise ValueError(f"sections {sections} do not add up to {len(f)} frequencies")
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        if interleaved:
+            axis = [a for i in range(max(sections)) for a, n in enumerate(sections) if i < n]
+        self.n_axes, self.head_dim = len(sections), int(head_dim)
+        self.c = RopeC(self.head_dim, 2 * len(f), self.n_axes,
+                       ROPE_HALF if pairing == "half" else ROPE_ADJACENT, float(scale))
+        self.c.inv_freq[:len(f)] = f
+        self.c.axis[:len(f)] = axis
+        self._ref = ctypes.byref(self.c)
+
+
+def _rope(fn, rope, pos, q, k, q_out, k_out, stream):
+    T, dev = q.shape[0], q.device
+    if pos.dtype != torch.int32 or pos.device != dev or not pos.is_contiguous() or \
+            pos.numel() != rope.n_axes * T:
+        raise ValueError(f"pos must be a contiguous int32 [{rope.n_axes}, {T}] tensor on {dev}")
+    qs = _rows(q, "q", dev)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
+    qos = _rows(q_out, "q_out", dev, T, q.shape[1])
+    H, KV, ks, kos = q.shape[1] // rope.head_dim, 0, 0, 0
+    if H * rope.head_dim != q.shape[1]:
+        raise ValueError(f"q has {q.shape[1]} columns, not a multiple of {rope.head_dim}")
+    if k is not None:
+        ks = _rows(k, "k", dev, T)
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev) if k_out is None else k_out
+        kos = _rows(k_out, "k_out", dev, T, k.shape[1])
+        KV = k.shape[1] // rope.head_dim
+        if KV * rope.head_dim != k.shape[1]:
+            raise ValueError(f"k has {k.shape[1]} columns, not a multiple of {rope.head_dim}")
+    st, guard = _on(dev, stream)
+    with guard:
+        _check(fn(rope._ref, pos.data_ptr(), T, H, KV, q.data_ptr(), qs, _p(k), ks,
+                  q_out.data_ptr(), qos, _p(k_out), kos, st))
+    return (q_out, k_out) if k is not None else q_out
+
+
+def rope_fwd(rope: Rope, pos, q, k=None, q_out=None, k_out=None, stream=None):
+    """q [T, H * head_dim] and k [T, KV * head_dim] turned to their positions
+    pos (int32 [n_axes, T], or [T] for one axis).  Rows may be strided
+    (columns of a fused tensor); q_out / k_out may be q / k.  Returns
+    (q_out, k_out), or q_out without k."""
+    return _rope(lib().decoder_rope_fwd, rope, pos, q, k, q_out, k_out, stream)
+
+
+def rope_bwd(rope: Rope, pos, dq, dk=None, dq_out=None, dk_out=None, stream=None):
+    """Gradients of rope_fwd's inputs from those of its outputs."""
+    return _rope(lib().decoder_rope_bwd, rope, pos, dq, dk, dq_out, dk_out, stream)
+
+
+# ------------------------------------------------------------------ packed attention
+
+def _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale):
+    dev = q.device
+    Tq, Tk = q.shape[0], k.shape[0]
+    if H < 1 or KV < 1 or q.shape[1] % H:
+        raise ValueError(f"q has {q.shape[1]} columns for {H} heads (KV heads: {KV})")
+    d = q.shape[1] // H
+    qs = _rows(q, "q", dev)
+    ks, vs = _rows(k, "k", dev, Tk, KV * d), _rows(v, "v", dev, Tk, KV * d)
+    cu_k = cu_q if cu_k is None else cu_k
+    for c, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
+        if c.dtype != torch.int32 or c.device != dev or c.dim() != 1 or not c.is_contiguous() or \
+                c.numel() != cu_q.numel() or c.numel() < 2:
+            raise ValueError(f"{name} must be a contiguous int32 [n_seq + 1] tensor on {dev}")
+    return PackedAttentionC(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cu_q.data_ptr(),
+                            cu_k.data_ptr(), Tq, Tk, cu_q.numel() - 1, H, KV, d, int(bool(causal)),
+                            d ** -0.5 if scale is None else float(scale)), d
+
+
+def attention_packed_fwd(q, k, v, cu_q, H, KV, causal=True, cu_k=None, scale=None, o=None,
+                         lse=None, stream=None):
+    """Attention over packed sequences: q [Tq, H * d], k, v [Tk, KV * d]
+    (rows may be strided), sequence s the tokens cu_q[s]..cu_q[s + 1] (int32,
+    on the device; cu_k: the keys', if they differ).  Rows outside every
+    sequence are left as they are in o and lse.  Returns (o, lse [H, Tq])."""
+    a, d = _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale)
+    dev = q.device
+    if o is None:
+        o = torch.zeros(q.shape, dtype=q.dtype, device=dev)
+    if lse is None:
+        lse = torch.zeros(H, q.shape[0], dtype=torch.float32, device=dev)
+    os_ = _rows(o, "o", dev, q.shape[0], H * d)
+    _lse(lse, H, q)
+    st, guard = _on(dev, stream)
+    with guard:
+        _check(lib().decoder_attention_packed_fwd(ctypes.byref(a), o.data_ptr(), os_,
+                                                  lse.data_ptr(), st))
+    return o, lse
+
+
+def _lse(lse, H, q):
+    if lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous() or \
+            lse.numel() != H * q.shape[0]:
+        raise ValueError(f"lse must be a contiguous fp32 [{H}, {q.shape[0]}] tensor on {q.device}")
+
+
+def attention_packed_workspace_bytes(Tq, Tk, n_seq, H, KV, d) -> int:
+    n = int(lib().decoder_attention_packed_workspace(Tq, Tk, n_seq, H, KV, d))
+    if n == 0:
+        raise HsNf4Error(ERR_INVALID, last_error())
+    return n
+
+
+def attention_packed_bwd(q, k, v, o, lse, dout, cu_q, H, KV, causal=True, cu_k=None, scale=None,
+                         dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Its gradients from the forward's o and lse: (dq, dk, dv).  Rows outside
+    every sequence are left as they are."""
+    a, d = _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale)
+    dev, Tq, Tk = q.device, q.shape[0], k.shape[0]
+    dq = torch.zeros(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
+    dk = torch.zeros(k.shape, dtype=k.dtype, device=dev) if dk is None else dk
+    dv = torch.zeros(v.shape, dtype=v.dtype, device=dev) if dv is None else dv
+    strides = [_rows(t, name, dev, T, n * d) for t, name, T, n in
+               ((o, "o", Tq, H), (dout, "dout", Tq, H), (dq, "dq", Tq, H), (dk, "dk", Tk, KV),
+                (dv, "dv", Tk, KV))]
+    _lse(lse, H, q)
+    st, guard = _on(dev, stream)
+    with guard:
+        if workspace is None:
+            workspace = torch.empty(
+                attention_packed_workspace_bytes(Tq, Tk, a.n_seq, H, KV, d), dtype=torch.uint8,
+                device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        _check(lib().decoder_attention_packed_bwd(
+            ctypes.byref(a), o.data_ptr(), strides[0], lse.data_ptr(), dout.data_ptr(), strides[1],
+            dq.data_ptr(), strides[2], dk.data_ptr(), strides[3], dv.data_ptr(), strides[4],
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st))
+    return dq, dk, dv
+
+
+# ------------------------------------------------------------------ gradient norm
+
+class GradSet:
+    """A fixed list of gradient tensors (fp32, bf16 or fp16, contiguous, any
+    mix) for grad_norm and grad_clip.  outs: where clipped gradients go, each
+    of its gradient's type and size (default: in place).  The set keeps the
+    tensors' addresses, so their memory must not be replaced."""
+
+    def __init__(self, tensors, outs=None, stream=None):
+        self.tensors = list(tensors)
+        self.outs = self.tensors if outs is None else list(outs)
+        if not self.tensors or len(self.outs) != len(self.tensors):
+            raise ValueError("GradSet takes one tensor or more, and as many outs")
+        dev = self.tensors[0].device
+        for i, (g, o) in enumerate(zip(self.tensors, self.outs)):
+            if g.dtype not in GRAD_DTYPES or o.dtype != g.dtype:
+                raise TypeError(f"tensor {i}: fp32, bf16 or fp16 and its out the same "
+                                f"(got {g.dtype}, {o.dtype})")
+            if not g.is_cuda or g.device != dev or o.device != dev:
+                raise ValueError(f"tensor {i} is not on {dev}")
+            if not g.is_contiguous() or not o.is_contiguous() or o.numel() != g.numel():
+                raise ValueError(f"tensor {i} or its out is not contiguous, or sizes differ")
+        n = len(self.tensors)
+        arr = (GradC * n)(*[GradC(g.data_ptr(), o.data_ptr(), g.numel(), GRAD_DTYPES[g.dtype], 0)
+                            for g, o in zip(self.tensors, self.outs)])
+        self.device, self.plan = dev, GradPlanC()
+        st, guard = _on(dev, stream)
+        with guard:
+            self.table = torch.empty(max(int(lib().lora_grad_table_bytes(n)), 16),
+                                     dtype=torch.uint8, device=dev)
+            _check(lib().lora_grad_plan(arr, n, self.table.data_ptr(), self.table.numel(),
+                                        ctypes.byref(self.plan), st))
+            self.workspace = self.new_workspace()
+        self._ref = ctypes.byref(self.plan)
+
+    def new_workspace(self) -> torch.Tensor:
+        """A workspace for calls that may run at the same time as others on
+        this set (which otherwise share its own)."""
+        return torch.empty(int(lib().lora_grad_workspace(ctypes.byref(self.plan))),
+                           dtype=torch.uint8, device=self.device)
+
+    def _call(self, fn, args, norm, workspace, stream):
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=self.device)
+        elif norm.dtype != torch.float32 or norm.device != self.device or norm.numel() != 1:
+            raise ValueError(f"norm must be one fp32 value on {self.device}")
+        ws = self.workspace if workspace is None else workspace
+        if ws.device != self.device or not ws.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        st, guard = _on(self.device, stream)
+        with guard:
+            _check(fn(self._ref, *args, norm.data_ptr(), ws.data_ptr(),
+                      ws.numel() * ws.element_size(), st))
+        return norm
+
+
+def grad_norm(grads: GradSet, norm=None, workspace=None, stream=None) -> torch.Tensor:
+    """The 2-norm of every gradient of the set together (fp32 scalar tensor)."""
+    return grads._call(lib().lora_grad_norm, (), norm, workspace, stream)
+
+
+def grad_clip(grads: GradSet, max_norm: float, norm=None, workspace=None,
+              stream=None) -> torch.Tensor:
+    """Scale every gradient of the set by min(1, max_norm / (norm + 1e-6));
+    returns the norm before that."""
+    return grads._call(lib().lora_grad_clip, (float(max_norm),), norm, workspace, stream)
 
 
 # ------------------------------------------------------------------ LoRA linear

@@ -23,7 +23,8 @@
  * Conventions for every entry point:
  *   - All tensors are row-major and contiguous.  bf16 tensors are passed as
  *     raw 16-bit storage (void*).  Pointers are DEVICE pointers unless a
- *     parameter says "host".  Device pointers must be 16-byte aligned.
+ *     parameter says "host".  Device pointers must be 16-byte aligned
+ *     unless a parameter says otherwise.
  *   - `stream` is a cudaStream_t passed as void*; NULL means the legacy
  *     default stream.  Work is enqueued asynchronously on it; results are
  *     valid once the stream has reached that point.
@@ -405,6 +406,165 @@ size_t decoder_attention_scratch_bytes(int64_t T, int H);
 int decoder_attention_bwd(const void *q, const void *k, const void *v, const void *o,
                           const float *lse, const void *dout, void *dq, void *dk, void *dv,
                           float *scratch, int64_t T, int H, int KV, void *stream);
+
+/* ----------------------------------------------------------------------- */
+/* Rotary positions, packed sequences, gradient clipping                    */
+/* ----------------------------------------------------------------------- */
+/* What a training step on real batches adds to the layer above: rotary
+ * positions of q and k (with several axes for images and video), attention
+ * over several sequences packed into one token axis, and the clipping of
+ * the adapter gradients by their global norm.  (The pages train these model
+ * families but print none of it.) */
+
+/* Rotary positions.  Each head's first rot_dim values are rot_dim / 2
+ * pairs; pair i of token t turns by pos[axis[i]][t] * inv_freq[i]:
+ *   y1 = scale (x1 cos - x2 sin),  y2 = scale (x2 cos + x1 sin),
+ * the angle formed and reduced in double, the rotation in fp32, rounded once
+ * to bf16; values from rot_dim on pass unchanged.  Pairs are (i, i +
+ * rot_dim/2) or (2i, 2i + 1).  Several axes (time, height, width) give each
+ * frequency its own row of positions; any frequency table may be passed
+ * (plain, or stretched for long contexts), scale multiplies its rotation. */
+#define HSNF4_ROPE_HALF 0     /* pairs (i, i + rot_dim / 2) */
+#define HSNF4_ROPE_ADJACENT 1 /* pairs (2i, 2i + 1) */
+#define HSNF4_ROPE_MAX_PAIRS 128
+
+typedef struct {
+  int32_t head_dim;   /* multiple of 8, 16..256 */
+  int32_t rot_dim;    /* multiple of 16, 16..head_dim */
+  int32_t n_axes;     /* rows of pos, 1..8 */
+  int32_t pairing;    /* HSNF4_ROPE_HALF or HSNF4_ROPE_ADJACENT */
+  float scale;        /* finite; 1 for plain rotary positions */
+  float inv_freq[HSNF4_ROPE_MAX_PAIRS];  /* of pair i < rot_dim / 2; finite */
+  uint8_t axis[HSNF4_ROPE_MAX_PAIRS];    /* of pair i, in [0, n_axes) */
+} hsnf4_rope;
+
+/* q_out = turned q [T, H, head_dim], k_out = turned k [T, KV, head_dim]
+ * (k and k_out NULL and KV 0: q only).  Heads are contiguous; *_stride is
+ * the distance between tokens in elements (0: heads * head_dim), so that q
+ * and k may be columns of one wider tensor.  An output may be exactly its
+ * input (same pointer and stride) but not overlap it, or anything else the
+ * call reads or writes, in any other way.  pos: int32 [n_axes, T], device
+ * memory, any value.  Errors: INVALID (sizes, strides below the row or not
+ * multiples of 8, pointers, table), CUDA. */
+int decoder_rope_fwd(const hsnf4_rope *rope, const int32_t *pos, int64_t T, int H, int KV,
+                     const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                     void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                     void *stream);
+
+/* Its backward, the transposed rotation: dq, dk are the gradients of
+ * decoder_rope_fwd's outputs, dq_out, dk_out those of its inputs. */
+int decoder_rope_bwd(const hsnf4_rope *rope, const int32_t *pos, int64_t T, int H, int KV,
+                     const void *dq, int64_t dq_stride, const void *dk, int64_t dk_stride,
+                     void *dq_out, int64_t dq_out_stride, void *dk_out, int64_t dk_out_stride,
+                     void *stream);
+
+/* Attention over packed sequences: sequence s holds query tokens
+ * [cu_q[s], cu_q[s+1]) of q [Tq, H, head_dim] and key tokens
+ * [cu_k[s], cu_k[s+1]) of k, v [Tk, KV, head_dim]; a query sees the keys of
+ * its own sequence only.  With causal set, the last query of a sequence
+ * stands on its last key: query i of lq sees keys j <= i + lk - lq of lk.
+ * Query head h reads KV head h / (H / KV).
+ *   o = softmax(scale q k^T) v,  lse = log sum e^(scale q k^T)
+ * A query that sees no key gives o = 0, lse = -inf and no gradient; a key
+ * that no query sees gets zero gradients.  Rows outside every sequence are
+ * neither read into a result nor written.  Products take bf16 operands with
+ * fp32 accumulation (the probabilities and their gradients are rounded to
+ * bf16 as operands); softmax statistics are fp32. */
+typedef struct {
+  const void *q, *k, *v;  /* bf16; heads contiguous within a token */
+  int64_t q_stride, k_stride, v_stride; /* elements between tokens (multiples
+                             of 8; 0: heads * head_dim) */
+  const int32_t *cu_q;    /* device int32 [n_seq + 1], not decreasing */
+  const int32_t *cu_k;    /* the same for the keys; may be cu_q */
+  int64_t Tq, Tk;         /* tokens of the tensors; 1..2^24.  Values of cu_q,
+                             cu_k outside [0, Tq], [0, Tk] are clamped */
+  int32_t n_seq;          /* 1..65535 */
+  int32_t H, KV;          /* H % KV == 0, H <= 1024 */
+  int32_t head_dim;       /* 64 or 128 */
+  int32_t causal;         /* 0 or 1 */
+  float scale;            /* finite and > 0 */
+} hsnf4_packed_attention;
+
+/* o bf16 [Tq, H, head_dim] (o_stride as above), lse fp32 [H, Tq].  o and
+ * lse may not overlap the inputs.  Errors: INVALID (sizes, strides,
+ * pointers), CUDA. */
+int decoder_attention_packed_fwd(const hsnf4_packed_attention *a, void *o, int64_t o_stride,
+                                 float *lse, void *stream);
+
+/* Workspace bytes of the backward (depends on the device's SM count); 0 for
+ * sizes that it refuses. */
+size_t decoder_attention_packed_workspace(int64_t Tq, int64_t Tk, int n_seq, int H, int KV,
+                                          int head_dim);
+
+/* The gradients, the probabilities recomputed from lse:
+ *   D = sum(dout o),  P = e^(scale q k^T - lse),  dS = P (dout v^T - D)
+ *   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dout
+ * (dk, dv added over each KV group's query heads in a fixed order; no
+ * atomics).  o and lse are the forward's; dq [Tq, H, head_dim], dk, dv
+ * [Tk, KV, head_dim] are overwritten and may not overlap the inputs or each
+ * other (they may be interleaved columns of one tensor).  workspace: device
+ * scratch of at least decoder_attention_packed_workspace() bytes, 256-byte
+ * aligned; its contents do not matter, and calls that may run at the same
+ * time need one each.  Errors: INVALID, OOM (workspace), CUDA. */
+int decoder_attention_packed_bwd(const hsnf4_packed_attention *a, const void *o, int64_t o_stride,
+                                 const float *lse, const void *dout, int64_t dout_stride,
+                                 void *dq, int64_t dq_stride, void *dk, int64_t dk_stride,
+                                 void *dv, int64_t dv_stride, void *workspace, size_t ws_bytes,
+                                 void *stream);
+
+/* Gradient norm and clipping over many tensors (a stack has 14 adapter
+ * gradients a layer).  Describe the tensors once, then clip every step:
+ * the plan keeps their addresses in a table in caller-owned device memory,
+ * so they must stay where they are while the plan is used. */
+#define HSNF4_F32 0
+#define HSNF4_BF16 1
+#define HSNF4_F16 2
+
+typedef struct {
+  const void *g;   /* device; aligned to its element */
+  void *out;       /* where the clipped gradient goes: g itself, or a tensor
+                      that overlaps no g and no other out */
+  int64_t n;       /* elements, >= 0, at most 2^40 */
+  int32_t dtype;   /* HSNF4_F32, HSNF4_BF16, HSNF4_F16 */
+  int32_t reserved; /* 0 */
+} hsnf4_grad;
+
+typedef struct {
+  const void *table;
+  int64_t chunks;
+  int64_t elements;
+  int32_t n;
+  int32_t reserved;
+} hsnf4_grad_plan;
+
+/* Device bytes of the table of n tensors. */
+size_t lora_grad_table_bytes(int n);
+
+/* Fill the table (device memory of table_bytes >= lora_grad_table_bytes(n),
+ * 16-byte aligned) on `stream`, and the plan (host).  grads: host array of
+ * n (1..65536) tensors.  Not during stream capture.  Errors: INVALID (sizes,
+ * pointers, tensors that overlap), OOM (table), STATE (capture), CUDA. */
+int lora_grad_plan(const hsnf4_grad *grads, int n, void *table, size_t table_bytes,
+                   hsnf4_grad_plan *plan, void *stream);
+
+/* Workspace bytes of the two calls below (at least 256; depends on the
+ * device's SM count). */
+size_t lora_grad_workspace(const hsnf4_grad_plan *plan);
+
+/* *norm (device fp32) = sqrt(sum g^2) over every tensor of the plan, the
+ * squares added in fp32 within 16 bytes and in double beyond (finite
+ * gradients never overflow it before the final rounding to fp32). */
+int lora_grad_norm(const hsnf4_grad_plan *plan, float *norm, void *workspace, size_t ws_bytes,
+                   void *stream);
+
+/* *norm as above, then out = round(g * c), c = min(1, max_norm / (norm +
+ * 1e-6)), for every tensor.  max_norm >= 0, infinity: c = 1.  A norm that
+ * is not finite gives c = 0 (infinite) or NaN, as the formula does.  In
+ * place, a tensor that c = 1 would leave alone is not written.  workspace:
+ * device scratch, 256-byte aligned, one per call that may run at the same
+ * time; its contents do not matter.  Errors: INVALID, OOM, CUDA. */
+int lora_grad_clip(const hsnf4_grad_plan *plan, float max_norm, float *norm, void *workspace,
+                   size_t ws_bytes, void *stream);
 
 /* ----------------------------------------------------------------------- */
 /* Host-pinned NF4 base -> VRAM ring streamer                              */
