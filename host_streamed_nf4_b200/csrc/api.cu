@@ -97,12 +97,13 @@ int hsnf4_device_status(void* stream, uint32_t* flags) {
   int rc = cuda_status(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)),
                        "hsnf4_device_status: cudaStreamSynchronize");
   if (rc) return rc;
-  uint32_t f = 0, fr = 0, fm = 0;
+  uint32_t f = 0, fr = 0, fm = 0, fa = 0;
   rc = cuda_status(read_gemm_flags(&f), "hsnf4_device_status: read flags");
   if (!rc) rc = cuda_status(read_rank_flags(&fr), "hsnf4_device_status: read flags");
   if (!rc) rc = cuda_status(read_merge_flags(&fm), "hsnf4_device_status: read flags");
+  if (!rc) rc = cuda_status(read_attn_flags(&fa), "hsnf4_device_status: read flags");
   if (rc) return rc;
-  f |= fr | fm;
+  f |= fr | fm | fa;
   *flags = f;
   if (f) return fail(HSNF4_ERR_DEVICE, "a kernel wait gave up (flags 0x%x)", f);
   return HSNF4_OK;

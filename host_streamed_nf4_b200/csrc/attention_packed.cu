@@ -14,16 +14,17 @@
 // could give (tokens / tile + sequences), so no length is needed on the host.
 #include <cuda_bf16.h>
 
+#include <stdlib.h>
 #include <algorithm>
 #include <atomic>
 
 #include "internal.h"
+#include "packed.cuh"
 
 namespace hsnf4 {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 64;
 
 struct PackedArgs {
@@ -33,55 +34,10 @@ struct PackedArgs {
   float* D;           // [H, Tq]
   float* part;        // backward: [splits][2][Tk][KV][d] partial dK, dV (splits > 1)
   int64_t qs, ks, vs, os, dos, dqs, dks, dvs;  // token strides
-  const int32_t *cu_q, *cu_k;
-  int Tq, Tk, n_seq, H, KV, causal, splits;
+  PackedSeqs S;
+  int H, KV, splits;
   float scale;
 };
-
-struct Tile {
-  int q0, lq, k0, lk;  // the sequence's first query and key token and its lengths
-  int t;               // tile of the sequence (of its queries or of its keys)
-};
-
-__device__ __forceinline__ void seq_range(const int32_t* cu, int s, int T, int& a, int& len) {
-  const int b = min(max(__ldg(cu + s), 0), T), e = min(__ldg(cu + s + 1), T);
-  a = b;
-  len = max(e - b, 0);
-}
-
-// Tile number `slot` over all sequences in order, tiles of `rows` tokens of
-// the queries (or keys); a sequence's tiles come last first (with a causal
-// mask its longest first).  Whole warp; false if there is no such tile.
-__device__ __forceinline__ bool find_tile(const PackedArgs& P, bool keys, int slot, int rows,
-                                          Tile& x) {
-  const int lane = threadIdx.x & 31;
-  const int32_t* cu = keys ? P.cu_k : P.cu_q;
-  const int T = keys ? P.Tk : P.Tq;
-  int before = 0;
-  for (int s0 = 0; s0 < P.n_seq; s0 += 32) {
-    int a = 0, len = 0;
-    if (s0 + lane < P.n_seq) seq_range(cu, s0 + lane, T, a, len);
-    const int n = (len + rows - 1) / rows;
-    int inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    const int lo = before + inc - n;
-    const unsigned hit = __ballot_sync(0xffffffffu, slot >= lo && slot < lo + n);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      const int s = s0 + src;
-      x.t = __shfl_sync(0xffffffffu, n - 1 - (slot - lo), src);
-      seq_range(P.cu_q, s, P.Tq, x.q0, x.lq);
-      seq_range(P.cu_k, s, P.Tk, x.k0, x.lk);
-      return true;
-    }
-    before = __shfl_sync(0xffffffffu, before + inc, 31);
-  }
-  return false;
-}
 
 __device__ __forceinline__ uint32_t su32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -210,11 +166,6 @@ __device__ __forceinline__ void zero(float (&acc)[D / 8][4]) {
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
 }
 
-// keys that query row i of the sequence sees: [0, limit)
-__device__ __forceinline__ int key_limit(const PackedArgs& P, const Tile& x, int i) {
-  return P.causal ? min(max(i + x.lk - x.lq + 1, 0), x.lk) : x.lk;
-}
-
 // ---------------------------------------------------------------- forward
 template <int D>
 __global__ void __launch_bounds__(128) packed_fwd_kernel(const __grid_constant__ PackedArgs P) {
@@ -222,16 +173,16 @@ __global__ void __launch_bounds__(128) packed_fwd_kernel(const __grid_constant__
   constexpr int kEl = kTile * (D + 8);
   uint16_t* Qs = reinterpret_cast<uint16_t*>(smem);
   uint16_t* KVs = Qs + kEl;  // K0 V0 K1 V1
-  Tile x;
+  PackedTile x;
   const int h = blockIdx.x % P.H;
-  if (!find_tile(P, false, blockIdx.x / P.H, kTile, x)) return;
+  if (!find_tile(P.S, false, blockIdx.x / P.H, kTile, x)) return;
   const int kh = h / (P.H / P.KV);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, qd = lane & 3;
   const int m0 = warp * 16, r0 = x.t * kTile;
   const uint16_t* q = P.q + x.q0 * P.qs + h * D;
   const uint16_t* k = P.k + x.k0 * P.ks + kh * D;
   const uint16_t* v = P.v + x.k0 * P.vs + kh * D;
-  const int tiles = (key_limit(P, x, min(r0 + kTile, x.lq) - 1) + kTile - 1) / kTile;
+  const int tiles = (key_limit(P.S, x, min(r0 + kTile, x.lq) - 1) + kTile - 1) / kTile;
   load_rows<D>(Qs, q, r0, x.lq, P.qs);
   if (tiles) {
     load_rows<D>(KVs, k, 0, x.lk, P.ks);
@@ -243,7 +194,7 @@ __global__ void __launch_bounds__(128) packed_fwd_kernel(const __grid_constant__
   float acc[D / 8][4];
   zero<D>(acc);
   const int rows[2] = {r0 + m0 + g, r0 + m0 + g + 8};
-  const int lim[2] = {key_limit(P, x, rows[0]), key_limit(P, x, rows[1])};
+  const int lim[2] = {key_limit(P.S, x, rows[0]), key_limit(P.S, x, rows[1])};
   for (int kt = 0; kt < tiles; ++kt) {
     const uint16_t* Ks = KVs + ((kt & 1) * 2) * kEl;
     if (kt + 1 < tiles) {
@@ -304,7 +255,7 @@ __global__ void __launch_bounds__(128) packed_fwd_kernel(const __grid_constant__
       *reinterpret_cast<uint32_t*>(dst + n * 8 + 2 * qd) =
           pack_bf16(acc[n][2 * hr] * inv, acc[n][2 * hr + 1] * inv);
     if (qd == 0)
-      P.lse[static_cast<int64_t>(h) * P.Tq + x.q0 + rows[hr]] =
+      P.lse[static_cast<int64_t>(h) * P.S.Tq + x.q0 + rows[hr]] =
           lim[hr] ? (m[hr] + log2f(l[hr])) / kLog2e : -INFINITY;
   }
 }
@@ -319,15 +270,15 @@ __global__ void __launch_bounds__(128) packed_dq_kernel(const __grid_constant__ 
   uint16_t* Os = dOs + kEl;
   uint16_t* KVs = Os + kEl;  // K0 V0 K1 V1
   __shared__ float Ds[kTile];
-  Tile x;
+  PackedTile x;
   const int h = blockIdx.x % P.H;
-  if (!find_tile(P, false, blockIdx.x / P.H, kTile, x)) return;
+  if (!find_tile(P.S, false, blockIdx.x / P.H, kTile, x)) return;
   const int kh = h / (P.H / P.KV);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, qd = lane & 3;
   const int m0 = warp * 16, r0 = x.t * kTile;
   const uint16_t* k = P.k + x.k0 * P.ks + kh * D;
   const uint16_t* v = P.v + x.k0 * P.vs + kh * D;
-  const int tiles = (key_limit(P, x, min(r0 + kTile, x.lq) - 1) + kTile - 1) / kTile;
+  const int tiles = (key_limit(P.S, x, min(r0 + kTile, x.lq) - 1) + kTile - 1) / kTile;
   load_rows<D>(Qs, P.q + x.q0 * P.qs + h * D, r0, x.lq, P.qs);
   load_rows<D>(dOs, P.dout + x.q0 * P.dos + h * D, r0, x.lq, P.dos);
   load_rows<D>(Os, P.o + x.q0 * P.os + h * D, r0, x.lq, P.os);
@@ -352,7 +303,7 @@ __global__ void __launch_bounds__(128) packed_dq_kernel(const __grid_constant__ 
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     if (!half) {
       Ds[row] = sum;
-      if (r0 + row < x.lq) P.D[static_cast<int64_t>(h) * P.Tq + x.q0 + r0 + row] = sum;
+      if (r0 + row < x.lq) P.D[static_cast<int64_t>(h) * P.S.Tq + x.q0 + r0 + row] = sum;
     }
   }
   __syncthreads();
@@ -363,9 +314,9 @@ __global__ void __launch_bounds__(128) packed_dq_kernel(const __grid_constant__ 
 #pragma unroll
   for (int hr = 0; hr < 2; ++hr) {
     const bool in = rows[hr] < x.lq;
-    lse2[hr] = in ? P.lse[static_cast<int64_t>(h) * P.Tq + x.q0 + rows[hr]] * kLog2e : 0.0f;
+    lse2[hr] = in ? P.lse[static_cast<int64_t>(h) * P.S.Tq + x.q0 + rows[hr]] * kLog2e : 0.0f;
     Dr[hr] = Ds[m0 + g + 8 * hr];
-    lim[hr] = in ? key_limit(P, x, rows[hr]) : 0;
+    lim[hr] = in ? key_limit(P.S, x, rows[hr]) : 0;
   }
   float acc[D / 8][4];
   zero<D>(acc);
@@ -418,14 +369,14 @@ __global__ void __launch_bounds__(128) packed_dkdv_kernel(const __grid_constant_
   float* LD = reinterpret_cast<float*>(QD + 4 * kEl);  // per buffer: lse [64], D [64]
   const int per = P.KV * P.splits;
   const int kh = blockIdx.x % per / P.splits, split = blockIdx.x % per % P.splits;
-  Tile x;
-  if (!find_tile(P, true, blockIdx.x / per, kTile, x)) return;
+  PackedTile x;
+  if (!find_tile(P.S, true, blockIdx.x / per, kTile, x)) return;
   const int G = P.H / P.KV;
   const int h0 = kh * G + G * split / P.splits, h1 = kh * G + G * (split + 1) / P.splits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, qd = lane & 3;
   const int m0 = warp * 16, c0 = x.t * kTile;
   // the first query that sees the tile's first key, and so the first query tile
-  const int first = P.causal ? max(c0 - (x.lk - x.lq), 0) : 0;
+  const int first = P.S.causal ? max(c0 - (x.lk - x.lq), 0) : 0;
   const int qt0 = first / kTile, qt1 = (x.lq + kTile - 1) / kTile;
   const int per_head = max(qt1 - qt0, 0), n = per_head * (h1 - h0);
   auto stage = [&](int i, int b) {
@@ -435,7 +386,7 @@ __global__ void __launch_bounds__(128) packed_dkdv_kernel(const __grid_constant_
     load_rows<D>(q + kEl, P.dout + x.q0 * P.dos + h * D, qt * kTile, x.lq, P.dos);
     for (int j = threadIdx.x; j < kTile; j += blockDim.x) {
       const int row = qt * kTile + j;
-      const int64_t at = static_cast<int64_t>(h) * P.Tq + x.q0 + row;
+      const int64_t at = static_cast<int64_t>(h) * P.S.Tq + x.q0 + row;
       LD[b * 128 + j] = row < x.lq ? P.lse[at] * kLog2e : 0.0f;
       LD[b * 128 + 64 + j] = row < x.lq ? P.D[at] : 0.0f;
     }
@@ -464,7 +415,7 @@ __global__ void __launch_bounds__(128) packed_dkdv_kernel(const __grid_constant_
     // an entry is on if the key exists and the query, which exists, sees it
     auto on = [&](int j, int e) {
       const int key = keys[e >> 1], row = qt * kTile + j * 8 + 2 * qd + (e & 1);
-      return key < x.lk && row < x.lq && (!P.causal || key <= row + x.lk - x.lq);
+      return key < x.lk && row < x.lq && (!P.S.causal || key <= row + x.lk - x.lq);
     };
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -487,7 +438,7 @@ __global__ void __launch_bounds__(128) packed_dkdv_kernel(const __grid_constant_
     if (keys[hr] >= x.lk) continue;
     const int64_t tok = x.k0 + keys[hr];
     if (P.splits > 1) {
-      const int64_t one = static_cast<int64_t>(P.Tk) * P.KV * D;
+      const int64_t one = static_cast<int64_t>(P.S.Tk) * P.KV * D;
       float* pk = P.part + 2 * split * one + (tok * P.KV + kh) * D;
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) {
@@ -513,10 +464,10 @@ __global__ void __launch_bounds__(128) packed_dkdv_kernel(const __grid_constant_
 // dK, dV of every token that belongs to a sequence, the shares added in order
 template <int D>
 __global__ void __launch_bounds__(256) packed_kv_reduce_kernel(const __grid_constant__ PackedArgs P) {
-  Tile x;
-  if (!find_tile(P, true, blockIdx.x, kTile, x)) return;
+  PackedTile x;
+  if (!find_tile(P.S, true, blockIdx.x, kTile, x)) return;
   const int rows = min(kTile, x.lk - x.t * kTile);
-  const int64_t one = static_cast<int64_t>(P.Tk) * P.KV * D;
+  const int64_t one = static_cast<int64_t>(P.S.Tk) * P.KV * D;
   const int per_row = P.KV * (D / 4);
   for (int i = threadIdx.x; i < rows * per_row; i += 256) {
     const int64_t tok = x.k0 + x.t * kTile + i / per_row;
@@ -574,14 +525,14 @@ PackedArgs args_of(const hsnf4_packed_attention& a) {
   P.qs = a.q_stride;
   P.ks = a.k_stride;
   P.vs = a.v_stride;
-  P.cu_q = a.cu_q;
-  P.cu_k = a.cu_k;
-  P.Tq = static_cast<int>(a.Tq);
-  P.Tk = static_cast<int>(a.Tk);
-  P.n_seq = a.n_seq;
+  P.S.cu_q = a.cu_q;
+  P.S.cu_k = a.cu_k;
+  P.S.Tq = static_cast<int>(a.Tq);
+  P.S.Tk = static_cast<int>(a.Tk);
+  P.S.n_seq = a.n_seq;
   P.H = a.H;
   P.KV = a.KV;
-  P.causal = a.causal;
+  P.S.causal = a.causal;
   P.scale = a.scale;
   P.splits = 1;
   return P;
@@ -593,7 +544,7 @@ cudaError_t fwd(const PackedArgs& P, cudaStream_t st) {
   const int smem = 5 * kTile * (D + 8) * 2;
   cudaError_t e = allow_smem(packed_fwd_kernel<D>, smem, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = most_tiles(P.Tq, P.n_seq, kTile) * P.H;
+  const int64_t grid = most_tiles(P.S.Tq, P.S.n_seq, kTile) * P.H;
   count_launch();
   packed_fwd_kernel<D><<<static_cast<unsigned>(grid), 128, smem, st>>>(P);
   return cudaGetLastError();
@@ -607,9 +558,9 @@ cudaError_t bwd(const PackedArgs& P, cudaStream_t st) {
   cudaError_t e = allow_smem(packed_dq_kernel<D>, smem_q, done_q);
   if (e == cudaSuccess) e = allow_smem(packed_dkdv_kernel<D>, smem_kv, done_kv);
   if (e != cudaSuccess) return e;
-  const int64_t kt = most_tiles(P.Tk, P.n_seq, kTile);
+  const int64_t kt = most_tiles(P.S.Tk, P.S.n_seq, kTile);
   count_launch();
-  packed_dq_kernel<D><<<static_cast<unsigned>(most_tiles(P.Tq, P.n_seq, kTile) * P.H), 128, smem_q,
+  packed_dq_kernel<D><<<static_cast<unsigned>(most_tiles(P.S.Tq, P.S.n_seq, kTile) * P.H), 128, smem_q,
                         st>>>(P);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -626,6 +577,7 @@ cudaError_t bwd(const PackedArgs& P, cudaStream_t st) {
 
 // D [H, Tq] fp32, then the shares' fp32 dK, dV
 size_t packed_workspace_bytes(int64_t Tq, int64_t Tk, int n_seq, int H, int KV, int d) {
+  if (!getenv("HX")) return packed_tc_workspace_bytes(Tq, Tk, n_seq, H, KV, d);
   const int splits = head_splits(Tk, H, KV);
   size_t n = round_up(static_cast<size_t>(H) * Tq * 4, 256);
   if (splits > 1) n += static_cast<size_t>(splits) * 2 * Tk * KV * d * 4;
@@ -634,6 +586,7 @@ size_t packed_workspace_bytes(int64_t Tq, int64_t Tk, int n_seq, int H, int KV, 
 
 cudaError_t launch_packed_fwd(const hsnf4_packed_attention& a, void* o, int64_t o_stride,
                               float* lse, cudaStream_t st) {
+  if (!getenv("HX")) return launch_packed_fwd_tc(a, o, o_stride, lse, st);
   PackedArgs P = args_of(a);
   P.out = static_cast<uint16_t*>(o);
   P.os = o_stride;
@@ -643,6 +596,7 @@ cudaError_t launch_packed_fwd(const hsnf4_packed_attention& a, void* o, int64_t 
 
 cudaError_t launch_packed_bwd(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws,
                               cudaStream_t st) {
+  if (!getenv("HX")) return launch_packed_bwd_tc(a, b, ws, st);
   PackedArgs P = args_of(a);
   P.o = static_cast<const uint16_t*>(b.o);
   P.os = b.o_stride;

@@ -1,0 +1,1167 @@
+// attention_tc.cu -- attention over packed sequences on tcgen05 (sm_100a),
+// forward and backward.
+#include <cuda_bf16.h>
+
+#include <string.h>
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "attention_tc.cuh"
+#include "internal.h"
+#include "packed.cuh"
+
+namespace hsnf4 {
+
+__device__ unsigned int g_attn_flags;
+
+namespace {
+
+enum : unsigned int {
+  kAtFlagLoad = 1u << 19,
+  kAtFlagMma = 1u << 20,
+  kAtFlagCompute = 1u << 21,
+  kAtFlagDrain = 1u << 22,
+};
+
+// Of every kPolyOf pairs of exponentials, kPolyPart go to the fp32 pipe.
+constexpr int kPolyOf = 8, kPolyPart = 3;
+constexpr int kComputeWarps = 16;  // four per SM sub-partition
+constexpr int kTcThreads = 32 * (kComputeWarps + 2);
+constexpr int kMmaWarp = kComputeWarps, kLoadWarp = kComputeWarps + 1;
+
+// A wait of the whole loading warp, which leaves whole when it gives up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, volatile int* abort,
+                                          unsigned int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort, &g_attn_flags, site));
+}
+
+// Wait of the whole loading warp for a tile that it will patch.  Giving up,
+// it first lets the copy land (or the limit pass) before the shared memory
+// goes away.
+__device__ __forceinline__ bool tail_landed(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_wait(bar, parity, abort, &g_attn_flags, kAtFlagLoad)))
+    return true;
+  volatile int never = 0;
+  mbar_wait(bar, parity, &never, &g_attn_flags, kAtFlagDrain);
+  return false;
+}
+
+// Two warps (64 threads) that share the rows of a tile: a barrier, and votes
+// over both.
+__device__ __forceinline__ void pair_sync(int id) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool pair_any(int id, bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool pair_all(int id, bool v) { return !pair_any(id, !v); }
+
+// 32 columns of this warp's lanes
+__device__ __forceinline__ void load_quarter(uint32_t taddr, uint32_t* r) {
+  tmem_ld32_at(taddr, r);
+  tmem_wait_ld();
+  tie32(r);
+}
+
+// ---------------------------------------------------------------- forward
+
+struct FwdTc {
+  CUtensorMap mq, mk, mv;
+  uint16_t* out;
+  float* lse;
+  int64_t os;
+  PackedSeqs S;
+  int H, KV;
+  float c;  // scale * log2(e)
+};
+
+template <int D>
+struct FwdGeo {
+  static constexpr int kTile = tile_bytes<D>();
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kSmem = (2 + kStages) * kTile;
+};
+
+// A CTA takes 256 query rows of one head as two tiles of 128 and walks the
+// keys 128 at a time.  Each tile has eight warps: a row belongs to two
+// threads, in two warps, 64 of the 128 keys each.  TMEM: S0 S1 (128 columns each; P overwrites its S as bf16), O0 O1.
+// The tensor cores work on one tile's products while the other tile's
+// warpgroup computes its probabilities.
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) packed_fwd_tc(const __grid_constant__ FwdTc P) {
+  using G = FwdGeo<D>;
+  constexpr int NS = G::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t q_full, kv_full[NS], kv_empty[NS], aux, s_full[2], p_full[2][2], o_full[2],
+      drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ float row_x[2][2][kRows];  // [half][tile][row]: exchanged between two warps
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&aux, 1);
+    mbar_init(&drain, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t][0], 8);
+      mbar_init(&p_full[t][1], 8);
+      mbar_init(&o_full[t], 1);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort_p = &abort_flag;
+  pdl_wait_then_release();
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need the alignment asked for
+    if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    return;
+  }
+
+  PackedTile x = {};
+  const int h = blockIdx.x % P.H, kh = h / (P.H / P.KV);
+  const bool work = find_tile(P.S, false, blockIdx.x / P.H, 2 * kRows, x);
+  int last_load = -1, n = 0, nt[2] = {0, 0};
+  bool q_loaded = false, mma_issued = false;
+  const int r0 = x.t * 2 * kRows;
+  if (work) {
+    for (int t = 0; t < 2; ++t) {
+      const int first = r0 + t * kRows, end = min(first + kRows, x.lq);
+      if (first < end) nt[t] = (key_limit(P.S, x, end - 1) + kRows - 1) / kRows;
+      n = max(n, nt[t]);
+    }
+  }
+  uint8_t* ring = smem + 2 * G::kTile;
+
+  if (warp == kLoadWarp && n) {
+    // ---------------------------------------------- TMA: Q, then K0 V0 K1 V1 ...
+    const bool two = r0 + kRows < x.lq;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * G::kTile);
+      tma_tile<D>(smem, &P.mq, &q_full, h * D, x.q0 + r0);
+      if (two) tma_tile<D>(smem + G::kTile, &P.mq, &q_full, h * D, x.q0 + r0 + kRows);
+    }
+    q_loaded = true;
+    for (int i = 0; i < 2 * n; ++i) {
+      const int s = i % NS, row = (i >> 1) * kRows;
+      if (i >= NS && !__all_sync(0xffffffffu, mbar_wait(&kv_empty[s], ((i / NS) - 1) & 1, abort_p,
+                                                         &g_attn_flags, kAtFlagLoad)))
+        break;
+      uint8_t* st = ring + s * G::kTile;
+      const CUtensorMap* map = (i & 1) ? &P.mv : &P.mk;
+      if ((i & 1) && row + kRows > x.lk) {
+        // the keys behind the sequence have probability 0; their values must
+        // be finite for the product: zeros
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&aux, G::kTile);
+          tma_tile<D>(st, map, &aux, kh * D, x.k0 + row);
+        }
+        __syncwarp();
+        if (!tail_landed(&aux, 0, abort_p)) break;
+        zero_rows<D>(st, x.lk - row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[s]);
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(&kv_full[s], G::kTile);
+        tma_tile<D>(st, map, &kv_full[s], kh * D, x.k0 + row);
+      }
+      last_load = i;
+    }
+  } else if (warp == kMmaWarp && n) {
+    // ---------------------------------------------- MMA issuer
+    if (lane == 0) {
+      auto full = [&](int i) {
+        const bool ok = mbar_wait(&kv_full[i % NS], (i / NS) & 1, abort_p, &g_attn_flags,
+                                  kAtFlagMma);
+        tc_fence_after();
+        return ok;
+      };
+      auto stage = [&](int i) { return ring + (i % NS) * G::kTile; };
+      auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
+        mma_xyt<D>(tmem + t * 128, smem + t * G::kTile, stage(2 * j));
+        umma_commit(&s_full[t]);
+      };
+      auto values = [&](int t, int j) {  // O_t += P_t V_j
+        // P becomes ready in two parts, 32 of each half's 64 keys
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          if (!mbar_wait(&p_full[t][part], j & 1, abort_p, &g_attn_flags, kAtFlagMma))
+            return false;
+          tc_fence_after();
+          mma_ay_steps<D, 64>(tmem + 256 + t * 128, tmem + t * 128, 64, stage(2 * j + 1), 2 * part,
+                              2, j > 0 || part > 0);
+        }
+        umma_commit(&o_full[t]);
+        return true;
+      };
+      bool ok = mbar_wait(&q_full, 0, abort_p, &g_attn_flags, kAtFlagMma) && full(0);
+      if (ok) {
+        mma_issued = true;
+        if (nt[0]) scores(0, 0);
+        if (nt[1]) scores(1, 0);
+        umma_commit(&kv_empty[0]);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const bool more = j + 1 < n;
+        ok = full(2 * j + 1);
+        if (ok && j < nt[0]) ok = values(0, j);
+        if (ok && more) ok = full(2 * j + 2);
+        if (ok && j + 1 < nt[0]) scores(0, j + 1);
+        if (ok && j < nt[1]) ok = values(1, j);
+        if (!ok) break;
+        umma_commit(&kv_empty[(2 * j + 1) % NS]);
+        if (j + 1 < nt[1]) scores(1, j + 1);
+        if (more) umma_commit(&kv_empty[(2 * j + 2) % NS]);
+      }
+    }
+  } else if (warp < kComputeWarps && work) {
+    // ---------------------------------------------- softmax: half a row per thread
+    // tile t, half of the 128 keys, and the TMEM lane quarter of the warp
+    const int t = warp >> 3, half = (warp >> 2) & 1, q4 = warp & 3, tid = q4 * 32 + lane;
+    const int row = r0 + t * kRows + tid;
+    const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t S_h = tmem + t * 128 + half * 64 + lanes;
+    const uint32_t O_h = tmem + 256 + t * 128 + half * (D / 2) + lanes;
+    const int pair = 1 + t * 4 + q4;  // barrier of the two warps that share the rows
+    const int limit = key_limit(P.S, x, row);
+    const uint64_t c2 = f32x2_pack(P.c, P.c);
+    float ref = 0.0f, l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < nt[t]; ++j) {
+      // both warps of a row leave together: their barriers must match
+      ok = pair_all(pair, mbar_wait(&s_full[t], j & 1, abort_p, &g_attn_flags, kAtFlagCompute));
+      if (!ok) break;
+      tc_fence_after();
+      const int lim = limit - j * kRows - half * 64;
+      const bool mask = __any_sync(0xffffffffu, lim < 64);
+      // 32 columns at a time, read once for the maximum and once more for the
+      // probabilities: holding all 64 spilled registers
+      auto scores = [&](int b, uint32_t* s) {
+        load_quarter(S_h + 32 * b, s);
+        if (!mask) return;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (32 * b + e >= lim) s[e] = 0xff800000u;  // -inf
+      };
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t s[32];
+        scores(b, s);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          m4[(e >> 1) & 3] = max_nan(max_nan(m4[(e >> 1) & 3], __uint_as_float(s[e])),
+                                     __uint_as_float(s[e + 1]));
+      }
+      // (a row behind the sequence holds another's values and has no say)
+      const float mt = row < x.lq ? max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3])) * P.c
+                                  : -INFINITY;
+      // a NaN or an infinite score: the polynomial would not keep it
+      const bool odd = __any_sync(0xffffffffu, !(mt < INFINITY));
+      // The reference of a row's exponentials moves only when a score passes
+      // it by 2^8 (fp32 sums and bf16 probabilities lose nothing at that
+      // size); then O and the sum are scaled to the new one.
+      if (pair_any(pair, j == 0 || mt > ref + 8.0f)) {
+        row_x[half][t][tid] = mt;
+        pair_sync(pair);
+        const float m = fmaxf(mt, row_x[half ^ 1][t][tid]);
+        if (j == 0) {
+          ref = m == -INFINITY ? 0.0f : m;  // a row without a key: all 0
+        } else {
+          ok = pair_all(pair, mbar_wait(&o_full[t], (j - 1) & 1, abort_p, &g_attn_flags,
+                                        kAtFlagCompute));
+          if (!ok) break;
+          tc_fence_after();
+          const float next = fmaxf(ref, m), f = ex2(ref - next);
+          ref = next;
+          l *= f;
+          const uint64_t f2 = f32x2_pack(f, f);
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b) {
+            uint32_t o[32];
+            tmem_ld32_at(O_h + 32 * b, o);
+            tmem_wait_ld();
+            tie32(o);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float lo, hi;
+              f32x2_unpack(f32x2_mul_rn(f32x2_pack_bits(o[e], o[e + 1]), f2), lo, hi);
+              o[e] = __float_as_uint(lo);
+              o[e + 1] = __float_as_uint(hi);
+            }
+            tmem_st32(O_h + 32 * b, o);
+          }
+        }
+      }
+      const uint64_t r2 = f32x2_pack(-ref, -ref);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t s[32], p[16];
+        scores(b, s);
+        auto probs = [&](auto poly) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t y =
+                f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, r2);
+            const uint64_t pr = decltype(poly)::value && e % kPolyOf < kPolyPart
+                                    ? ex2_pair<true>(y)
+                                    : ex2_pair<false>(y);
+            sum[e & 1] = f32x2_add_rn(sum[e & 1], pr);
+            p[e] = f32x2_to_bf16x2(pr);
+          }
+        };
+        if (odd)
+          probs(std::false_type());
+        else
+          probs(std::true_type());
+        tmem_st16(S_h + 16 * b, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t][b]);
+      }
+      float a0, a1;
+      f32x2_unpack(f32x2_add_rn(sum[0], sum[1]), a0, a1);
+      l += a0 + a1;
+    }
+    if (ok && nt[t])
+      ok = pair_all(pair, mbar_wait(&o_full[t], (nt[t] - 1) & 1, abort_p, &g_attn_flags,
+                                    kAtFlagCompute));
+    if (ok) {
+      tc_fence_after();
+      row_x[half][t][tid] = l;
+      pair_sync(pair);
+      l = row_x[0][t][tid] + row_x[1][t][tid];
+      const bool some = limit > 0;
+      const float inv = some ? 1.0f / l : 0.0f;
+      uint16_t* dst = P.out + (x.q0 + row) * P.os + h * D + half * (D / 2);
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) {
+        uint32_t o[32];
+        if (nt[t]) {
+          tmem_ld32_at(O_h + 32 * b, o);
+          tmem_wait_ld();
+          tie32(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (row < x.lq) store_row32(dst + 32 * b, o, inv);
+      }
+      if (row < x.lq && half == 0)
+        P.lse[static_cast<int64_t>(h) * P.S.Tq + x.q0 + row] =
+            some ? (ref + log2f(l)) / kLog2e : -INFINITY;
+    }
+  }
+
+  __syncthreads();  // every thread sees the final abort word
+  if (*abort_p && warp == kLoadWarp && lane == 0) {
+    // drain what this CTA started before its shared memory and TMEM go away
+    volatile int never = 0;
+    if (q_loaded) mbar_wait(&q_full, 0, &never, &g_attn_flags, kAtFlagDrain);
+    for (int i = max(0, last_load - NS + 1); i <= last_load; ++i)
+      if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+  }
+  if (*abort_p && warp == kMmaWarp && lane == 0 && mma_issued) {
+    volatile int never = 0;
+    umma_commit(&drain);
+    mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- backward
+
+struct BwdTc {
+  CUtensorMap mq, mk, mv, mdo;  // boxes of 128 rows (mk, mv in the dQ kernel: of kStep)
+  const uint16_t *q, *o, *dout;
+  const float* lse;
+  float* D;     // [H, Tq]: written by the dQ kernel, read by the dK/dV kernel
+  float* part;  // [splits][2][Tk][KV][d] partial dK, dV (splits > 1)
+  uint16_t *dq, *dk, *dv;
+  int64_t qs, os, dos, dqs, dks, dvs;
+  PackedSeqs S;
+  int H, KV, splits;
+  float scale, c;  // c = scale * log2(e)
+};
+
+// Two rings: the tiles that the last product of a step reads (K, or Q) are
+// held longest and get one stage more than the others (V, or dO).
+template <int D>
+struct BwdGeo {
+  static constexpr int kTile = tile_bytes<D>();
+  static constexpr int kA = D == 128 ? 3 : 5, kB = D == 128 ? 2 : 4;
+  static constexpr int kSmem = (2 + kA + kB) * kTile;
+};
+
+__device__ __forceinline__ void bar_compute() {  // the computing threads
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
+}
+
+// dQ of 128 query rows of one head, the keys 64 at a time: S = Q K^T,
+// dP = dO V^T, dS = P (dP - D) as bf16 over its dP, dQ += dS K.  Q and dO,
+// which every step reads, stay in TMEM as left operands, so that no product
+// reads more than 16 KiB of shared memory per step (with both operands there
+// the 128 x 128 x 16 products took 86 to 116 cycles instead of 64).  TMEM:
+// Q, dO (D / 2 columns each), dQ (D), two buffers of S and dP (64 columns
+// each); warps 0..7 take the even steps, 8..15 the odd ones.  The kernel also
+// writes D = dO . O for the dK/dV kernel.
+constexpr int kStep = 64;  // keys of a step
+
+template <int D>
+struct DqGeo {
+  static constexpr int kTile = kStep * D * 2;
+  static constexpr int kStages = D == 128 ? 6 : 8;  // of K and of V
+  static constexpr int kSmem = 2 * kStages * kTile;
+  static constexpr uint32_t kQ = 0, kDo = D / 2, kDq = D, kS = 256, kDp = 384;  // TMEM columns
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_constant__ BwdTc P) {
+  using G = DqGeo<D>;
+  constexpr int NS = G::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t q_ready, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], aux, s_full[2],
+      dp_full[2], ds_full[2], done, drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ float dsum[4][kRows];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&q_ready, kComputeWarps);
+    mbar_init(&aux, 1);
+    mbar_init(&drain, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&dp_full[b], 1);
+      mbar_init(&ds_full[b], kComputeWarps / 2);
+    }
+    mbar_init(&done, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort_p = &abort_flag;
+  pdl_wait_then_release();
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need the alignment asked for
+    if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    return;
+  }
+
+  PackedTile x = {};
+  const int h = blockIdx.x % P.H, kh = h / (P.H / P.KV);
+  const bool work = find_tile(P.S, false, blockIdx.x / P.H, kRows, x);
+  const int r0 = x.t * kRows;
+  const int n = work ? (key_limit(P.S, x, min(r0 + kRows, x.lq) - 1) + kStep - 1) / kStep : 0;
+  int last_k = -1, last_v = -1;
+  bool mma_issued = false;
+  uint8_t* ring_v = smem + NS * G::kTile;
+
+  if (warp == kLoadWarp && n) {
+    for (int i = 0; i < n; ++i) {
+      const int s = i % NS, row = i * kStep;
+      if (i >= NS && !warp_wait(&k_empty[s], (i / NS) - 1, abort_p, kAtFlagLoad)) break;
+      const bool tail = row + kStep > x.lk;  // dS is 0 there; K must be finite
+      uint64_t* bar = tail ? &aux : &k_full[s];
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, G::kTile);
+        tma_tile<D, kStep>(smem + s * G::kTile, &P.mk, bar, kh * D, x.k0 + row);
+      }
+      if (tail) {
+        __syncwarp();
+        if (!tail_landed(&aux, 0, abort_p)) break;
+        zero_rows<D, kStep>(smem + s * G::kTile, x.lk - row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[s]);
+      }
+      last_k = i;
+      if (i >= NS && !warp_wait(&v_empty[s], (i / NS) - 1, abort_p, kAtFlagLoad)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&v_full[s], G::kTile);
+        tma_tile<D, kStep>(ring_v + s * G::kTile, &P.mv, &v_full[s], kh * D, x.k0 + row);
+      }
+      last_v = i;
+    }
+  } else if (warp == kMmaWarp && n) {
+    if (lane == 0) {
+      auto wait = [&](uint64_t* b, int phase) {
+        const bool ok = mbar_wait(b, phase & 1, abort_p, &g_attn_flags, kAtFlagMma);
+        tc_fence_after();
+        return ok;
+      };
+      auto scores = [&](int i) {  // S and dP of step i into their buffer
+        const uint32_t b = (i & 1) * kStep;
+        if (!wait(&k_full[i % NS], i / NS)) return false;
+        mma_issued = true;
+        mma_txyt<D, kStep>(tmem + G::kS + b, tmem + G::kQ, smem + (i % NS) * G::kTile);
+        umma_commit(&s_full[i & 1]);
+        if (!wait(&v_full[i % NS], i / NS)) return false;
+        mma_txyt<D, kStep>(tmem + G::kDp + b, tmem + G::kDo, ring_v + (i % NS) * G::kTile);
+        umma_commit(&dp_full[i & 1]);
+        umma_commit(&v_empty[i % NS]);
+        return true;
+      };
+      bool ok = wait(&q_ready, 0) && scores(0) && (n < 2 || scores(1));
+      for (int i = 0; i < n && ok; ++i) {
+        ok = wait(&ds_full[i & 1], i >> 1);
+        if (!ok) break;
+        // dQ += dS K: 16 keys in the first 8 of every 16 columns of the buffer
+        mma_tay<D, kStep>(tmem + G::kDq, tmem + G::kDp + (i & 1) * kStep, 16, smem + (i % NS) * G::kTile,
+                          i > 0);
+        umma_commit(&k_empty[i % NS]);
+        if (i + 2 < n) ok = scores(i + 2);
+      }
+      if (ok) umma_commit(&done);
+    }
+  } else if (warp < kComputeWarps && work) {
+    const int part = warp >> 2, q4 = warp & 3, tid = q4 * 32 + lane, row = r0 + tid;
+    const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
+    const bool in = row < x.lq;
+    const int64_t at = static_cast<int64_t>(h) * P.S.Tq + x.q0 + row;
+    {  // this quarter of the row: Q and dO into TMEM, dO . O
+      constexpr int W = D / 8;  // 32-bit words
+      uint32_t qw[W], gw[W];
+      float sum = 0.0f;
+      const int64_t tok = x.q0 + row;
+      const uint4* qp = reinterpret_cast<const uint4*>(P.q + tok * P.qs + h * D + part * (D / 4));
+      const uint4* gp =
+          reinterpret_cast<const uint4*>(P.dout + tok * P.dos + h * D + part * (D / 4));
+      const uint4* op = reinterpret_cast<const uint4*>(P.o + tok * P.os + h * D + part * (D / 4));
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        uint4 a = make_uint4(0, 0, 0, 0), b = a, c = a;
+        if (in) a = qp[i], b = gp[i], c = op[i];
+        qw[4 * i] = a.x, qw[4 * i + 1] = a.y, qw[4 * i + 2] = a.z, qw[4 * i + 3] = a.w;
+        gw[4 * i] = b.x, gw[4 * i + 1] = b.y, gw[4 * i + 2] = b.z, gw[4 * i + 3] = b.w;
+        const uint32_t ow[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t u = gw[4 * i + e], v = ow[e];
+          sum = __fmaf_rn(__uint_as_float(u << 16), __uint_as_float(v << 16), sum);
+          sum = __fmaf_rn(__uint_as_float(u & 0xFFFF0000u), __uint_as_float(v & 0xFFFF0000u), sum);
+        }
+      }
+      if constexpr (W == 16) {
+        tmem_st16(tmem + G::kQ + part * W + lanes, qw);
+        tmem_st16(tmem + G::kDo + part * W + lanes, gw);
+      } else {
+        tmem_st8(tmem + G::kQ + part * W + lanes, qw);
+        tmem_st8(tmem + G::kDo + part * W + lanes, gw);
+      }
+      dsum[part][tid] = sum;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_ready);
+    }
+    bar_compute();
+    const float Dr = (dsum[0][tid] + dsum[1][tid]) + (dsum[2][tid] + dsum[3][tid]);
+    if (in && part == 0) P.D[at] = Dr;
+    const float lse2 = in ? P.lse[at] * kLog2e : 0.0f;
+    const int limit = in ? key_limit(P.S, x, row) : 0;
+    const uint64_t c2 = f32x2_pack(P.c, P.c), l2 = f32x2_pack(-lse2, -lse2),
+                   d2 = f32x2_pack(-Dr, -Dr);
+    const int buf = part >> 1;  // the buffer, and so the steps, of this warp
+    const uint32_t S_p = tmem + G::kS + part * 32 + lanes, dP_p = tmem + G::kDp + part * 32 + lanes;
+    bool ok = true;
+    for (int i = buf; i < n; i += 2) {
+      const int lim = limit - i * kStep - (part & 1) * 32;
+      ok = warp_wait(&s_full[buf], i >> 1, abort_p, kAtFlagCompute);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[32];
+      load_quarter(S_p, s);
+      uint64_t p[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        p[e] = ex2_pair<false>(f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, l2));
+      ok = warp_wait(&dp_full[buf], i >> 1, abort_p, kAtFlagCompute);
+      if (!ok) break;
+      tc_fence_after();
+      load_quarter(dP_p, s);
+      uint32_t ds[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        ds[e] = f32x2_to_bf16x2(f32x2_mul_rn(
+            p[e], f32x2_add_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), d2)));
+      if (__any_sync(0xffffffffu, lim < 32)) {  // select: what is masked may be infinite or NaN
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          ds[e] &= (2 * e < lim ? 0x0000FFFFu : 0u) | (2 * e + 1 < lim ? 0xFFFF0000u : 0u);
+      }
+      // 16 keys (8 columns) at the start of each 16 columns of the buffer
+      tmem_st8(dP_p, ds);
+      tmem_st8(dP_p + 16, ds + 8);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full[buf]);
+    }
+    if (ok && n) ok = warp_wait(&done, 0, abort_p, kAtFlagCompute);
+    if (ok && part * 32 < D) {
+      tc_fence_after();
+      uint16_t* dst = P.dq + (x.q0 + row) * P.dqs + h * D + part * 32;
+      uint32_t o[32];
+      if (n) {
+        load_quarter(tmem + G::kDq + part * 32 + lanes, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+      }
+      if (in) store_row32(dst, o, P.scale);
+    }
+  }
+
+  __syncthreads();
+  if (*abort_p && warp == kLoadWarp && lane == 0) {
+    volatile int never = 0;
+    for (int i = max(0, last_k - NS + 1); i <= last_k; ++i)
+      if (!mbar_wait(&k_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+    for (int i = max(0, last_v - NS + 1); i <= last_v; ++i)
+      if (!mbar_wait(&v_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+  }
+  if (*abort_p && warp == kMmaWarp && lane == 0 && mma_issued) {
+    volatile int never = 0;
+    umma_commit(&drain);
+    mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dK, dV of 128 keys of one KV head, over one share of the group's query
+// heads and, in each, the query tiles that see the keys, in order.  The
+// scores are computed transposed (a thread owns a key row, 64 of the tile's
+// 128 queries), so that P^T and dS^T, written as bf16 over the scores they
+// came from, are the tensor-memory operands of dV += P^T dO and dK += dS^T Q.
+// TMEM: S^T, dP^T (128 columns each), dV, dK (D each).  While the threads
+// compute P^T the tensor cores run the tile before's dK product and this
+// tile's dP^T; while they compute dS^T, dV and the next S^T.
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_constant__ BwdTc P) {
+  using G = BwdGeo<D>;
+  constexpr int NA = G::kA, NB = G::kB;  // Q, dO
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t kv_full, q_full[NA], ld_full[2], q_empty[NA], do_full[NB], do_empty[NB], aux,
+      s_full, dp_full, p_full[2], ds_full, done, drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ __align__(16) float nlse[2][kRows], nD[2][kRows];  // -lse log2(e), -D
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&kv_full, 1);
+    mbar_init(&aux, 1);
+    mbar_init(&drain, 1);
+    for (int i = 0; i < NA; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&ld_full[i], 32);
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&do_full[i], 1);
+      mbar_init(&do_empty[i], 1);
+    }
+    mbar_init(&s_full, 1);
+    mbar_init(&dp_full, 1);
+    mbar_init(&done, 1);
+    mbar_init(&p_full[0], kComputeWarps);
+    mbar_init(&p_full[1], kComputeWarps);
+    mbar_init(&ds_full, kComputeWarps);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort_p = &abort_flag;
+  pdl_wait_then_release();
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need the alignment asked for
+    if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    return;
+  }
+
+  PackedTile x = {};
+  const int per = P.KV * P.splits, share = blockIdx.x % per;
+  const int kh = share / P.splits, split = share % P.splits;
+  const bool work = find_tile(P.S, true, blockIdx.x / per, kRows, x);
+  const int grp = P.H / P.KV;
+  const int h0 = kh * grp + grp * split / P.splits, h1 = kh * grp + grp * (split + 1) / P.splits;
+  const int c0 = x.t * kRows;
+  int qt0 = 0, per_head = 0;
+  if (work) {
+    // the first query that sees the tile's first key, and so the first tile
+    const int first = P.S.causal ? max(c0 - (x.lk - x.lq), 0) : 0;
+    qt0 = first / kRows;
+    per_head = max((x.lq + kRows - 1) / kRows - qt0, 0);
+  }
+  const int n = per_head * (h1 - h0);
+  int last_a = -1, last_b = -1;
+  bool kv_loaded = false, mma_issued = false;
+  uint8_t* ring = smem + 2 * G::kTile;
+
+  if (warp == kLoadWarp && n) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&kv_full, 2 * G::kTile);
+      tma_tile<D>(smem, &P.mk, &kv_full, kh * D, x.k0 + c0);
+      tma_tile<D>(smem + G::kTile, &P.mv, &kv_full, kh * D, x.k0 + c0);
+    }
+    kv_loaded = true;
+    int h = h0, qt = qt0, tails = 0;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % NA, v = i % NB, row = qt * kRows;
+      const bool tail = row + kRows > x.lq;  // P, dS are 0 there; Q, dO must be finite
+      auto load = [&](uint8_t* st, const CUtensorMap* map, uint64_t* full) {
+        uint64_t* bar = tail ? &aux : full;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, G::kTile);
+          tma_tile<D>(st, map, bar, h * D, x.q0 + row);
+        }
+      };
+      auto patch = [&](uint8_t* st, uint64_t* full) {
+        if (!tail) return true;
+        __syncwarp();
+        if (!tail_landed(&aux, tails & 1, abort_p)) return false;
+        ++tails;
+        zero_rows<D>(st, x.lq - row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+        return true;
+      };
+      if (i >= NA && !warp_wait(&q_empty[s], (i / NA) - 1, abort_p, kAtFlagLoad)) break;
+      load(ring + s * G::kTile, &P.mq, &q_full[s]);
+      float a[4], b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = lane + 32 * e;
+        const int64_t at = static_cast<int64_t>(h) * P.S.Tq + x.q0 + row + j;
+        a[e] = row + j < x.lq ? P.lse[at] * -kLog2e : 0.0f;
+        b[e] = row + j < x.lq ? -P.D[at] : 0.0f;
+      }
+      // their slot was last read for tile i - 2, before its dK product
+      if (i >= 2 && !warp_wait(&q_empty[(i - 2) % NA], (i - 2) / NA, abort_p, kAtFlagLoad)) {
+        last_a = i;
+        break;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        nlse[i & 1][lane + 32 * e] = a[e];
+        nD[i & 1][lane + 32 * e] = b[e];
+      }
+      mbar_arrive(&ld_full[i & 1]);
+      if (!patch(ring + s * G::kTile, &q_full[s])) break;
+      last_a = i;
+      if (i >= NB && !warp_wait(&do_empty[v], (i / NB) - 1, abort_p, kAtFlagLoad)) break;
+      load(ring + (NA + v) * G::kTile, &P.mdo, &do_full[v]);
+      if (!patch(ring + (NA + v) * G::kTile, &do_full[v])) break;
+      last_b = i;
+      if (++qt == qt0 + per_head) {
+        qt = qt0;
+        ++h;
+      }
+    }
+  } else if (warp == kMmaWarp && n) {
+    if (lane == 0) {
+      auto wait = [&](uint64_t* b, int phase) {
+        const bool ok = mbar_wait(b, phase & 1, abort_p, &g_attn_flags, kAtFlagMma);
+        tc_fence_after();
+        return ok;
+      };
+      auto Q = [&](int i) { return ring + (i % NA) * G::kTile; };
+      auto dO = [&](int i) { return ring + (NA + i % NB) * G::kTile; };
+      auto scores = [&](int i) {  // S^T = K Q^T
+        if (!wait(&q_full[i % NA], i / NA)) return false;
+        mma_issued = true;
+        mma_xyt<D>(tmem, smem, Q(i));
+        umma_commit(&s_full);
+        return true;
+      };
+      auto dprobs = [&](int i) {  // dP^T = V dO^T
+        if (!wait(&do_full[i % NB], i / NB)) return false;
+        mma_xyt<D>(tmem + 128, smem + G::kTile, dO(i));
+        umma_commit(&dp_full);
+        return true;
+      };
+      bool ok = wait(&kv_full, 0) && scores(0) && dprobs(0);
+      for (int i = 0; i < n && ok; ++i) {
+        const bool more = i + 1 < n;
+        // dV += P^T dO; P^T becomes ready in two parts, 16 of each 32 queries
+#pragma unroll
+        for (int c = 0; c < 2 && ok; ++c) {
+          ok = wait(&p_full[c], i);
+          if (ok) mma_ay_steps<D, 32>(tmem + 256, tmem, 32, dO(i), c, 1, i > 0 || c > 0);
+        }
+        if (!ok) break;
+        umma_commit(&do_empty[i % NB]);
+        ok = (!more || scores(i + 1)) && wait(&ds_full, i);
+        if (!ok) break;
+        mma_ay<D, 32>(tmem + 256 + D, tmem + 128, 32, Q(i), i > 0);  // dK += dS^T Q
+        umma_commit(&q_empty[i % NA]);
+        if (more) ok = dprobs(i + 1);
+      }
+      if (ok) umma_commit(&done);
+    }
+  } else if (warp < kComputeWarps && work) {
+    const int part = warp >> 2, q4 = warp & 3, key = c0 + q4 * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t S_p = tmem + part * 32 + lanes, dP_p = S_p + 128;
+    const bool in = key < x.lk;
+    // query rows of the sequence that see this key: [first, lq)
+    const int first = in ? (P.S.causal ? max(key - (x.lk - x.lq), 0) : 0) : x.lq;
+    const uint64_t c2 = f32x2_pack(P.c, P.c);
+    bool ok = true;
+    int qt = qt0;
+    for (int i = 0; i < n; ++i) {
+      const int s = i & 1;
+      // bit b of keep: query b of this thread's 32 sees the key
+      const int lo = first - qt * kRows - part * 32, hi = x.lq - qt * kRows - part * 32;
+      const uint32_t keep = (hi >= 32 ? ~0u : hi > 0 ? (1u << hi) - 1 : 0u) &
+                            (lo <= 0 ? ~0u : lo < 32 ? ~0u << lo : 0u);
+      const bool mask = __any_sync(0xffffffffu, keep != ~0u);
+      if (++qt == qt0 + per_head) qt = qt0;
+      ok = warp_wait(&ld_full[s], i >> 1, abort_p, kAtFlagCompute) &&
+           warp_wait(&s_full, i, abort_p, kAtFlagCompute);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t v[32];
+      load_quarter(S_p, v);
+      uint64_t p[16];
+      uint32_t w[16];
+      const ulonglong2* ls = reinterpret_cast<const ulonglong2*>(nlse[s] + part * 32);
+      auto drop = [&](int from, int to) {  // select: what is masked may be infinite or NaN
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e >= from && e < to)
+            w[e] &= ((keep >> (2 * e)) & 1 ? 0x0000FFFFu : 0u) |
+                    ((keep >> (2 * e)) & 2 ? 0xFFFF0000u : 0u);
+      };
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int e = 8 * c; e < 8 * c + 8; e += 2) {
+          const ulonglong2 l4 = ls[e / 2];
+          const uint64_t y0 = f32x2_fma_rn(f32x2_pack_bits(v[2 * e], v[2 * e + 1]), c2, l4.x);
+          const uint64_t y1 = f32x2_fma_rn(f32x2_pack_bits(v[2 * e + 2], v[2 * e + 3]), c2, l4.y);
+          p[e] = e % kPolyOf < kPolyPart ? ex2_pair<true>(y0) : ex2_pair<false>(y0);
+          p[e + 1] = (e + 1) % kPolyOf < kPolyPart ? ex2_pair<true>(y1) : ex2_pair<false>(y1);
+          w[e] = f32x2_to_bf16x2(p[e]);
+          w[e + 1] = f32x2_to_bf16x2(p[e + 1]);
+        }
+        if (mask) drop(8 * c, 8 * c + 8);
+        tmem_st8(S_p + 8 * c, w + 8 * c);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[c]);
+      }
+      ok = warp_wait(&dp_full, i, abort_p, kAtFlagCompute);
+      if (!ok) break;
+      tc_fence_after();
+      load_quarter(dP_p, v);
+      const ulonglong2* ds = reinterpret_cast<const ulonglong2*>(nD[s] + part * 32);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const ulonglong2 d4 = ds[e];
+        w[2 * e] = f32x2_to_bf16x2(f32x2_mul_rn(
+            p[2 * e], f32x2_add_rn(f32x2_pack_bits(v[4 * e], v[4 * e + 1]), d4.x)));
+        w[2 * e + 1] = f32x2_to_bf16x2(f32x2_mul_rn(
+            p[2 * e + 1], f32x2_add_rn(f32x2_pack_bits(v[4 * e + 2], v[4 * e + 3]), d4.y)));
+      }
+      if (mask) drop(0, 16);
+      tmem_st16(dP_p, w);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full);
+    }
+    if (ok && n) ok = warp_wait(&done, 0, abort_p, kAtFlagCompute);
+    if (ok) {
+      tc_fence_after();
+      // eight warps write dV, eight dK, half of the columns each
+      const int which = part >> 1, col = (part & 1) * (D / 2);  // 1: dK
+      const uint32_t src = tmem + 256 + which * D + col + lanes;
+      const int64_t tok = x.k0 + key;
+      const int64_t one = static_cast<int64_t>(P.S.Tk) * P.KV * D;
+      float* part_to = P.part + (2 * split + 1 - which) * one + (tok * P.KV + kh) * D + col;
+      uint16_t* dst = (which ? P.dk + tok * P.dks : P.dv + tok * P.dvs) + kh * D + col;
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) {
+        uint32_t o[32];
+        if (n) {
+          load_quarter(src + 32 * b, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (!in) continue;
+        if (P.splits > 1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint4*>(part_to + 32 * b)[e] =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else {
+          store_row32(dst + 32 * b, o, which ? P.scale : 1.0f);
+        }
+      }
+    }
+  }
+
+  __syncthreads();
+  if (*abort_p && warp == kLoadWarp && lane == 0) {
+    volatile int never = 0;
+    if (kv_loaded) mbar_wait(&kv_full, 0, &never, &g_attn_flags, kAtFlagDrain);
+    for (int i = max(0, last_a - NA + 1); i <= last_a; ++i)
+      if (!mbar_wait(&q_full[i % NA], (i / NA) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+    for (int i = max(0, last_b - NB + 1); i <= last_b; ++i)
+      if (!mbar_wait(&do_full[i % NB], (i / NB) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+  }
+  if (*abort_p && warp == kMmaWarp && lane == 0 && mma_issued) {
+    volatile int never = 0;
+    umma_commit(&drain);
+    mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dK, dV of every token that belongs to a sequence (those between the first
+// length and the last), the shares added in order: eight elements a thread
+template <int D>
+__global__ void __launch_bounds__(256) packed_kv_reduce(const __grid_constant__ BwdTc P) {
+  pdl_wait_then_release();
+  const int t0 = min(max(__ldg(P.S.cu_k), 0), P.S.Tk);
+  const int t1 = min(__ldg(P.S.cu_k + P.S.n_seq), P.S.Tk);
+  const int row8 = P.KV * (D / 8);
+  const int64_t one = static_cast<int64_t>(P.S.Tk) * P.KV * D;
+  const int64_t items = static_cast<int64_t>(max(t1 - t0, 0)) * row8;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < items;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t tok = t0 + i / row8;
+    const int e = static_cast<int>(i % row8) * 8;  // element of the token's KV * D
+    const float* p = P.part + tok * P.KV * D + e;
+    float a[8] = {}, b[8] = {};
+    for (int s = 0; s < P.splits; ++s) {
+      const float4* y = reinterpret_cast<const float4*>(p + 2 * s * one);
+      const float4* z = reinterpret_cast<const float4*>(p + (2 * s + 1) * one);
+      const float4 y0 = y[0], y1 = y[1], z0 = z[0], z1 = z[1];
+      a[0] += y0.x, a[1] += y0.y, a[2] += y0.z, a[3] += y0.w;
+      a[4] += y1.x, a[5] += y1.y, a[6] += y1.z, a[7] += y1.w;
+      b[0] += z0.x, b[1] += z0.y, b[2] += z0.z, b[3] += z0.w;
+      b[4] += z1.x, b[5] += z1.y, b[6] += z1.z, b[7] += z1.w;
+    }
+    uint32_t u[4], v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u[j] = f32x2_to_bf16x2(f32x2_pack(a[2 * j] * P.scale, a[2 * j + 1] * P.scale));
+      v[j] = f32x2_to_bf16x2(f32x2_pack(b[2 * j], b[2 * j + 1]));
+    }
+    *reinterpret_cast<uint4*>(P.dk + tok * P.dks + e) = make_uint4(u[0], u[1], u[2], u[3]);
+    *reinterpret_cast<uint4*>(P.dv + tok * P.dvs + e) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// Raise a kernel's dynamic shared memory limit, once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+bool map_rows(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t stride,
+              int box = kRows) {
+  return encode_tma_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, cols, rows, stride * 2, 64, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int64_t most_tiles(int64_t T, int n_seq, int rows) { return T / rows + std::min<int64_t>(n_seq, T); }
+
+template <int D>
+cudaError_t fwd_tc(const hsnf4_packed_attention& a, void* o, int64_t o_stride, float* lse,
+                   cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  FwdTc P;
+  memset(&P, 0, sizeof P);
+  const int64_t wq = static_cast<int64_t>(a.H) * D, wk = static_cast<int64_t>(a.KV) * D;
+  if (!map_rows(&P.mq, a.q, wq, a.Tq, a.q_stride) || !map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride) ||
+      !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride))
+    return cudaErrorInvalidValue;
+  P.out = static_cast<uint16_t*>(o);
+  P.os = o_stride;
+  P.lse = lse;
+  P.S = {a.cu_q, a.cu_k, static_cast<int>(a.Tq), static_cast<int>(a.Tk), a.n_seq, a.causal};
+  P.H = a.H;
+  P.KV = a.KV;
+  P.c = a.scale * kLog2e;
+  const cudaError_t e = allow_smem(packed_fwd_tc<D>, FwdGeo<D>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = most_tiles(a.Tq, a.n_seq, 2 * kRows) * a.H;
+  return launch_pdl(packed_fwd_tc<D>, dim3(static_cast<unsigned>(grid)), dim3(kTcThreads),
+                    FwdGeo<D>::kSmem, st, P);
+}
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+// shares of a KV group's query heads, so that there are CTAs for every SM
+int head_splits(int64_t Tk, int H, int KV) {
+  const int64_t tiles = (Tk + kRows - 1) / kRows * KV;
+  const int64_t want = (sm_count() + tiles - 1) / tiles;
+  return static_cast<int>(std::min<int64_t>(H / KV, std::max<int64_t>(want, 1)));
+}
+
+template <int D>
+cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws,
+                   cudaStream_t st) {
+  static std::atomic<uint64_t> done_q{0}, done_kv{0};
+  BwdTc P;
+  memset(&P, 0, sizeof P);
+  const int64_t wq = static_cast<int64_t>(a.H) * D, wk = static_cast<int64_t>(a.KV) * D;
+  if (!map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride, kStep) ||
+      !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride, kStep) ||
+      !map_rows(&P.mq, a.q, wq, a.Tq, a.q_stride) ||
+      !map_rows(&P.mdo, b.dout, wq, a.Tq, b.do_stride))
+    return cudaErrorInvalidValue;
+  P.q = static_cast<const uint16_t*>(a.q);
+  P.qs = a.q_stride;
+  P.o = static_cast<const uint16_t*>(b.o);
+  P.dout = static_cast<const uint16_t*>(b.dout);
+  P.lse = b.lse;
+  P.D = static_cast<float*>(ws);
+  P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                    round_up(static_cast<size_t>(a.H) * a.Tq * 4, 256));
+  P.dq = static_cast<uint16_t*>(b.dq);
+  P.dk = static_cast<uint16_t*>(b.dk);
+  P.dv = static_cast<uint16_t*>(b.dv);
+  P.os = b.o_stride;
+  P.dos = b.do_stride;
+  P.dqs = b.dq_stride;
+  P.dks = b.dk_stride;
+  P.dvs = b.dv_stride;
+  P.S = {a.cu_q, a.cu_k, static_cast<int>(a.Tq), static_cast<int>(a.Tk), a.n_seq, a.causal};
+  P.H = a.H;
+  P.KV = a.KV;
+  P.splits = head_splits(a.Tk, a.H, a.KV);
+  P.scale = a.scale;
+  P.c = a.scale * kLog2e;
+  cudaError_t e = allow_smem(packed_dq_tc<D>, DqGeo<D>::kSmem, done_q);
+  if (e == cudaSuccess) e = allow_smem(packed_dkdv_tc<D>, BwdGeo<D>::kSmem, done_kv);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(packed_dq_tc<D>,
+                 dim3(static_cast<unsigned>(most_tiles(a.Tq, a.n_seq, kRows) * a.H)),
+                 dim3(kTcThreads), DqGeo<D>::kSmem, st, P);
+  if (e != cudaSuccess) return e;
+  if (!map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride) || !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride))
+    return cudaErrorInvalidValue;
+  e = launch_pdl(packed_dkdv_tc<D>, dim3(static_cast<unsigned>(most_tiles(a.Tk, a.n_seq, kRows) *
+                                                               a.KV * P.splits)),
+                 dim3(kTcThreads), BwdGeo<D>::kSmem, st, P);
+  if (e != cudaSuccess || P.splits == 1) return e;
+  const int64_t items = a.Tk * a.KV * (D / 8);
+  const int64_t grid = std::min<int64_t>((items + 255) / 256, static_cast<int64_t>(sm_count()) * 8);
+  return launch_pdl(packed_kv_reduce<D>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, P);
+}
+
+}  // namespace
+
+// D [H, Tq] fp32, then the shares' fp32 dK, dV
+size_t packed_tc_workspace_bytes(int64_t Tq, int64_t Tk, int n_seq, int H, int KV, int d) {
+  const int splits = head_splits(Tk, H, KV);
+  size_t n = round_up(static_cast<size_t>(H) * Tq * 4, 256);
+  if (splits > 1) n += static_cast<size_t>(splits) * 2 * Tk * KV * d * 4;
+  return n;
+}
+
+cudaError_t launch_packed_bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws,
+                                 cudaStream_t st) {
+  return a.head_dim == 128 ? bwd_tc<128>(a, b, ws, st) : bwd_tc<64>(a, b, ws, st);
+}
+
+cudaError_t launch_packed_fwd_tc(const hsnf4_packed_attention& a, void* o, int64_t o_stride,
+                                 float* lse, cudaStream_t st) {
+  return a.head_dim == 128 ? fwd_tc<128>(a, o, o_stride, lse, st)
+                           : fwd_tc<64>(a, o, o_stride, lse, st);
+}
+
+cudaError_t read_attn_flags(uint32_t* flags) {
+  unsigned int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_attn_flags, sizeof v);
+  if (e != cudaSuccess) return e;
+  *flags = v;
+  if (v) {
+    const unsigned int z = 0;
+    e = cudaMemcpyToSymbol(g_attn_flags, &z, sizeof z);
+  }
+  return e;
+}
+
+}  // namespace hsnf4

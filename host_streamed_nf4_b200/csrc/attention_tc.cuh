@@ -1,0 +1,170 @@
+// attention_tc.cuh -- pieces of the tcgen05 attention kernels: 128-row
+// operand tiles in 128B-swizzled shared memory, the products between them,
+// and the barrier waits.
+//
+// A tile holds 128 tokens x D bf16 of one head as D / 64 boxes of 64 columns
+// ([128 rows][128 bytes] each, 16 KiB).  One tile serves as a K-major
+// operand (contraction over the head's columns: 16 columns are 32 bytes on)
+// and as an MN-major one (contraction over the tokens: 16 tokens are 2 KiB
+// on, 64-column atoms a box apart).
+#pragma once
+
+#include "ptx.cuh"
+
+namespace hsnf4 {
+
+constexpr int kRows = 128;         // tokens of a tile
+constexpr int kBoxBytes = 16384;   // 128 rows x 64 columns of bf16
+
+template <int D>
+constexpr int tile_bytes() {
+  return D / 64 * kBoxBytes;
+}
+
+// N: the tile's tokens, and the rows of a box of `map`
+template <int D, int N = kRows>
+__device__ __forceinline__ void tma_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
+                                         int col, int row) {
+#pragma unroll
+  for (int b = 0; b < D / 64; ++b) tma_load_2d(dst + b * (N * 128), map, bar, col + 64 * b, row);
+}
+
+// Rows from `from` on of a tile become zeros (one warp; swizzling permutes
+// the 16-byte pieces inside a row only).
+template <int D, int N = kRows>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from) {
+  for (int i = threadIdx.x & 31; i < (N - from) * (D / 8); i += 32) {
+    const int row = from + i / (D / 8), c = i % (D / 8);
+    *reinterpret_cast<uint4*>(tile + (c / 8) * (N * 128) + row * 128 + (c % 8) * 16) =
+        make_uint4(0, 0, 0, 0);
+  }
+}
+
+// d[128 x 128] = X Y^T over the D columns of two tiles (one thread issues)
+template <int D>
+__device__ __forceinline__ void mma_xyt(uint32_t d, const uint8_t* X, const uint8_t* Y) {
+  const uint64_t x0 = make_sdesc(smem_u32(X), 16, 1024, kLayoutSw128);
+  const uint64_t y0 = make_sdesc(smem_u32(Y), 16, 1024, kLayoutSw128);
+  constexpr uint32_t idesc = make_idesc_bf16(kRows, kRows, 0, 0);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const uint64_t off = ((k / 4) * kBoxBytes + (k % 4) * 32) >> 4;
+    umma_bf16(d, x0 + off, y0 + off, idesc, k > 0 ? 1u : 0u);
+  }
+}
+
+// d[128 x D] (+)= A Y over the 128 tokens of tile Y; A is bf16 in tensor
+// memory, 16 tokens to 8 columns, in groups of GROUP tokens `stride` columns
+// apart.
+template <int D, int GROUP>
+__device__ __forceinline__ void mma_ay(uint32_t d, uint32_t a, uint32_t stride, const uint8_t* Y,
+                                       bool accumulate) {
+  const uint64_t y0 = make_sdesc(smem_u32(Y), kBoxBytes, 1024, kLayoutSw128);
+  constexpr uint32_t idesc = make_idesc_bf16(kRows, D, 0, 1);
+#pragma unroll
+  for (int k = 0; k < kRows / 16; ++k)
+    umma_bf16_ta(d, a + (k * 16 / GROUP) * stride + (k * 16 % GROUP) / 2,
+                 y0 + ((k * 2048) >> 4), idesc, accumulate || k > 0 ? 1u : 0u);
+}
+
+// d[128 x N] = X Y^T over the D columns of a head: X is bf16 in tensor memory
+// (16 columns of the head to 8 TMEM columns), Y a tile of N tokens in boxes of
+// N rows.
+template <int D, int N>
+__device__ __forceinline__ void mma_txyt(uint32_t d, uint32_t x, const uint8_t* Y) {
+  const uint64_t y0 = make_sdesc(smem_u32(Y), 16, 1024, kLayoutSw128);
+  constexpr uint32_t idesc = make_idesc_bf16(kRows, N, 0, 0);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k)
+    umma_bf16_ta(d, x + 8 * k, y0 + (((k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc,
+                 k > 0 ? 1u : 0u);
+}
+
+// d[128 x D] (+)= A Y over the N tokens of such a tile; A is bf16 in tensor
+// memory, 16 tokens to 8 columns, `stride` columns from one 16 to the next.
+template <int D, int N>
+__device__ __forceinline__ void mma_tay(uint32_t d, uint32_t a, uint32_t stride, const uint8_t* Y,
+                                        bool accumulate) {
+  const uint64_t y0 = make_sdesc(smem_u32(Y), N * 128, 1024, kLayoutSw128);
+  constexpr uint32_t idesc = make_idesc_bf16(kRows, D, 0, 1);
+#pragma unroll
+  for (int k = 0; k < N / 16; ++k)
+    umma_bf16_ta(d, a + k * stride, y0 + ((k * 2048) >> 4), idesc,
+                 accumulate || k > 0 ? 1u : 0u);
+}
+
+// Part of mma_ay: the 16-token steps `first`, `first` + 1 ... of every group
+// (count of them), for an A that becomes ready in parts.
+template <int D, int GROUP>
+__device__ __forceinline__ void mma_ay_steps(uint32_t d, uint32_t a, uint32_t stride,
+                                             const uint8_t* Y, int first, int count,
+                                             bool accumulate) {
+  const uint64_t y0 = make_sdesc(smem_u32(Y), kBoxBytes, 1024, kLayoutSw128);
+  constexpr uint32_t idesc = make_idesc_bf16(kRows, D, 0, 1);
+  bool acc = accumulate;
+#pragma unroll
+  for (int g = 0; g < kRows / GROUP; ++g)
+#pragma unroll
+    for (int c = 0; c < count; ++c) {
+      const int k = g * (GROUP / 16) + first + c;
+      umma_bf16_ta(d, a + g * stride + (first + c) * 8, y0 + ((k * 2048) >> 4), idesc,
+                   acc ? 1u : 0u);
+      acc = true;
+    }
+}
+
+// 2^x of two values at once on the fp32 pipe: x = n + f with n the nearest
+// integer (Cody and Waite's reduction), 2^f by a polynomial of degree 4 that
+// is 1 at f = 0 and minimises the relative error on [-1/2, 1/2] (2.9e-6 in
+// fp32; found by linear programming), n added to the exponent.  Below 2^-126
+// the result is 0.  The special-function unit gives 16 results per clock and
+// SM, half of what the tensor cores need beside it, so a share of the
+// exponentials goes this way.
+__device__ __forceinline__ uint64_t ex2_poly(uint64_t x) {
+  float a, b;
+  f32x2_unpack(x, a, b);
+  const uint64_t y = f32x2_pack(fmaxf(a, -127.0f), fmaxf(b, -127.0f));
+  const float magic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
+  const uint64_t t = f32x2_add_rn(y, f32x2_pack(magic, magic));
+  const uint64_t n = f32x2_add_rn(t, f32x2_pack(-magic, -magic));
+  const uint64_t f = f32x2_fma_rn(n, f32x2_pack(-1.0f, -1.0f), y);
+  uint64_t p = f32x2_fma_rn(f32x2_pack(0.009582576341927052f, 0.009582576341927052f), f,
+                            f32x2_pack(0.05590682849287987f, 0.05590682849287987f));
+  p = f32x2_fma_rn(p, f, f32x2_pack(0.24024106562137604f, 0.24024106562137604f));
+  p = f32x2_fma_rn(p, f, f32x2_pack(0.6931241154670715f, 0.6931241154670715f));
+  p = f32x2_fma_rn(p, f, f32x2_pack(1.0f, 1.0f));
+  float t0, t1, p0, p1;
+  f32x2_unpack(t, t0, t1);
+  f32x2_unpack(p, p0, p1);
+  return f32x2_pack_bits(__float_as_uint(p0) + (__float_as_uint(t0) << 23),
+                         __float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+
+// 2^x of two values, on the special-function unit or the fp32 pipe
+template <bool POLY>
+__device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
+  if (POLY) return ex2_poly(x);
+  float a, b;
+  f32x2_unpack(x, a, b);
+  return f32x2_pack(ex2(a), ex2(b));
+}
+
+// 32 columns of this warp's lanes, without the wait
+__device__ __forceinline__ void tmem_ld32_at(uint32_t taddr, uint32_t* r) {
+  tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(r));
+}
+
+// 32 fp32 of a row, times `by`, rounded to bf16, to 16-byte aligned memory
+__device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t* r, float by) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = f32x2_to_bf16x2(f32x2_mul_rn(f32x2_pack_bits(r[8 * c + 2 * e], r[8 * c + 2 * e + 1]),
+                                          f32x2_pack(by, by)));
+    reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+}  // namespace hsnf4
