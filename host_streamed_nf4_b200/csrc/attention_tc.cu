@@ -133,12 +133,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_fwd_tc(const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
   volatile int* abort_p = &abort_flag;
   pdl_wait_then_release();
-  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need the alignment asked for
+  // the swizzled tiles need the alignment asked for
+  if ((smem_u32(smem) & 1023u) || tmem_slot != tmem) {
     if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
-    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem_slot, 512);
     return;
   }
 
@@ -194,50 +195,56 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_fwd_tc(const __grid_cons
     }
   } else if (warp == kMmaWarp && n) {
     // ---------------------------------------------- MMA issuer
-    if (lane == 0) {
-      auto full = [&](int i) {
-        const bool ok = mbar_wait(&kv_full[i % NS], (i / NS) & 1, abort_p, &g_attn_flags,
-                                  kAtFlagMma);
-        tc_fence_after();
-        return ok;
-      };
-      auto stage = [&](int i) { return ring + (i % NS) * G::kTile; };
-      auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
+    auto wait = [&](uint64_t* bar, int phase) {
+      const bool ok = warp_wait(bar, phase, abort_p, kAtFlagMma);
+      tc_fence_after();
+      return ok;
+    };
+    auto full = [&](int i) { return wait(&kv_full[i % NS], i / NS); };
+    auto stage = [&](int i) { return ring + (i % NS) * G::kTile; };
+    auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
+      if (elect_one()) {
         mma_xyt<D>(tmem + t * 128, smem + t * G::kTile, stage(2 * j));
         umma_commit(&s_full[t]);
-      };
-      auto values = [&](int t, int j) {  // O_t += P_t V_j
-        // P becomes ready in two parts, 32 of each half's 64 keys
+      }
+      __syncwarp();
+    };
+    auto values = [&](int t, int j) {  // O_t += P_t V_j
+      // P becomes ready in two parts, 32 of each half's 64 keys
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          if (!mbar_wait(&p_full[t][part], j & 1, abort_p, &g_attn_flags, kAtFlagMma))
-            return false;
-          tc_fence_after();
+      for (int part = 0; part < 2; ++part) {
+        if (!wait(&p_full[t][part], j)) return false;
+        if (elect_one()) {
           mma_ay_steps<D, 64>(tmem + 256 + t * 128, tmem + t * 128, 64, stage(2 * j + 1), 2 * part,
                               2, j > 0 || part > 0);
+          if (part == 1) umma_commit(&o_full[t]);
         }
-        umma_commit(&o_full[t]);
-        return true;
-      };
-      bool ok = mbar_wait(&q_full, 0, abort_p, &g_attn_flags, kAtFlagMma) && full(0);
-      if (ok) {
-        mma_issued = true;
-        if (nt[0]) scores(0, 0);
-        if (nt[1]) scores(1, 0);
-        umma_commit(&kv_empty[0]);
+        __syncwarp();
       }
-      for (int j = 0; j < n && ok; ++j) {
-        const bool more = j + 1 < n;
-        ok = full(2 * j + 1);
-        if (ok && j < nt[0]) ok = values(0, j);
-        if (ok && more) ok = full(2 * j + 2);
-        if (ok && j + 1 < nt[0]) scores(0, j + 1);
-        if (ok && j < nt[1]) ok = values(1, j);
-        if (!ok) break;
-        umma_commit(&kv_empty[(2 * j + 1) % NS]);
-        if (j + 1 < nt[1]) scores(1, j + 1);
-        if (more) umma_commit(&kv_empty[(2 * j + 2) % NS]);
-      }
+      return true;
+    };
+    auto release = [&](int i) {
+      if (elect_one()) umma_commit(&kv_empty[i % NS]);
+      __syncwarp();
+    };
+    bool ok = wait(&q_full, 0) && full(0);
+    if (ok) {
+      mma_issued = true;
+      if (nt[0]) scores(0, 0);
+      if (nt[1]) scores(1, 0);
+      release(0);
+    }
+    for (int j = 0; j < n && ok; ++j) {
+      const bool more = j + 1 < n;
+      ok = full(2 * j + 1);
+      if (ok && j < nt[0]) ok = values(0, j);
+      if (ok && more) ok = full(2 * j + 2);
+      if (ok && j + 1 < nt[0]) scores(0, j + 1);
+      if (ok && j < nt[1]) ok = values(1, j);
+      if (!ok) break;
+      release(2 * j + 1);
+      if (j + 1 < nt[1]) scores(1, j + 1);
+      if (more) release(2 * j + 2);
     }
   } else if (warp < kComputeWarps && work) {
     // ---------------------------------------------- softmax: half a row per thread
@@ -388,7 +395,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_fwd_tc(const __grid_cons
     for (int i = max(0, last_load - NS + 1); i <= last_load; ++i)
       if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
   }
-  if (*abort_p && warp == kMmaWarp && lane == 0 && mma_issued) {
+  if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
     volatile int never = 0;
     umma_commit(&drain);
     mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
@@ -484,12 +491,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
   volatile int* abort_p = &abort_flag;
   pdl_wait_then_release();
-  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need the alignment asked for
+  // the swizzled tiles need the alignment asked for
+  if ((smem_u32(smem) & 1023u) || tmem_slot != tmem) {
     if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
-    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem_slot, 512);
     return;
   }
 
@@ -529,36 +537,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
       last_v = i;
     }
   } else if (warp == kMmaWarp && n) {
-    if (lane == 0) {
-      auto wait = [&](uint64_t* b, int phase) {
-        const bool ok = mbar_wait(b, phase & 1, abort_p, &g_attn_flags, kAtFlagMma);
-        tc_fence_after();
-        return ok;
-      };
-      auto scores = [&](int i) {  // S and dP of step i into their buffer
-        const uint32_t b = (i & 1) * kStep;
-        if (!wait(&k_full[i % NS], i / NS)) return false;
-        mma_issued = true;
+    auto wait = [&](uint64_t* bar, int phase) {
+      const bool ok = warp_wait(bar, phase, abort_p, kAtFlagMma);
+      tc_fence_after();
+      return ok;
+    };
+    auto scores = [&](int i) {  // S and dP of step i into their buffer
+      const uint32_t b = (i & 1) * kStep;
+      if (!wait(&k_full[i % NS], i / NS) || !wait(&v_full[i % NS], i / NS)) return false;
+      mma_issued = true;
+      if (elect_one()) {
         mma_txyt<D, kStep>(tmem + G::kS + b, tmem + G::kQ, smem + (i % NS) * G::kTile);
         umma_commit(&s_full[i & 1]);
-        if (!wait(&v_full[i % NS], i / NS)) return false;
         mma_txyt<D, kStep>(tmem + G::kDp + b, tmem + G::kDo, ring_v + (i % NS) * G::kTile);
         umma_commit(&dp_full[i & 1]);
         umma_commit(&v_empty[i % NS]);
-        return true;
-      };
-      bool ok = wait(&q_ready, 0) && scores(0) && (n < 2 || scores(1));
-      for (int i = 0; i < n && ok; ++i) {
-        ok = wait(&ds_full[i & 1], i >> 1);
-        if (!ok) break;
-        // dQ += dS K: 16 keys in the first 8 of every 16 columns of the buffer
-        mma_tay<D, kStep>(tmem + G::kDq, tmem + G::kDp + (i & 1) * kStep, 16, smem + (i % NS) * G::kTile,
-                          i > 0);
-        umma_commit(&k_empty[i % NS]);
-        if (i + 2 < n) ok = scores(i + 2);
       }
-      if (ok) umma_commit(&done);
+      __syncwarp();
+      return true;
+    };
+    bool ok = wait(&q_ready, 0) && scores(0) && (n < 2 || scores(1));
+    for (int i = 0; i < n && ok; ++i) {
+      ok = wait(&ds_full[i & 1], i >> 1);
+      if (!ok) break;
+      // dQ += dS K: 16 keys in the first 8 of every 16 columns of the buffer
+      if (elect_one()) {
+        mma_tay<D, kStep>(tmem + G::kDq, tmem + G::kDp + (i & 1) * kStep, 16,
+                          smem + (i % NS) * G::kTile, i > 0);
+        umma_commit(&k_empty[i % NS]);
+      }
+      __syncwarp();
+      if (i + 2 < n) ok = scores(i + 2);
     }
+    if (ok && elect_one()) umma_commit(&done);
+    __syncwarp();
   } else if (warp < kComputeWarps && work) {
     const int part = warp >> 2, q4 = warp & 3, tid = q4 * 32 + lane, row = r0 + tid;
     const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
@@ -666,7 +678,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
     for (int i = max(0, last_v - NS + 1); i <= last_v; ++i)
       if (!mbar_wait(&v_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
   }
-  if (*abort_p && warp == kMmaWarp && lane == 0 && mma_issued) {
+  if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
     volatile int never = 0;
     umma_commit(&drain);
     mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
@@ -727,12 +739,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
   volatile int* abort_p = &abort_flag;
   pdl_wait_then_release();
-  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need the alignment asked for
+  // the swizzled tiles need the alignment asked for
+  if ((smem_u32(smem) & 1023u) || tmem_slot != tmem) {
     if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
-    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem_slot, 512);
     return;
   }
 
@@ -817,46 +830,56 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
       }
     }
   } else if (warp == kMmaWarp && n) {
-    if (lane == 0) {
-      auto wait = [&](uint64_t* b, int phase) {
-        const bool ok = mbar_wait(b, phase & 1, abort_p, &g_attn_flags, kAtFlagMma);
-        tc_fence_after();
-        return ok;
-      };
-      auto Q = [&](int i) { return ring + (i % NA) * G::kTile; };
-      auto dO = [&](int i) { return ring + (NA + i % NB) * G::kTile; };
-      auto scores = [&](int i) {  // S^T = K Q^T
-        if (!wait(&q_full[i % NA], i / NA)) return false;
-        mma_issued = true;
+    auto wait = [&](uint64_t* bar, int phase) {
+      const bool ok = warp_wait(bar, phase, abort_p, kAtFlagMma);
+      tc_fence_after();
+      return ok;
+    };
+    auto Q = [&](int i) { return ring + (i % NA) * G::kTile; };
+    auto dO = [&](int i) { return ring + (NA + i % NB) * G::kTile; };
+    auto scores = [&](int i) {  // S^T = K Q^T
+      if (!wait(&q_full[i % NA], i / NA)) return false;
+      mma_issued = true;
+      if (elect_one()) {
         mma_xyt<D>(tmem, smem, Q(i));
         umma_commit(&s_full);
-        return true;
-      };
-      auto dprobs = [&](int i) {  // dP^T = V dO^T
-        if (!wait(&do_full[i % NB], i / NB)) return false;
+      }
+      __syncwarp();
+      return true;
+    };
+    auto dprobs = [&](int i) {  // dP^T = V dO^T
+      if (!wait(&do_full[i % NB], i / NB)) return false;
+      if (elect_one()) {
         mma_xyt<D>(tmem + 128, smem + G::kTile, dO(i));
         umma_commit(&dp_full);
-        return true;
-      };
-      bool ok = wait(&kv_full, 0) && scores(0) && dprobs(0);
-      for (int i = 0; i < n && ok; ++i) {
-        const bool more = i + 1 < n;
-        // dV += P^T dO; P^T becomes ready in two parts, 16 of each 32 queries
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = wait(&kv_full, 0) && scores(0) && dprobs(0);
+    for (int i = 0; i < n && ok; ++i) {
+      const bool more = i + 1 < n;
+      // dV += P^T dO; P^T becomes ready in two parts, 16 of each 32 queries
 #pragma unroll
-        for (int c = 0; c < 2 && ok; ++c) {
-          ok = wait(&p_full[c], i);
-          if (ok) mma_ay_steps<D, 32>(tmem + 256, tmem, 32, dO(i), c, 1, i > 0 || c > 0);
+      for (int c = 0; c < 2 && ok; ++c) {
+        ok = wait(&p_full[c], i);
+        if (ok && elect_one()) {
+          mma_ay_steps<D, 32>(tmem + 256, tmem, 32, dO(i), c, 1, i > 0 || c > 0);
+          if (c == 1) umma_commit(&do_empty[i % NB]);
         }
-        if (!ok) break;
-        umma_commit(&do_empty[i % NB]);
-        ok = (!more || scores(i + 1)) && wait(&ds_full, i);
-        if (!ok) break;
+        __syncwarp();
+      }
+      ok = ok && (!more || scores(i + 1)) && wait(&ds_full, i);
+      if (!ok) break;
+      if (elect_one()) {
         mma_ay<D, 32>(tmem + 256 + D, tmem + 128, 32, Q(i), i > 0);  // dK += dS^T Q
         umma_commit(&q_empty[i % NA]);
-        if (more) ok = dprobs(i + 1);
       }
-      if (ok) umma_commit(&done);
+      __syncwarp();
+      if (more) ok = dprobs(i + 1);
     }
+    if (ok && elect_one()) umma_commit(&done);
+    __syncwarp();
   } else if (warp < kComputeWarps && work) {
     const int part = warp >> 2, q4 = warp & 3, key = c0 + q4 * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
@@ -971,7 +994,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
     for (int i = max(0, last_b - NB + 1); i <= last_b; ++i)
       if (!mbar_wait(&do_full[i % NB], (i / NB) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
   }
-  if (*abort_p && warp == kMmaWarp && lane == 0 && mma_issued) {
+  if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
     volatile int never = 0;
     umma_commit(&drain);
     mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
