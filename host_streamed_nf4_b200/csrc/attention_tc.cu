@@ -26,7 +26,7 @@ enum : unsigned int {
 };
 
 // Of every kPolyOf pairs of exponentials, kPolyPart go to the fp32 pipe.
-constexpr int kPolyOf = 8, kPolyPart = 3;
+constexpr int kPolyOf = 8, kPolyPart = 2;
 constexpr int kComputeWarps = 16;  // four per SM sub-partition
 constexpr int kTcThreads = 32 * (kComputeWarps + 2);
 constexpr int kMmaWarp = kComputeWarps, kLoadWarp = kComputeWarps + 1;
@@ -449,7 +449,7 @@ constexpr int kStep = 64;  // keys of a step
 template <int D>
 struct DqGeo {
   static constexpr int kTile = kStep * D * 2;
-  static constexpr int kStages = D == 128 ? 6 : 8;  // of K and of V
+  static constexpr int kStages = D == 128 ? 6 : 8;  // of a K and a V tile
   static constexpr int kSmem = 2 * kStages * kTile;
   static constexpr uint32_t kQ = 0, kDo = D / 2, kDq = D, kS = 256, kDp = 384;  // TMEM columns
 };
@@ -459,8 +459,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
   using G = DqGeo<D>;
   constexpr int NS = G::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ uint64_t q_ready, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], aux, s_full[2],
-      dp_full[2], ds_full[2], done, drain;
+  __shared__ uint64_t q_ready, kv_full[NS], kv_empty[NS], aux, s_full[2], ds_full[2], done, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float dsum[4][kRows];
@@ -470,14 +469,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
     mbar_init(&aux, 1);
     mbar_init(&drain, 1);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&dp_full[b], 1);
       mbar_init(&ds_full[b], kComputeWarps / 2);
     }
     mbar_init(&done, 1);
@@ -506,68 +502,69 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
   const bool work = find_tile(P.S, false, blockIdx.x / P.H, kRows, x);
   const int r0 = x.t * kRows;
   const int n = work ? (key_limit(P.S, x, min(r0 + kRows, x.lq) - 1) + kStep - 1) / kStep : 0;
-  int last_k = -1, last_v = -1;
+  int last_load = -1;
   bool mma_issued = false;
-  uint8_t* ring_v = smem + NS * G::kTile;
 
   if (warp == kLoadWarp && n) {
     for (int i = 0; i < n; ++i) {
       const int s = i % NS, row = i * kStep;
-      if (i >= NS && !warp_wait(&k_empty[s], (i / NS) - 1, abort_p, kAtFlagLoad)) break;
+      if (i >= NS && !warp_wait(&kv_empty[s], (i / NS) - 1, abort_p, kAtFlagLoad)) break;
+      uint8_t* st = smem + s * 2 * G::kTile;
       const bool tail = row + kStep > x.lk;  // dS is 0 there; K must be finite
-      uint64_t* bar = tail ? &aux : &k_full[s];
+      uint64_t* bar = tail ? &aux : &kv_full[s];
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar, G::kTile);
-        tma_tile<D, kStep>(smem + s * G::kTile, &P.mk, bar, kh * D, x.k0 + row);
+        mbar_arrive_expect_tx(bar, 2 * G::kTile);
+        tma_tile<D, kStep>(st, &P.mk, bar, kh * D, x.k0 + row);
+        tma_tile<D, kStep>(st + G::kTile, &P.mv, bar, kh * D, x.k0 + row);
       }
       if (tail) {
         __syncwarp();
         if (!tail_landed(&aux, 0, abort_p)) break;
-        zero_rows<D, kStep>(smem + s * G::kTile, x.lk - row);
+        zero_rows<D, kStep>(st, x.lk - row);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[s]);
+        if (lane == 0) mbar_arrive(&kv_full[s]);
       }
-      last_k = i;
-      if (i >= NS && !warp_wait(&v_empty[s], (i / NS) - 1, abort_p, kAtFlagLoad)) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&v_full[s], G::kTile);
-        tma_tile<D, kStep>(ring_v + s * G::kTile, &P.mv, &v_full[s], kh * D, x.k0 + row);
-      }
-      last_v = i;
+      last_load = i;
     }
   } else if (warp == kMmaWarp && n) {
+    // As in the forward, a condition is tested before the products that
+    // precede its use, and waited for only if that test failed.
     auto wait = [&](uint64_t* bar, int phase) {
-      const bool ok = warp_wait(bar, phase, abort_p, kAtFlagMma);
-      tc_fence_after();
-      return ok;
+      return warp_wait(bar, phase, abort_p, kAtFlagMma);
     };
-    auto scores = [&](int i) {  // S and dP of step i into their buffer
+    auto stage = [&](int i) { return smem + (i % NS) * 2 * G::kTile; };
+    auto scores = [&](int i) {  // S and dP of step i into their buffer (one thread)
       const uint32_t b = (i & 1) * kStep;
-      if (!wait(&k_full[i % NS], i / NS) || !wait(&v_full[i % NS], i / NS)) return false;
-      mma_issued = true;
-      if (elect_one()) {
-        mma_txyt<D, kStep>(tmem + G::kS + b, tmem + G::kQ, smem + (i % NS) * G::kTile);
-        umma_commit(&s_full[i & 1]);
-        mma_txyt<D, kStep>(tmem + G::kDp + b, tmem + G::kDo, ring_v + (i % NS) * G::kTile);
-        umma_commit(&dp_full[i & 1]);
-        umma_commit(&v_empty[i % NS]);
-      }
-      __syncwarp();
-      return true;
+      mma_txyt<D, kStep>(tmem + G::kS + b, tmem + G::kQ, stage(i));
+      mma_txyt<D, kStep>(tmem + G::kDp + b, tmem + G::kDo, stage(i) + G::kTile);
+      umma_commit(&s_full[i & 1]);
     };
-    bool ok = wait(&q_ready, 0) && scores(0) && (n < 2 || scores(1));
-    for (int i = 0; i < n && ok; ++i) {
-      ok = wait(&ds_full[i & 1], i >> 1);
+    bool ok = wait(&q_ready, 0);
+    tc_fence_after();
+    for (int i = 0; i < 2 && i < n && ok; ++i) {
+      ok = wait(&kv_full[i % NS], i / NS);
       if (!ok) break;
+      mma_issued = true;
+      if (elect_one()) scores(i);
+      __syncwarp();
+    }
+    bool ready = false;
+    for (int i = 0; i < n && ok; ++i) {
+      const bool more = i + 2 < n;
+      ok = (!more || wait(&kv_full[(i + 2) % NS], (i + 2) / NS)) &&
+           (ready || wait(&ds_full[i & 1], i >> 1));
+      if (!ok) break;
+      ready = i + 1 < n && mbar_test(&ds_full[(i + 1) & 1], ((i + 1) >> 1) & 1);
+      ready = __all_sync(0xffffffffu, ready);
+      tc_fence_after();
       // dQ += dS K: 16 keys in the first 8 of every 16 columns of the buffer
       if (elect_one()) {
-        mma_tay<D, kStep>(tmem + G::kDq, tmem + G::kDp + (i & 1) * kStep, 16,
-                          smem + (i % NS) * G::kTile, i > 0);
-        umma_commit(&k_empty[i % NS]);
+        mma_tay<D, kStep>(tmem + G::kDq, tmem + G::kDp + (i & 1) * kStep, 16, stage(i), i > 0);
+        umma_commit(&kv_empty[i % NS]);
+        if (more) scores(i + 2);
       }
       __syncwarp();
-      if (i + 2 < n) ok = scores(i + 2);
     }
     if (ok && elect_one()) umma_commit(&done);
     __syncwarp();
@@ -633,9 +630,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         p[e] = ex2_pair<false>(f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, l2));
-      ok = warp_wait(&dp_full[buf], i >> 1, abort_p, kAtFlagCompute);
-      if (!ok) break;
-      tc_fence_after();
       load_quarter(dP_p, s);
       uint32_t ds[16];
 #pragma unroll
@@ -673,10 +667,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
   __syncthreads();
   if (*abort_p && warp == kLoadWarp && lane == 0) {
     volatile int never = 0;
-    for (int i = max(0, last_k - NS + 1); i <= last_k; ++i)
-      if (!mbar_wait(&k_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
-    for (int i = max(0, last_v - NS + 1); i <= last_v; ++i)
-      if (!mbar_wait(&v_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+    for (int i = max(0, last_load - NS + 1); i <= last_load; ++i)
+      if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
   }
   if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
     volatile int never = 0;
@@ -705,7 +697,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
   constexpr int NA = G::kA, NB = G::kB;  // Q, dO
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t kv_full, q_full[NA], ld_full[2], q_empty[NA], do_full[NB], do_empty[NB], aux,
-      s_full, dp_full, p_full[2], ds_full, done, drain;
+      s_full, dp_full, p_full, ds_full, done, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ __align__(16) float nlse[2][kRows], nD[2][kRows];  // -lse log2(e), -D
@@ -726,8 +718,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
     mbar_init(&s_full, 1);
     mbar_init(&dp_full, 1);
     mbar_init(&done, 1);
-    mbar_init(&p_full[0], kComputeWarps);
-    mbar_init(&p_full[1], kComputeWarps);
+    mbar_init(&p_full, kComputeWarps);
     mbar_init(&ds_full, kComputeWarps);
     abort_flag = 0;
     fence_mbar_init();
@@ -830,53 +821,56 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
       }
     }
   } else if (warp == kMmaWarp && n) {
+    // As in the forward, conditions are tested before the products that
+    // precede their use.
     auto wait = [&](uint64_t* bar, int phase) {
-      const bool ok = warp_wait(bar, phase, abort_p, kAtFlagMma);
-      tc_fence_after();
-      return ok;
+      return warp_wait(bar, phase, abort_p, kAtFlagMma);
+    };
+    auto test = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0;
     };
     auto Q = [&](int i) { return ring + (i % NA) * G::kTile; };
     auto dO = [&](int i) { return ring + (NA + i % NB) * G::kTile; };
-    auto scores = [&](int i) {  // S^T = K Q^T
-      if (!wait(&q_full[i % NA], i / NA)) return false;
-      mma_issued = true;
-      if (elect_one()) {
-        mma_xyt<D>(tmem, smem, Q(i));
-        umma_commit(&s_full);
-      }
-      __syncwarp();
-      return true;
+    auto scores = [&](int i) {  // S^T = K Q^T (one thread)
+      mma_xyt<D>(tmem, smem, Q(i));
+      umma_commit(&s_full);
     };
     auto dprobs = [&](int i) {  // dP^T = V dO^T
-      if (!wait(&do_full[i % NB], i / NB)) return false;
+      mma_xyt<D>(tmem + 128, smem + G::kTile, dO(i));
+      umma_commit(&dp_full);
+    };
+    bool ok = wait(&kv_full, 0) && wait(&q_full[0], 0) && wait(&do_full[0], 0);
+    if (ok) {
+      mma_issued = true;
       if (elect_one()) {
-        mma_xyt<D>(tmem + 128, smem + G::kTile, dO(i));
-        umma_commit(&dp_full);
+        scores(0);
+        dprobs(0);
       }
       __syncwarp();
-      return true;
-    };
-    bool ok = wait(&kv_full, 0) && scores(0) && dprobs(0);
+    }
+    bool q_in = false;
     for (int i = 0; i < n && ok; ++i) {
       const bool more = i + 1 < n;
-      // dV += P^T dO; P^T becomes ready in two parts, 16 of each 32 queries
-#pragma unroll
-      for (int c = 0; c < 2 && ok; ++c) {
-        ok = wait(&p_full[c], i);
-        if (ok && elect_one()) {
-          mma_ay_steps<D, 32>(tmem + 256, tmem, 32, dO(i), c, 1, i > 0 || c > 0);
-          if (c == 1) umma_commit(&do_empty[i % NB]);
-        }
-        __syncwarp();
-      }
-      ok = ok && (!more || scores(i + 1)) && wait(&ds_full, i);
+      ok = (!more || q_in || wait(&q_full[(i + 1) % NA], (i + 1) / NA)) && wait(&p_full, i);
       if (!ok) break;
+      const bool do_in = more && test(&do_full[(i + 1) % NB], (i + 1) / NB);
+      tc_fence_after();
+      if (elect_one()) {
+        mma_ay<D, 32>(tmem + 256, tmem, 32, dO(i), i > 0);  // dV += P^T dO
+        umma_commit(&do_empty[i % NB]);
+        if (more) scores(i + 1);
+      }
+      __syncwarp();
+      ok = (!more || do_in || wait(&do_full[(i + 1) % NB], (i + 1) / NB)) && wait(&ds_full, i);
+      if (!ok) break;
+      q_in = i + 2 < n && test(&q_full[(i + 2) % NA], (i + 2) / NA);
+      tc_fence_after();
       if (elect_one()) {
         mma_ay<D, 32>(tmem + 256 + D, tmem + 128, 32, Q(i), i > 0);  // dK += dS^T Q
         umma_commit(&q_empty[i % NA]);
+        if (more) dprobs(i + 1);
       }
       __syncwarp();
-      if (more) ok = dprobs(i + 1);
     }
     if (ok && elect_one()) umma_commit(&done);
     __syncwarp();
@@ -907,32 +901,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
       uint64_t p[16];
       uint32_t w[16];
       const ulonglong2* ls = reinterpret_cast<const ulonglong2*>(nlse[s] + part * 32);
-      auto drop = [&](int from, int to) {  // select: what is masked may be infinite or NaN
+      auto drop = [&] {  // select: what is masked may be infinite or NaN
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (e >= from && e < to)
-            w[e] &= ((keep >> (2 * e)) & 1 ? 0x0000FFFFu : 0u) |
-                    ((keep >> (2 * e)) & 2 ? 0xFFFF0000u : 0u);
+          w[e] &= ((keep >> (2 * e)) & 1 ? 0x0000FFFFu : 0u) |
+                  ((keep >> (2 * e)) & 2 ? 0xFFFF0000u : 0u);
       };
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int e = 8 * c; e < 8 * c + 8; e += 2) {
-          const ulonglong2 l4 = ls[e / 2];
-          const uint64_t y0 = f32x2_fma_rn(f32x2_pack_bits(v[2 * e], v[2 * e + 1]), c2, l4.x);
-          const uint64_t y1 = f32x2_fma_rn(f32x2_pack_bits(v[2 * e + 2], v[2 * e + 3]), c2, l4.y);
-          p[e] = e % kPolyOf < kPolyPart ? ex2_pair<true>(y0) : ex2_pair<false>(y0);
-          p[e + 1] = (e + 1) % kPolyOf < kPolyPart ? ex2_pair<true>(y1) : ex2_pair<false>(y1);
-          w[e] = f32x2_to_bf16x2(p[e]);
-          w[e + 1] = f32x2_to_bf16x2(p[e + 1]);
-        }
-        if (mask) drop(8 * c, 8 * c + 8);
-        tmem_st8(S_p + 8 * c, w + 8 * c);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[c]);
+      for (int e = 0; e < 16; e += 2) {
+        const ulonglong2 l4 = ls[e / 2];
+        const uint64_t y0 = f32x2_fma_rn(f32x2_pack_bits(v[2 * e], v[2 * e + 1]), c2, l4.x);
+        const uint64_t y1 = f32x2_fma_rn(f32x2_pack_bits(v[2 * e + 2], v[2 * e + 3]), c2, l4.y);
+        p[e] = e % kPolyOf < kPolyPart ? ex2_pair<true>(y0) : ex2_pair<false>(y0);
+        p[e + 1] = (e + 1) % kPolyOf < kPolyPart ? ex2_pair<true>(y1) : ex2_pair<false>(y1);
+        w[e] = f32x2_to_bf16x2(p[e]);
+        w[e + 1] = f32x2_to_bf16x2(p[e + 1]);
       }
+      if (mask) drop();
+      tmem_st16(S_p, w);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full);
       ok = warp_wait(&dp_full, i, abort_p, kAtFlagCompute);
       if (!ok) break;
       tc_fence_after();
@@ -946,7 +936,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
         w[2 * e + 1] = f32x2_to_bf16x2(f32x2_mul_rn(
             p[2 * e + 1], f32x2_add_rn(f32x2_pack_bits(v[4 * e + 2], v[4 * e + 3]), d4.y)));
       }
-      if (mask) drop(0, 16);
+      if (mask) drop();
       tmem_st16(dP_p, w);
       tmem_wait_st();
       tc_fence_before();
