@@ -464,38 +464,59 @@ def attention_bwd(q, k, v, o, lse, dout, H, KV, dq=None, dk=None, dv=None, scrat
 
 # ------------------------------------------------------------------ rotary positions
 
-def _on(dev: torch.device, stream=None):
-    """(raw stream, guard): the stream a call on device `dev` takes, and the
-    context to make it in (the library launches on the current device)."""
-    guard = _NO_GUARD if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device != dev:
-        raise ValueError(f"the stream is on {s.device}, the tensors on {dev}")
-    return s.cuda_stream, guard
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+# the current stream's handle without building a Stream object, and the
+# current device's index
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_cur_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-class _NoGuard:
-    def __enter__(self):
-        return self
+def _launch(index: int, stream, fn, *args):
+    """fn(*args, stream) on device `index` (the library launches on the
+    current device), on `stream` or that device's current one."""
+    if index < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is None:
+        st = _raw_stream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    else:
+        st = stream.cuda_stream
+    if index == _cur_device():
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, st)
+    if rc != OK:
+        raise HsNf4Error(rc, last_error())
 
-    def __exit__(self, *exc):
-        return False
+
+def _bad(t, name, dtype, index, shape):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the others on cuda:{index}")
+    raise ValueError(f"{name} must be {shape}, got {list(t.shape)}, strides {t.stride()}")
 
 
-_NO_GUARD = _NoGuard()
+def _rows(t: torch.Tensor, name: str, index: int, shape) -> int:
+    """Row stride of a bf16 tensor of that (rows, columns) with contiguous
+    rows, on device `index`."""
+    if t.dtype is not _bf16 or t.get_device() != index or t.shape != shape:
+        _bad(t, name, _bf16, index, shape)
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] != 1:
+        _bad(t, name, _bf16, index, f"{shape} with contiguous rows")
+    return s0 if shape[0] > 1 else shape[1]
 
 
-def _rows(t: torch.Tensor, name: str, dev, rows=None, cols=None) -> int:
-    """Row stride of a bf16 [rows, cols] CUDA tensor with contiguous rows."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
-        raise ValueError(f"{name} must be two-dimensional with contiguous rows")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _plain(t: torch.Tensor, name: str, index: int, dtype, numel: int) -> int:
+    """Address of a contiguous tensor of that type and size on device `index`."""
+    if t.dtype is not dtype or t.get_device() != index or t.numel() != numel or \
+            not t.is_contiguous():
+        _bad(t, name, dtype, index, f"contiguous, {numel} values")
+    return t.data_ptr()
 
 
 def rope_inv_freq(rot_dim: int, theta: float) -> torch.Tensor:
@@ -536,28 +557,28 @@ class Rope:
 
 
 def _rope(fn, rope, pos, q, k, q_out, k_out, stream):
-    T, dev = q.shape[0], q.device
-    if pos.dtype != torch.int32 or pos.device != dev or not pos.is_contiguous() or \
-            pos.numel() != rope.n_axes * T:
-        raise ValueError(f"pos must be a contiguous int32 [{rope.n_axes}, {T}] tensor on {dev}")
-    qs = _rows(q, "q", dev)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
-    qos = _rows(q_out, "q_out", dev, T, q.shape[1])
-    H, KV, ks, kos = q.shape[1] // rope.head_dim, 0, 0, 0
-    if H * rope.head_dim != q.shape[1]:
-        raise ValueError(f"q has {q.shape[1]} columns, not a multiple of {rope.head_dim}")
-    if k is not None:
-        ks = _rows(k, "k", dev, T)
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev) if k_out is None else k_out
-        kos = _rows(k_out, "k_out", dev, T, k.shape[1])
-        KV = k.shape[1] // rope.head_dim
-        if KV * rope.head_dim != k.shape[1]:
-            raise ValueError(f"k has {k.shape[1]} columns, not a multiple of {rope.head_dim}")
-    st, guard = _on(dev, stream)
-    with guard:
-        _check(fn(rope._ref, pos.data_ptr(), T, H, KV, q.data_ptr(), qs, _p(k), ks,
-                  q_out.data_ptr(), qos, _p(k_out), kos, st))
-    return (q_out, k_out) if k is not None else q_out
+    dev, d, shape = q.get_device(), rope.head_dim, q.shape
+    T, wq = shape
+    if wq % d:
+        raise ValueError(f"q has {wq} columns, not a multiple of {d}")
+    p = _plain(pos, "pos", dev, _i32, rope.n_axes * T)
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=_bf16, device=q.device)
+    qs, qos = _rows(q, "q", dev, shape), _rows(q_out, "q_out", dev, shape)
+    if k is None:
+        _launch(dev, stream, fn, rope._ref, p, T, wq // d, 0, q.data_ptr(), qs, None, 0,
+                q_out.data_ptr(), qos, None, 0)
+        return q_out
+    wk = k.shape[1]
+    shape = (T, wk)
+    if wk % d:
+        raise ValueError(f"k has {wk} columns, not a multiple of {d}")
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=_bf16, device=q.device)
+    ks, kos = _rows(k, "k", dev, shape), _rows(k_out, "k_out", dev, shape)
+    _launch(dev, stream, fn, rope._ref, p, T, wq // d, wk // d, q.data_ptr(), qs, k.data_ptr(), ks,
+            q_out.data_ptr(), qos, k_out.data_ptr(), kos)
+    return q_out, k_out
 
 
 def rope_fwd(rope: Rope, pos, q, k=None, q_out=None, k_out=None, stream=None):
@@ -576,21 +597,22 @@ def rope_bwd(rope: Rope, pos, dq, dk=None, dq_out=None, dk_out=None, stream=None
 # ------------------------------------------------------------------ packed attention
 
 def _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale):
-    dev = q.device
-    Tq, Tk = q.shape[0], k.shape[0]
-    if H < 1 or KV < 1 or q.shape[1] % H:
-        raise ValueError(f"q has {q.shape[1]} columns for {H} heads (KV heads: {KV})")
-    d = q.shape[1] // H
-    qs = _rows(q, "q", dev)
-    ks, vs = _rows(k, "k", dev, Tk, KV * d), _rows(v, "v", dev, Tk, KV * d)
-    cu_k = cu_q if cu_k is None else cu_k
-    for c, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
-        if c.dtype != torch.int32 or c.device != dev or c.dim() != 1 or not c.is_contiguous() or \
-                c.numel() != cu_q.numel() or c.numel() < 2:
-            raise ValueError(f"{name} must be a contiguous int32 [n_seq + 1] tensor on {dev}")
-    return PackedAttentionC(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cu_q.data_ptr(),
-                            cu_k.data_ptr(), Tq, Tk, cu_q.numel() - 1, H, KV, d, int(bool(causal)),
-                            d ** -0.5 if scale is None else float(scale)), d
+    dev, sq = q.get_device(), q.shape
+    Tq, wq = sq
+    Tk = k.shape[0]
+    if H < 1 or KV < 1 or wq % H:
+        raise ValueError(f"q has {wq} columns for {H} heads (KV heads: {KV})")
+    d = wq // H
+    sk = (Tk, KV * d)
+    n = cu_q.numel()
+    if n < 2:
+        raise ValueError("cu_q must have n_seq + 1 values")
+    pq = _plain(cu_q, "cu_q", dev, _i32, n)
+    pk = pq if cu_k is None or cu_k is cu_q else _plain(cu_k, "cu_k", dev, _i32, n)
+    return dev, sq, sk, d, PackedAttentionC(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, "q", dev, sq), _rows(k, "k", dev, sk),
+        _rows(v, "v", dev, sk), pq, pk, Tq, Tk, n - 1, H, KV, d, 1 if causal else 0,
+        d ** -0.5 if scale is None else scale)
 
 
 def attention_packed_fwd(q, k, v, cu_q, H, KV, causal=True, cu_k=None, scale=None, o=None,
@@ -599,25 +621,15 @@ def attention_packed_fwd(q, k, v, cu_q, H, KV, causal=True, cu_k=None, scale=Non
     (rows may be strided), sequence s the tokens cu_q[s]..cu_q[s + 1] (int32,
     on the device; cu_k: the keys', if they differ).  Rows outside every
     sequence are left as they are in o and lse.  Returns (o, lse [H, Tq])."""
-    a, d = _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale)
-    dev = q.device
+    dev, sq, _, _, a = _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale)
+    Tq = sq[0]
     if o is None:
-        o = torch.zeros(q.shape, dtype=q.dtype, device=dev)
+        o = torch.zeros(sq, dtype=_bf16, device=q.device)
     if lse is None:
-        lse = torch.zeros(H, q.shape[0], dtype=torch.float32, device=dev)
-    os_ = _rows(o, "o", dev, q.shape[0], H * d)
-    _lse(lse, H, q)
-    st, guard = _on(dev, stream)
-    with guard:
-        _check(lib().decoder_attention_packed_fwd(ctypes.byref(a), o.data_ptr(), os_,
-                                                  lse.data_ptr(), st))
+        lse = torch.zeros((H, Tq), dtype=_f32, device=q.device)
+    _launch(dev, stream, lib().decoder_attention_packed_fwd, ctypes.byref(a), o.data_ptr(),
+            _rows(o, "o", dev, sq), _plain(lse, "lse", dev, _f32, H * Tq))
     return o, lse
-
-
-def _lse(lse, H, q):
-    if lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous() or \
-            lse.numel() != H * q.shape[0]:
-        raise ValueError(f"lse must be a contiguous fp32 [{H}, {q.shape[0]}] tensor on {q.device}")
 
 
 def attention_packed_workspace_bytes(Tq, Tk, n_seq, H, KV, d) -> int:
@@ -631,27 +643,22 @@ def attention_packed_bwd(q, k, v, o, lse, dout, cu_q, H, KV, causal=True, cu_k=N
                          dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Its gradients from the forward's o and lse: (dq, dk, dv).  Rows outside
     every sequence are left as they are."""
-    a, d = _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale)
-    dev, Tq, Tk = q.device, q.shape[0], k.shape[0]
-    dq = torch.zeros(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
-    dk = torch.zeros(k.shape, dtype=k.dtype, device=dev) if dk is None else dk
-    dv = torch.zeros(v.shape, dtype=v.dtype, device=dev) if dv is None else dv
-    strides = [_rows(t, name, dev, T, n * d) for t, name, T, n in
-               ((o, "o", Tq, H), (dout, "dout", Tq, H), (dq, "dq", Tq, H), (dk, "dk", Tk, KV),
-                (dv, "dv", Tk, KV))]
-    _lse(lse, H, q)
-    st, guard = _on(dev, stream)
-    with guard:
-        if workspace is None:
+    dev, sq, sk, d, a = _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale)
+    dq = torch.zeros(sq, dtype=_bf16, device=q.device) if dq is None else dq
+    dk = torch.zeros(sk, dtype=_bf16, device=q.device) if dk is None else dk
+    dv = torch.zeros(sk, dtype=_bf16, device=q.device) if dv is None else dv
+    if workspace is None:
+        with torch.cuda.device(dev):
             workspace = torch.empty(
-                attention_packed_workspace_bytes(Tq, Tk, a.n_seq, H, KV, d), dtype=torch.uint8,
-                device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        _check(lib().decoder_attention_packed_bwd(
-            ctypes.byref(a), o.data_ptr(), strides[0], lse.data_ptr(), dout.data_ptr(), strides[1],
-            dq.data_ptr(), strides[2], dk.data_ptr(), strides[3], dv.data_ptr(), strides[4],
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st))
+                attention_packed_workspace_bytes(sq[0], sk[0], a.n_seq, H, KV, d),
+                dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    _launch(dev, stream, lib().decoder_attention_packed_bwd, ctypes.byref(a), o.data_ptr(),
+            _rows(o, "o", dev, sq), _plain(lse, "lse", dev, _f32, H * sq[0]),
+            dout.data_ptr(), _rows(dout, "dout", dev, sq), dq.data_ptr(), _rows(dq, "dq", dev, sq),
+            dk.data_ptr(), _rows(dk, "dk", dev, sk), dv.data_ptr(), _rows(dv, "dv", dev, sk),
+            workspace.data_ptr(), workspace.nbytes)
     return dq, dk, dv
 
 
@@ -669,45 +676,45 @@ class GradSet:
         if not self.tensors or len(self.outs) != len(self.tensors):
             raise ValueError("GradSet takes one tensor or more, and as many outs")
         dev = self.tensors[0].device
-        for i, (g, o) in enumerate(zip(self.tensors, self.outs)):
-            if g.dtype not in GRAD_DTYPES or o.dtype != g.dtype:
+        index = self.tensors[0].get_device()
+        arr = (GradC * len(self.tensors))()
+        for i, (g, o, c) in enumerate(zip(self.tensors, self.outs, arr)):
+            t = GRAD_DTYPES.get(g.dtype)
+            if t is None or o.dtype is not g.dtype:
                 raise TypeError(f"tensor {i}: fp32, bf16 or fp16 and its out the same "
                                 f"(got {g.dtype}, {o.dtype})")
-            if not g.is_cuda or g.device != dev or o.device != dev:
-                raise ValueError(f"tensor {i} is not on {dev}")
-            if not g.is_contiguous() or not o.is_contiguous() or o.numel() != g.numel():
-                raise ValueError(f"tensor {i} or its out is not contiguous, or sizes differ")
+            n = g.numel()
+            if index < 0 or g.get_device() != index or not g.is_contiguous():
+                raise ValueError(f"tensor {i} is not a contiguous tensor on {dev}")
+            if o is not g and (o.get_device() != index or not o.is_contiguous() or
+                               o.numel() != n):
+                raise ValueError(f"out {i} is not a contiguous tensor of {n} values on {dev}")
+            c.g, c.out, c.n, c.dtype = g.data_ptr(), o.data_ptr(), n, t
+        self.device, self.index, self.plan = dev, index, GradPlanC()
         n = len(self.tensors)
-        arr = (GradC * n)(*[GradC(g.data_ptr(), o.data_ptr(), g.numel(), GRAD_DTYPES[g.dtype], 0)
-                            for g, o in zip(self.tensors, self.outs)])
-        self.device, self.plan = dev, GradPlanC()
-        st, guard = _on(dev, stream)
-        with guard:
-            self.table = torch.empty(max(int(lib().lora_grad_table_bytes(n)), 16),
-                                     dtype=torch.uint8, device=dev)
-            _check(lib().lora_grad_plan(arr, n, self.table.data_ptr(), self.table.numel(),
-                                        ctypes.byref(self.plan), st))
-            self.workspace = self.new_workspace()
+        self.table = torch.empty(int(lib().lora_grad_table_bytes(n)) or 16, dtype=torch.uint8,
+                                 device=dev)
+        _launch(index, stream, lambda *a: lib().lora_grad_plan(arr, n, self.table.data_ptr(),
+                                                               self.table.numel(),
+                                                               ctypes.byref(self.plan), *a))
+        self.workspace = self.new_workspace()
         self._ref = ctypes.byref(self.plan)
 
     def new_workspace(self) -> torch.Tensor:
         """A workspace for calls that may run at the same time as others on
         this set (which otherwise share its own)."""
-        return torch.empty(int(lib().lora_grad_workspace(ctypes.byref(self.plan))),
-                           dtype=torch.uint8, device=self.device)
+        with torch.cuda.device(self.index):
+            return torch.empty(int(lib().lora_grad_workspace(ctypes.byref(self.plan))),
+                               dtype=torch.uint8, device=self.device)
 
     def _call(self, fn, args, norm, workspace, stream):
         if norm is None:
             norm = torch.empty((), dtype=torch.float32, device=self.device)
-        elif norm.dtype != torch.float32 or norm.device != self.device or norm.numel() != 1:
-            raise ValueError(f"norm must be one fp32 value on {self.device}")
         ws = self.workspace if workspace is None else workspace
-        if ws.device != self.device or not ws.is_contiguous():
+        if workspace is not None and (ws.get_device() != self.index or not ws.is_contiguous()):
             raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
-        st, guard = _on(self.device, stream)
-        with guard:
-            _check(fn(self._ref, *args, norm.data_ptr(), ws.data_ptr(),
-                      ws.numel() * ws.element_size(), st))
+        _launch(self.index, stream, fn, self._ref, *args,
+                _plain(norm, "norm", self.index, _f32, 1), ws.data_ptr(), ws.nbytes)
         return norm
 
 
