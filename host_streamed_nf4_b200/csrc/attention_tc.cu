@@ -86,6 +86,12 @@ struct FwdTc {
   float c;  // scale * log2(e)
 };
 
+__device__ __forceinline__ void prefetch_maps(const FwdTc& P) {
+  tma_prefetch_desc(&P.mq);
+  tma_prefetch_desc(&P.mk);
+  tma_prefetch_desc(&P.mv);
+}
+
 template <int D>
 struct FwdGeo {
   static constexpr int kTile = tile_bytes<D>();
@@ -126,6 +132,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_fwd_tc(const __grid_cons
     abort_flag = 0;
     fence_mbar_init();
   }
+  if (warp == kLoadWarp && lane == 0) prefetch_maps(P);
   if (warp == kMmaWarp) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
@@ -367,20 +374,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_fwd_tc(const __grid_cons
       l = row_x[0][t][tid] + row_x[1][t][tid];
       const bool some = limit > 0;
       const float inv = some ? 1.0f / l : 0.0f;
-      uint16_t* dst = P.out + (x.q0 + row) * P.os + h * D + half * (D / 2);
+      // the tile's Q is read: its shared memory stages the rows
+      const int first = r0 + t * kRows + q4 * 32;
+      uint4 v[D / 16];
 #pragma unroll
       for (int b = 0; b < D / 64; ++b) {
         uint32_t o[32];
         if (nt[t]) {
-          tmem_ld32_at(O_h + 32 * b, o);
-          tmem_wait_ld();
-          tie32(o);
+          load_quarter(O_h + 32 * b, o);
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (row < x.lq) store_row32(dst + 32 * b, o, inv);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[4 * b + c] = pack8_scaled(o + 8 * c, inv);
       }
+      put_rows<D / 16>(smem + t * G::kTile + (warp & 7) * (32 * D), v,
+                       P.out + static_cast<int64_t>(x.q0 + first) * P.os + h * D + half * (D / 2),
+                       P.os * 2, x.lq - first);
       if (row < x.lq && half == 0)
         P.lse[static_cast<int64_t>(h) * P.S.Tq + x.q0 + row] =
             some ? (ref + log2f(l)) / kLog2e : -INFINITY;
@@ -411,17 +422,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_fwd_tc(const __grid_cons
 // ---------------------------------------------------------------- backward
 
 struct BwdTc {
-  CUtensorMap mq, mk, mv, mdo;  // boxes of 128 rows (mk, mv in the dQ kernel: of kStep)
-  const uint16_t *q, *o, *dout;
+  CUtensorMap mq, mk, mv, mdo, mo;  // boxes of 128 rows (mk, mv in the dQ kernel: of kStep)
   const float* lse;
   float* D;     // [H, Tq]: written by the dQ kernel, read by the dK/dV kernel
   float* part;  // [splits][2][Tk][KV][d] partial dK, dV (splits > 1)
   uint16_t *dq, *dk, *dv;
-  int64_t qs, os, dos, dqs, dks, dvs;
+  int64_t dqs, dks, dvs;
   PackedSeqs S;
   int H, KV, splits;
   float scale, c;  // c = scale * log2(e)
 };
+
+__device__ __forceinline__ void prefetch_maps(const BwdTc& P) {
+  tma_prefetch_desc(&P.mq);
+  tma_prefetch_desc(&P.mk);
+  tma_prefetch_desc(&P.mv);
+  tma_prefetch_desc(&P.mdo);
+}
 
 // Two rings: the tiles that the last product of a step reads (K, or Q) are
 // held longest and get one stage more than the others (V, or dO).
@@ -451,6 +468,7 @@ struct DqGeo {
   static constexpr int kTile = kStep * D * 2;
   static constexpr int kStages = D == 128 ? 6 : 8;  // of a K and a V tile
   static constexpr int kSmem = 2 * kStages * kTile;
+  static constexpr int kFirst = kStages - 3 * kRows / (2 * kStep);  // stages before Q, dO, O
   static constexpr uint32_t kQ = 0, kDo = D / 2, kDq = D, kS = 256, kDp = 384;  // TMEM columns
 };
 
@@ -459,12 +477,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
   using G = DqGeo<D>;
   constexpr int NS = G::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ uint64_t q_ready, kv_full[NS], kv_empty[NS], aux, s_full[2], ds_full[2], done, drain;
+  __shared__ uint64_t q_full, q_ready, kv_full[NS], kv_empty[NS], aux, s_full[2], ds_full[2], done,
+      drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float dsum[4][kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
     mbar_init(&q_ready, kComputeWarps);
     mbar_init(&aux, 1);
     mbar_init(&drain, 1);
@@ -480,6 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
     abort_flag = 0;
     fence_mbar_init();
   }
+  if (warp == kLoadWarp && lane == 0) prefetch_maps(P);
   if (warp == kMmaWarp) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
@@ -503,11 +524,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
   const int r0 = x.t * kRows;
   const int n = work ? (key_limit(P.S, x, min(r0 + kRows, x.lq) - 1) + kStep - 1) / kStep : 0;
   int last_load = -1;
-  bool mma_issued = false;
+  bool q_loaded = false, mma_issued = false;
+  // Q, dO and O of the 128 rows come through the last stages of the ring
+  uint8_t* first_tile = smem + G::kFirst * 2 * G::kTile;
 
   if (warp == kLoadWarp && n) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&q_full, 3 * kRows * D * 2);
+      tma_tile<D>(first_tile, &P.mq, &q_full, h * D, x.q0 + r0);
+      tma_tile<D>(first_tile + kRows * D * 2, &P.mdo, &q_full, h * D, x.q0 + r0);
+      tma_tile<D>(first_tile + 2 * kRows * D * 2, &P.mo, &q_full, h * D, x.q0 + r0);
+    }
+    q_loaded = true;
     for (int i = 0; i < n; ++i) {
       const int s = i % NS, row = i * kStep;
+      // the first tiles' stages
+      if (i == G::kFirst && !warp_wait(&q_ready, 0, abort_p, kAtFlagLoad)) break;
       if (i >= NS && !warp_wait(&kv_empty[s], (i / NS) - 1, abort_p, kAtFlagLoad)) break;
       uint8_t* st = smem + s * 2 * G::kTile;
       const bool tail = row + kStep > x.lk;  // dS is 0 there; K must be finite
@@ -577,15 +609,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
       constexpr int W = D / 8;  // 32-bit words
       uint32_t qw[W], gw[W];
       float sum = 0.0f;
-      const int64_t tok = x.q0 + row;
-      const uint4* qp = reinterpret_cast<const uint4*>(P.q + tok * P.qs + h * D + part * (D / 4));
-      const uint4* gp =
-          reinterpret_cast<const uint4*>(P.dout + tok * P.dos + h * D + part * (D / 4));
-      const uint4* op = reinterpret_cast<const uint4*>(P.o + tok * P.os + h * D + part * (D / 4));
+      if (n) warp_wait(&q_full, 0, abort_p, kAtFlagCompute);  // giving up shows in the next wait
 #pragma unroll
       for (int i = 0; i < W / 4; ++i) {
+        // 16-byte piece of the row in its swizzled box
+        const int piece = part * (D / 32) + i;
+        const uint8_t* at16 = first_tile + (piece >> 3) * kBoxBytes + tid * 128 +
+                              (((piece & 7) ^ (tid & 7)) * 16);
         uint4 a = make_uint4(0, 0, 0, 0), b = a, c = a;
-        if (in) a = qp[i], b = gp[i], c = op[i];
+        if (n) {
+          a = *reinterpret_cast<const uint4*>(at16);
+          b = *reinterpret_cast<const uint4*>(at16 + kRows * D * 2);
+          c = *reinterpret_cast<const uint4*>(at16 + 2 * kRows * D * 2);
+        }
         qw[4 * i] = a.x, qw[4 * i + 1] = a.y, qw[4 * i + 2] = a.z, qw[4 * i + 3] = a.w;
         gw[4 * i] = b.x, gw[4 * i + 1] = b.y, gw[4 * i + 2] = b.z, gw[4 * i + 3] = b.w;
         const uint32_t ow[4] = {c.x, c.y, c.z, c.w};
@@ -607,6 +643,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
+      // the rows are in registers and TMEM: their stages may be refilled
       if (lane == 0) mbar_arrive(&q_ready);
     }
     bar_compute();
@@ -652,7 +689,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
     if (ok && n) ok = warp_wait(&done, 0, abort_p, kAtFlagCompute);
     if (ok && part * 32 < D) {
       tc_fence_after();
-      uint16_t* dst = P.dq + (x.q0 + row) * P.dqs + h * D + part * 32;
       uint32_t o[32];
       if (n) {
         load_quarter(tmem + G::kDq + part * 32 + lanes, o);
@@ -660,13 +696,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0;
       }
-      if (in) store_row32(dst, o, P.scale);
+      uint4 v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = pack8_scaled(o + 8 * c, P.scale);
+      const int first = r0 + q4 * 32;  // all products are done: the ring stages the rows
+      put_rows<4>(smem + warp * 2048, v,
+                  P.dq + static_cast<int64_t>(x.q0 + first) * P.dqs + h * D + part * 32,
+                  P.dqs * 2, x.lq - first);
     }
   }
 
   __syncthreads();
   if (*abort_p && warp == kLoadWarp && lane == 0) {
     volatile int never = 0;
+    if (q_loaded) mbar_wait(&q_full, 0, &never, &g_attn_flags, kAtFlagDrain);
     for (int i = max(0, last_load - NS + 1); i <= last_load; ++i)
       if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
   }
@@ -723,6 +766,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
     abort_flag = 0;
     fence_mbar_init();
   }
+  if (warp == kLoadWarp && lane == 0) prefetch_maps(P);
   if (warp == kMmaWarp) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
@@ -949,10 +993,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
       // eight warps write dV, eight dK, half of the columns each
       const int which = part >> 1, col = (part & 1) * (D / 2);  // 1: dK
       const uint32_t src = tmem + 256 + which * D + col + lanes;
-      const int64_t tok = x.k0 + key;
+      const int first = c0 + q4 * 32;  // all products are done: the ring stages the rows
+      const int64_t tok = x.k0 + first;
       const int64_t one = static_cast<int64_t>(P.S.Tk) * P.KV * D;
-      float* part_to = P.part + (2 * split + 1 - which) * one + (tok * P.KV + kh) * D + col;
-      uint16_t* dst = (which ? P.dk + tok * P.dks : P.dv + tok * P.dvs) + kh * D + col;
+      uint8_t* stage = ring + warp * 4096;
+      uint4 v[D / 16];
 #pragma unroll
       for (int b = 0; b < D / 64; ++b) {
         uint32_t o[32];
@@ -962,15 +1007,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (!in) continue;
         if (P.splits > 1) {
+          uint4 u[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<uint4*>(part_to + 32 * b)[e] =
-                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int c = 0; c < 8; ++c)
+            u[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          put_rows<8>(stage, u,
+                      P.part + (2 * split + 1 - which) * one + (tok * P.KV + kh) * D + col + 32 * b,
+                      static_cast<int64_t>(P.KV) * D * 4, x.lk - first);
         } else {
-          store_row32(dst + 32 * b, o, which ? P.scale : 1.0f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            v[4 * b + c] = pack8_scaled(o + 8 * c, which ? P.scale : 1.0f);
         }
+      }
+      if (P.splits == 1) {
+        const int64_t pitch = which ? P.dks : P.dvs;
+        put_rows<D / 16>(stage, v, (which ? P.dk : P.dv) + tok * pitch + kh * D + col, pitch * 2,
+                         x.lk - first);
       }
     }
   }
@@ -1102,12 +1156,9 @@ cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws
   if (!map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride, kStep) ||
       !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride, kStep) ||
       !map_rows(&P.mq, a.q, wq, a.Tq, a.q_stride) ||
-      !map_rows(&P.mdo, b.dout, wq, a.Tq, b.do_stride))
+      !map_rows(&P.mdo, b.dout, wq, a.Tq, b.do_stride) ||
+      !map_rows(&P.mo, b.o, wq, a.Tq, b.o_stride))
     return cudaErrorInvalidValue;
-  P.q = static_cast<const uint16_t*>(a.q);
-  P.qs = a.q_stride;
-  P.o = static_cast<const uint16_t*>(b.o);
-  P.dout = static_cast<const uint16_t*>(b.dout);
   P.lse = b.lse;
   P.D = static_cast<float*>(ws);
   P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
@@ -1115,8 +1166,6 @@ cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws
   P.dq = static_cast<uint16_t*>(b.dq);
   P.dk = static_cast<uint16_t*>(b.dk);
   P.dv = static_cast<uint16_t*>(b.dv);
-  P.os = b.o_stride;
-  P.dos = b.do_stride;
   P.dqs = b.dq_stride;
   P.dks = b.dk_stride;
   P.dvs = b.dv_stride;

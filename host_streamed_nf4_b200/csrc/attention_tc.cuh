@@ -154,17 +154,39 @@ __device__ __forceinline__ void tmem_ld32_at(uint32_t taddr, uint32_t* r) {
   tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(r));
 }
 
-// 32 fp32 of a row, times `by`, rounded to bf16, to 16-byte aligned memory
-__device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t* r, float by) {
+// 8 fp32, times `by`, rounded to bf16
+__device__ __forceinline__ uint4 pack8_scaled(const uint32_t* r, float by) {
+  uint32_t w[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t w[4];
+  for (int e = 0; e < 4; ++e)
+    w[e] = f32x2_to_bf16x2(
+        f32x2_mul_rn(f32x2_pack_bits(r[2 * e], r[2 * e + 1]), f32x2_pack(by, by)));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Write 32 rows, one per lane, of PIECES (4 or 8) 16-byte pieces to global
+// memory `pitch` bytes apart, the first `rows` of them.  They go through
+// shared memory (512 PIECES bytes of this warp's own) so that a store
+// instruction covers whole row segments: one row per lane touches 32 lines an
+// instruction, which took up to 13000 cycles of a dK/dV tile's epilogue.
+template <int PIECES>
+__device__ __forceinline__ void put_rows(uint8_t* stage, const uint4* v, void* dst, int64_t pitch,
+                                         int rows) {
+  const int lane = threadIdx.x & 31;
+  auto slot = [&](int r, int c) {  // pieces rotated so that a warp's accesses spread over banks
+    return reinterpret_cast<uint4*>(stage) + r * PIECES +
+           (c ^ (PIECES == 8 ? r & 7 : (r >> 1) & 3));
+  };
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = f32x2_to_bf16x2(f32x2_mul_rn(f32x2_pack_bits(r[8 * c + 2 * e], r[8 * c + 2 * e + 1]),
-                                          f32x2_pack(by, by)));
-    reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int c = 0; c < PIECES; ++c) *slot(lane, c) = v[c];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int r = (i * 32 + lane) / PIECES, c = (i * 32 + lane) % PIECES;
+    if (r < rows)
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + r * pitch + c * 16) = *slot(r, c);
   }
+  __syncwarp();
 }
 
 }  // namespace hsnf4

@@ -24,40 +24,56 @@ struct PackedTile {
   int t;               // tile of the sequence (of its queries or of its keys)
 };
 
-__device__ __forceinline__ void seq_range(const int32_t* cu, int s, int T, int& a, int& len) {
-  const int b = min(max(__ldg(cu + s), 0), T), e = min(__ldg(cu + s + 1), T);
-  a = b;
-  len = max(e - b, 0);
-}
-
 // Tile number `slot` over all sequences in order, tiles of `rows` tokens of
 // the queries (or keys).  Within a sequence the longest work comes first
 // under a causal mask: query tiles from the last, key tiles from the first.
-// Whole warp; false if there is no such tile.
+// Whole warp, four sequences a lane at a time: up to 128 sequences cost one
+// round trip to memory.  False if there is no such tile.
 __device__ __forceinline__ bool find_tile(const PackedSeqs& S, bool keys, int slot, int rows,
                                           PackedTile& x) {
   const int lane = threadIdx.x & 31;
-  const int32_t* cu = keys ? S.cu_k : S.cu_q;
-  const int T = keys ? S.Tk : S.Tq;
+  const bool same = S.cu_q == S.cu_k;
   int before = 0;
-  for (int s0 = 0; s0 < S.n_seq; s0 += 32) {
-    int a = 0, len = 0;
-    if (s0 + lane < S.n_seq) seq_range(cu, s0 + lane, T, a, len);
-    const int n = (len + rows - 1) / rows;
-    int inc = n;
+  for (int s0 = 0; s0 < S.n_seq; s0 += 128) {
+    int cq[5], ck[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+      const int i = min(s0 + 4 * lane + j, S.n_seq);  // behind the last: empty
+      cq[j] = __ldg(S.cu_q + i);
+      ck[j] = same ? cq[j] : __ldg(S.cu_k + i);
+    }
+    int n[4], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int T = keys ? S.Tk : S.Tq, c = keys ? ck[j] : cq[j], e = keys ? ck[j + 1] : cq[j + 1];
+      const int len = max(min(e, T) - min(max(c, 0), T), 0);
+      n[j] = (len + rows - 1) / rows;
+      sum += n[j];
+    }
+    int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    const int lo = before + inc - n;
-    const unsigned hit = __ballot_sync(0xffffffffu, slot >= lo && slot < lo + n);
+    const int lo = before + inc - sum;
+    const unsigned hit = __ballot_sync(0xffffffffu, slot >= lo && slot < lo + sum);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      const int s = s0 + src;
-      x.t = __shfl_sync(0xffffffffu, keys ? slot - lo : n - 1 - (slot - lo), src);
-      seq_range(S.cu_q, s, S.Tq, x.q0, x.lq);
-      seq_range(S.cu_k, s, S.Tk, x.k0, x.lk);
+      int at = slot - lo, t = 0, aq = 0, eq = 0, ak = 0, ek = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (at >= 0 && at < n[j]) {
+          t = keys ? at : n[j] - 1 - at;
+          aq = cq[j], eq = cq[j + 1], ak = ck[j], ek = ck[j + 1];
+        }
+        at -= n[j];
+      }
+      x.t = __shfl_sync(0xffffffffu, t, src);
+      x.q0 = min(max(__shfl_sync(0xffffffffu, aq, src), 0), S.Tq);
+      x.lq = max(min(__shfl_sync(0xffffffffu, eq, src), S.Tq) - x.q0, 0);
+      x.k0 = min(max(__shfl_sync(0xffffffffu, ak, src), 0), S.Tk);
+      x.lk = max(min(__shfl_sync(0xffffffffu, ek, src), S.Tk) - x.k0, 0);
       return true;
     }
     before = __shfl_sync(0xffffffffu, before + inc, 31);
