@@ -1,5 +1,6 @@
 // attention_packed.cu -- attention over several sequences packed into one
-// token axis, forward and backward, head_dim 64 or 128, causal or not.
+// token axis, forward and backward, head_dim 64 or 128, causal or not, on the
+// tcgen05 tensor cores.
 //
 // Per sequence (lq queries, lk keys) and query head h with KV head
 // h / (H / KV):
@@ -8,500 +9,1104 @@
 //   D_i = dout_i . o_i,  P_ij = e^{scale q_i . k_j - lse_i},
 //   dS_ij = P_ij (dout_i . v_j - D_i)
 //   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dout
+// Scores, statistics and sums are fp32; P and dS are rounded to bf16 as
+// operands of the second products (2^-9 relative, the size of the outputs'
+// own rounding).
 //
-// Every kernel finds its tile (sequence, tile of the sequence) by itself from
-// the device's cumulative lengths: the grid covers the most tiles the lengths
-// could give (tokens / tile + sequences), so no length is needed on the host.
+// No atomics: dQ and dK/dV come from two kernels that each recompute P (seven
+// products where five would do with unordered additions), and heads that
+// share a KV head are added in order.
 #include <cuda_bf16.h>
 
-#include <stdlib.h>
+#include <string.h>
+
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
+#include "attention_tc.cuh"
 #include "internal.h"
 #include "packed.cuh"
 
 namespace hsnf4 {
 
+__device__ unsigned int g_attn_flags;
+
 namespace {
 
-constexpr int kTile = 64;
-
-struct PackedArgs {
-  const uint16_t *q, *k, *v, *o, *dout;
-  uint16_t *out, *dq, *dk, *dv;
-  float* lse;         // [H, Tq]
-  float* D;           // [H, Tq]
-  float* part;        // backward: [splits][2][Tk][KV][d] partial dK, dV (splits > 1)
-  int64_t qs, ks, vs, os, dos, dqs, dks, dvs;  // token strides
-  PackedSeqs S;
-  int H, KV, splits;
-  float scale;
+enum : unsigned int {
+  kAtFlagLoad = 1u << 19,
+  kAtFlagMma = 1u << 20,
+  kAtFlagCompute = 1u << 21,
+  kAtFlagDrain = 1u << 22,
 };
 
-__device__ __forceinline__ uint32_t su32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+// Of every kPolyOf pairs of exponentials, kPolyPart go to the fp32 pipe.
+constexpr int kPolyOf = 8, kPolyPart = 2;
+constexpr int kComputeWarps = 16;  // four per SM sub-partition
+constexpr int kTcThreads = 32 * (kComputeWarps + 2);
+constexpr int kMmaWarp = kComputeWarps, kLoadWarp = kComputeWarps + 1;
+
+// A wait of the whole loading warp, which leaves whole when it gives up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, volatile int* abort,
+                                          unsigned int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort, &g_attn_flags, site));
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+// Wait of the whole loading warp for a tile that it will patch.  Giving up,
+// it first lets the copy land (or the limit pass) before the shared memory
+// goes away.
+__device__ __forceinline__ bool tail_landed(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_wait(bar, parity, abort, &g_attn_flags, kAtFlagLoad)))
+    return true;
+  volatile int never = 0;
+  mbar_wait(bar, parity, &never, &g_attn_flags, kAtFlagDrain);
+  return false;
+}
+
+// Two warps (64 threads) that share the rows of a tile: a barrier, and votes
+// over both.
+__device__ __forceinline__ void pair_sync(int id) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool pair_any(int id, bool v) {
+  uint32_t r;
+  __syncwarp();
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id)
+      : "memory");
+  return r != 0;
 }
+__device__ __forceinline__ bool pair_all(int id, bool v) { return !pair_any(id, !v); }
 
-__device__ __forceinline__ void ldm_x4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-
-__device__ __forceinline__ void ldm_x4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(src_bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// 64 rows x D columns of a sequence's rows (len of them from `src`, one head)
-// from row r0 on into a padded tile; rows past the sequence become zeros, so
-// that what stands behind it in memory (other sequences, unset rows, even
-// NaN) meets no product.
-template <int D>
-__device__ __forceinline__ void load_rows(uint16_t* dst, const uint16_t* src, int r0, int len,
-                                          int64_t stride) {
-  for (int v = threadIdx.x; v < kTile * (D / 8); v += blockDim.x) {
-    const int row = v / (D / 8), col = (v % (D / 8)) * 8;
-    const bool in = r0 + row < len;
-    const uint16_t* s = in ? src + static_cast<int64_t>(r0 + row) * stride + col : src;
-    cp_async16(su32(dst + row * (D + 8) + col), s, in ? 16 : 0);
-  }
-}
-
-template <int D>
-__device__ __forceinline__ void frag_a(uint32_t (&a)[4], const uint16_t* tile, int m0, int k0) {
-  const int lane = threadIdx.x & 31;
-  ldm_x4(a, su32(tile + (m0 + (lane & 15)) * (D + 8) + k0 + (lane >> 4) * 8));
-}
-template <int D>
-__device__ __forceinline__ void frag_bt(uint32_t (&b)[4], const uint16_t* tile, int n0, int k0) {
-  const int lane = threadIdx.x & 31;
-  ldm_x4(b, su32(tile + (n0 + (lane & 7)) * (D + 8) + k0 + (lane >> 3) * 8));
-}
-template <int D>
-__device__ __forceinline__ void frag_b(uint32_t (&b)[4], const uint16_t* tile, int k0, int n0) {
-  const int lane = threadIdx.x & 31;
-  ldm_x4_t(b, su32(tile + (k0 + (lane & 7) + ((lane >> 3) & 1) * 8) * (D + 8) + n0 +
-                   (lane >> 4) * 8));
-}
-
-// S[16 x 64] = 16 rows (m0) of tile X . Y^T
-template <int D>
-__device__ __forceinline__ void gemm_xyt(float (&s)[8][4], const uint16_t* X, int m0,
-                                         const uint16_t* Y) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[j][e] = 0.0f;
-#pragma unroll
-  for (int k0 = 0; k0 < D; k0 += 32) {
-    uint32_t a0[4], a1[4];
-    frag_a<D>(a0, X, m0, k0);
-    frag_a<D>(a1, X, m0, k0 + 16);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t b[4];
-      frag_bt<D>(b, Y, j * 8, k0);
-      mma16816(s[j], a0, b[0], b[1]);
-      mma16816(s[j], a1, b[2], b[3]);
-    }
-  }
-}
-
-// acc[16 x D] += P (16 x 64, rounded to bf16) . Y (64 x D tile)
-template <int D>
-__device__ __forceinline__ void gemm_py(float (&acc)[D / 8][4], const float (&p)[8][4],
-                                        const uint16_t* Y) {
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
-    uint32_t a[4];
-    a[0] = pack_bf16(p[2 * kk][0], p[2 * kk][1]);
-    a[1] = pack_bf16(p[2 * kk][2], p[2 * kk][3]);
-    a[2] = pack_bf16(p[2 * kk + 1][0], p[2 * kk + 1][1]);
-    a[3] = pack_bf16(p[2 * kk + 1][2], p[2 * kk + 1][3]);
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n) {
-      uint32_t b[4];
-      frag_b<D>(b, Y, kk * 16, n * 16);
-      mma16816(acc[2 * n], a, b[0], b[1]);
-      mma16816(acc[2 * n + 1], a, b[2], b[3]);
-    }
-  }
-}
-
-template <int D>
-__device__ __forceinline__ void zero(float (&acc)[D / 8][4]) {
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+// 32 columns of this warp's lanes
+__device__ __forceinline__ void load_quarter(uint32_t taddr, uint32_t* r) {
+  tmem_ld32_at(taddr, r);
+  tmem_wait_ld();
+  tie32(r);
 }
 
 // ---------------------------------------------------------------- forward
-template <int D>
-__global__ void __launch_bounds__(128) packed_fwd_kernel(const __grid_constant__ PackedArgs P) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kEl = kTile * (D + 8);
-  uint16_t* Qs = reinterpret_cast<uint16_t*>(smem);
-  uint16_t* KVs = Qs + kEl;  // K0 V0 K1 V1
+
+struct FwdTc {
+  CUtensorMap mq, mk, mv;
+  uint16_t* out;
+  float* lse;
+  int64_t os;
+  PackedSeqs S;
+  int H, KV;
+  float c;  // scale * log2(e)
+};
+
+__device__ __forceinline__ void prefetch_maps(const FwdTc& P) {
+  tma_prefetch_desc(&P.mq);
+  tma_prefetch_desc(&P.mk);
+  tma_prefetch_desc(&P.mv);
+}
+
+// NQ query tiles of 128 rows per CTA: two share the keys' loads and keep the
+// tensor cores busy in turn; with one, two CTAs fit an SM, so that one's start
+// and end hide behind the other's work (short sequences).
+template <int D, int NQ>
+struct FwdGeo {
+  static constexpr int kTile = tile_bytes<D>();
+  static constexpr int kStages = NQ == 1 ? (D == 128 ? 2 : 4) : (D == 128 ? 4 : 8);
+  static constexpr int kSmem = (NQ + kStages) * kTile;
+  static constexpr int kWarps = 8 * NQ;  // computing warps; then the MMA issuer and the loader
+  static constexpr int kThreads = 32 * (kWarps + 2);
+  static constexpr uint32_t kO = 128 * NQ, kCols = 256 * NQ;  // TMEM: S per tile, then O per tile
+};
+
+// A CTA takes 256 query rows of one head as two tiles of 128 and walks the
+// keys 128 at a time.  Each tile has eight warps: a row belongs to two
+// threads, in two warps, 64 of the 128 keys each.  TMEM: S0 S1 (128 columns each; P overwrites its S as bf16), O0 O1.
+// The tensor cores work on one tile's products while the other tile's
+// warpgroup computes its probabilities.
+template <int D, int NQ>
+__global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
+    packed_fwd_tc(const __grid_constant__ FwdTc P) {
+  using G = FwdGeo<D, NQ>;
+  constexpr int NS = G::kStages, kMmaWarp = G::kWarps, kLoadWarp = G::kWarps + 1;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t q_full, kv_full[NS], kv_empty[NS], aux, s_full[NQ], p_full[NQ][2], o_full[NQ],
+      drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ float row_x[2][NQ][kRows];  // [half][tile][row]: exchanged between two warps
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0 && lane == 0) prefetch_maps(P);
+  pdl_wait_then_release();
+  // (before anything is set up: the grid covers the most tiles there could be)
   PackedTile x;
-  const int h = blockIdx.x % P.H;
-  if (!find_tile(P.S, false, blockIdx.x / P.H, kTile, x)) return;
-  const int kh = h / (P.H / P.KV);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, qd = lane & 3;
-  const int m0 = warp * 16, r0 = x.t * kTile;
-  const uint16_t* q = P.q + x.q0 * P.qs + h * D;
-  const uint16_t* k = P.k + x.k0 * P.ks + kh * D;
-  const uint16_t* v = P.v + x.k0 * P.vs + kh * D;
-  const int tiles = (key_limit(P.S, x, min(r0 + kTile, x.lq) - 1) + kTile - 1) / kTile;
-  load_rows<D>(Qs, q, r0, x.lq, P.qs);
-  if (tiles) {
-    load_rows<D>(KVs, k, 0, x.lk, P.ks);
-    load_rows<D>(KVs + kEl, v, 0, x.lk, P.vs);
-  }
-  cp_async_commit();
-  const float c = P.scale * kLog2e;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-  float acc[D / 8][4];
-  zero<D>(acc);
-  const int rows[2] = {r0 + m0 + g, r0 + m0 + g + 8};
-  const int lim[2] = {key_limit(P.S, x, rows[0]), key_limit(P.S, x, rows[1])};
-  for (int kt = 0; kt < tiles; ++kt) {
-    const uint16_t* Ks = KVs + ((kt & 1) * 2) * kEl;
-    if (kt + 1 < tiles) {
-      uint16_t* Kn = KVs + (((kt + 1) & 1) * 2) * kEl;
-      load_rows<D>(Kn, k, (kt + 1) * kTile, x.lk, P.ks);
-      load_rows<D>(Kn + kEl, v, (kt + 1) * kTile, x.lk, P.vs);
+  if (!find_tile(P.S, false, blockIdx.x / P.H, NQ * kRows, x)) return;
+  if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&aux, 1);
+    mbar_init(&drain, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
     }
-    cp_async_commit();
-    cp_async_wait<1>();
-    __syncthreads();
-    float s[8][4];
-    gemm_xyt<D>(s, Qs, m0, Ks);
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      float mx = m[hr];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int key = kt * kTile + j * 8 + 2 * qd + e;
-          float& y = s[j][2 * hr + e];
-          y = key < lim[hr] ? y * c : -INFINITY;
-          mx = fmaxf(mx, y);
+    for (int t = 0; t < NQ; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t][0], 8);
+      mbar_init(&p_full[t][1], 8);
+      mbar_init(&o_full[t], 1);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_slot, G::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // with two tiles all 512 columns are this CTA's: a base known at compile time
+  const uint32_t tmem = NQ == 2 ? 0u : tmem_slot;
+  volatile int* abort_p = &abort_flag;
+  // the swizzled tiles need the alignment asked for
+  if ((smem_u32(smem) & 1023u) || tmem_slot != tmem) {
+    if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
+    if (warp == kMmaWarp) tmem_dealloc(tmem_slot, G::kCols);
+    return;
+  }
+
+  const int h = blockIdx.x % P.H, kh = h / (P.H / P.KV);
+  int last_load = -1, n = 0, nt[NQ] = {};
+  bool q_loaded = false, mma_issued = false;
+  const int r0 = x.t * NQ * kRows;
+  for (int t = 0; t < NQ; ++t) {
+    const int first = r0 + t * kRows, end = min(first + kRows, x.lq);
+    if (first < end) nt[t] = (key_limit(P.S, x, end - 1) + kRows - 1) / kRows;
+    n = max(n, nt[t]);
+  }
+  uint8_t* ring = smem + NQ * G::kTile;
+
+  if (warp == kLoadWarp && n) {
+    // ---------------------------------------------- TMA: Q, then K0 V0 K1 V1 ...
+    const bool two = NQ == 2 && r0 + kRows < x.lq;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * G::kTile);
+      tma_tile<D>(smem, &P.mq, &q_full, h * D, x.q0 + r0);
+      if (two) tma_tile<D>(smem + G::kTile, &P.mq, &q_full, h * D, x.q0 + r0 + kRows);
+    }
+    q_loaded = true;
+    for (int i = 0; i < 2 * n; ++i) {
+      const int s = i % NS, row = (i >> 1) * kRows;
+      if (i >= NS && !__all_sync(0xffffffffu, mbar_wait(&kv_empty[s], ((i / NS) - 1) & 1, abort_p,
+                                                         &g_attn_flags, kAtFlagLoad)))
+        break;
+      uint8_t* st = ring + s * G::kTile;
+      const CUtensorMap* map = (i & 1) ? &P.mv : &P.mk;
+      if ((i & 1) && row + kRows > x.lk) {
+        // the keys behind the sequence have probability 0; their values must
+        // be finite for the product: zeros
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&aux, G::kTile);
+          tma_tile<D>(st, map, &aux, kh * D, x.k0 + row);
         }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float ref = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet: e^-inf = 0
-      const float corr = exp2f(m[hr] - ref);
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& y = s[j][2 * hr + e];
-          y = exp2f(y - ref);
-          sum += y;
-        }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      l[hr] = l[hr] * corr + sum;
-      m[hr] = mx;
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        acc[n][2 * hr] *= corr;
-        acc[n][2 * hr + 1] *= corr;
+        __syncwarp();
+        if (!tail_landed(&aux, 0, abort_p)) break;
+        zero_rows<D>(st, x.lk - row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[s]);
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(&kv_full[s], G::kTile);
+        tma_tile<D>(st, map, &kv_full[s], kh * D, x.k0 + row);
       }
+      last_load = i;
     }
-    gemm_py<D>(acc, s, Ks + kEl);
-    __syncthreads();
+  } else if (warp == kMmaWarp && n) {
+    // ---------------------------------------------- MMA issuer
+    auto wait = [&](uint64_t* bar, int phase) {
+      const bool ok = warp_wait(bar, phase, abort_p, kAtFlagMma);
+      tc_fence_after();
+      return ok;
+    };
+    auto full = [&](int i) { return wait(&kv_full[i % NS], i / NS); };
+    auto stage = [&](int i) { return ring + (i % NS) * G::kTile; };
+    auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
+      if (elect_one()) {
+        mma_xyt<D>(tmem + t * 128, smem + t * G::kTile, stage(2 * j));
+        umma_commit(&s_full[t]);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int t, int j) {  // O_t += P_t V_j
+      // P becomes ready in two parts, 32 of each half's 64 keys
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        if (!wait(&p_full[t][part], j)) return false;
+        if (elect_one()) {
+          mma_ay_steps<D, 64>(tmem + G::kO + t * 128, tmem + t * 128, 64, stage(2 * j + 1), 2 * part,
+                              2, j > 0 || part > 0);
+          if (part == 1) umma_commit(&o_full[t]);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+    auto release = [&](int i) {
+      if (elect_one()) umma_commit(&kv_empty[i % NS]);
+      __syncwarp();
+    };
+    bool ok = wait(&q_full, 0) && full(0);
+    if (ok) {
+      mma_issued = true;
+      for (int t = 0; t < NQ; ++t)
+        if (nt[t]) scores(t, 0);
+      release(0);
+    }
+    for (int j = 0; j < n && ok; ++j) {
+      const bool more = j + 1 < n;
+      ok = full(2 * j + 1);
+      if (ok && j < nt[0]) ok = values(0, j);
+      if (ok && more) ok = full(2 * j + 2);
+      if (ok && j + 1 < nt[0]) scores(0, j + 1);
+      if (ok && NQ == 2 && j < nt[NQ - 1]) ok = values(NQ - 1, j);
+      if (!ok) break;
+      release(2 * j + 1);
+      if (NQ == 2 && j + 1 < nt[NQ - 1]) scores(NQ - 1, j + 1);
+      if (more) release(2 * j + 2);
+    }
+  } else if (warp < G::kWarps) {
+    // ---------------------------------------------- softmax: half a row per thread
+    // tile t, half of the 128 keys, and the TMEM lane quarter of the warp
+    const int t = warp >> 3, half = (warp >> 2) & 1, q4 = warp & 3, tid = q4 * 32 + lane;
+    const int row = r0 + t * kRows + tid;
+    const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t S_h = tmem + t * 128 + half * 64 + lanes;
+    const uint32_t O_h = tmem + G::kO + t * 128 + half * (D / 2) + lanes;
+    const int pair = 1 + t * 4 + q4;  // barrier of the two warps that share the rows
+    const int limit = key_limit(P.S, x, row);
+    const uint64_t c2 = f32x2_pack(P.c, P.c);
+    float ref = 0.0f, l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < nt[t]; ++j) {
+      // both warps of a row leave together: their barriers must match
+      ok = pair_all(pair, mbar_wait(&s_full[t], j & 1, abort_p, &g_attn_flags, kAtFlagCompute));
+      if (!ok) break;
+      tc_fence_after();
+      const int lim = limit - j * kRows - half * 64;
+      const bool mask = __any_sync(0xffffffffu, lim < 64);
+      // 32 columns at a time, read once for the maximum and once more for the
+      // probabilities: holding all 64 spilled registers
+      auto scores = [&](int b, uint32_t* s) {
+        load_quarter(S_h + 32 * b, s);
+        if (!mask) return;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (32 * b + e >= lim) s[e] = 0xff800000u;  // -inf
+      };
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t s[32];
+        scores(b, s);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          m4[(e >> 1) & 3] = max_nan(max_nan(m4[(e >> 1) & 3], __uint_as_float(s[e])),
+                                     __uint_as_float(s[e + 1]));
+      }
+      // (a row behind the sequence holds another's values and has no say)
+      const float mt = row < x.lq ? max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3])) * P.c
+                                  : -INFINITY;
+      // a NaN or an infinite score: the polynomial would not keep it
+      const bool odd = __any_sync(0xffffffffu, !(mt < INFINITY));
+      // The reference of a row's exponentials moves only when a score passes
+      // it by 2^8 (fp32 sums and bf16 probabilities lose nothing at that
+      // size); then O and the sum are scaled to the new one.
+      if (pair_any(pair, j == 0 || mt > ref + 8.0f)) {
+        row_x[half][t][tid] = mt;
+        pair_sync(pair);
+        const float m = fmaxf(mt, row_x[half ^ 1][t][tid]);
+        if (j == 0) {
+          ref = m == -INFINITY ? 0.0f : m;  // a row without a key: all 0
+        } else {
+          ok = pair_all(pair, mbar_wait(&o_full[t], (j - 1) & 1, abort_p, &g_attn_flags,
+                                        kAtFlagCompute));
+          if (!ok) break;
+          tc_fence_after();
+          const float next = fmaxf(ref, m), f = ex2(ref - next);
+          ref = next;
+          l *= f;
+          const uint64_t f2 = f32x2_pack(f, f);
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b) {
+            uint32_t o[32];
+            tmem_ld32_at(O_h + 32 * b, o);
+            tmem_wait_ld();
+            tie32(o);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float lo, hi;
+              f32x2_unpack(f32x2_mul_rn(f32x2_pack_bits(o[e], o[e + 1]), f2), lo, hi);
+              o[e] = __float_as_uint(lo);
+              o[e + 1] = __float_as_uint(hi);
+            }
+            tmem_st32(O_h + 32 * b, o);
+          }
+        }
+      }
+      const uint64_t r2 = f32x2_pack(-ref, -ref);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t s[32], p[16];
+        scores(b, s);
+        auto probs = [&](auto poly) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t y =
+                f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, r2);
+            const uint64_t pr = decltype(poly)::value && e % kPolyOf < kPolyPart
+                                    ? ex2_pair<true>(y)
+                                    : ex2_pair<false>(y);
+            sum[e & 1] = f32x2_add_rn(sum[e & 1], pr);
+            p[e] = f32x2_to_bf16x2(pr);
+          }
+        };
+        if (odd)
+          probs(std::false_type());
+        else
+          probs(std::true_type());
+        tmem_st16(S_h + 16 * b, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t][b]);
+      }
+      float a0, a1;
+      f32x2_unpack(f32x2_add_rn(sum[0], sum[1]), a0, a1);
+      l += a0 + a1;
+    }
+    if (ok && nt[t])
+      ok = pair_all(pair, mbar_wait(&o_full[t], (nt[t] - 1) & 1, abort_p, &g_attn_flags,
+                                    kAtFlagCompute));
+    if (ok) {
+      tc_fence_after();
+      row_x[half][t][tid] = l;
+      pair_sync(pair);
+      l = row_x[0][t][tid] + row_x[1][t][tid];
+      const bool some = limit > 0;
+      const float inv = some ? 1.0f / l : 0.0f;
+      // the tile's Q is read: its shared memory stages the rows
+      const int first = r0 + t * kRows + q4 * 32;
+      uint4 v[D / 16];
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) {
+        uint32_t o[32];
+        if (nt[t]) {
+          load_quarter(O_h + 32 * b, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[4 * b + c] = pack8_scaled(o + 8 * c, inv);
+      }
+      put_rows<D / 16>(smem + t * G::kTile + (warp & 7) * (32 * D), v,
+                       P.out + static_cast<int64_t>(x.q0 + first) * P.os + h * D + half * (D / 2),
+                       P.os * 2, x.lq - first);
+      if (row < x.lq && half == 0)
+        P.lse[static_cast<int64_t>(h) * P.S.Tq + x.q0 + row] =
+            some ? (ref + log2f(l)) / kLog2e : -INFINITY;
+    }
   }
-#pragma unroll
-  for (int hr = 0; hr < 2; ++hr) {
-    if (rows[hr] >= x.lq) continue;
-    const float inv = lim[hr] ? 1.0f / l[hr] : 0.0f;
-    uint16_t* dst = P.out + (x.q0 + rows[hr]) * P.os + h * D;
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-      *reinterpret_cast<uint32_t*>(dst + n * 8 + 2 * qd) =
-          pack_bf16(acc[n][2 * hr] * inv, acc[n][2 * hr + 1] * inv);
-    if (qd == 0)
-      P.lse[static_cast<int64_t>(h) * P.S.Tq + x.q0 + rows[hr]] =
-          lim[hr] ? (m[hr] + log2f(l[hr])) / kLog2e : -INFINITY;
+
+  __syncthreads();  // every thread sees the final abort word
+  if (*abort_p && warp == kLoadWarp && lane == 0) {
+    // drain what this CTA started before its shared memory and TMEM go away
+    volatile int never = 0;
+    if (q_loaded) mbar_wait(&q_full, 0, &never, &g_attn_flags, kAtFlagDrain);
+    for (int i = max(0, last_load - NS + 1); i <= last_load; ++i)
+      if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+  }
+  if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
+    volatile int never = 0;
+    umma_commit(&drain);
+    mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, G::kCols);
   }
 }
 
-// ---------------------------------------------------------------- dQ
+// ---------------------------------------------------------------- backward
+
+struct BwdTc {
+  CUtensorMap mq, mk, mv, mdo, mo;  // boxes of 128 rows (mk, mv in the dQ kernel: of kStep)
+  const float* lse;
+  float* D;     // [H, Tq]: written by the dQ kernel, read by the dK/dV kernel
+  float* part;  // [splits][2][Tk][KV][d] partial dK, dV (splits > 1)
+  uint16_t *dq, *dk, *dv;
+  int64_t dqs, dks, dvs;
+  PackedSeqs S;
+  int H, KV, splits;
+  float scale, c;  // c = scale * log2(e)
+};
+
+__device__ __forceinline__ void prefetch_maps(const BwdTc& P) {
+  tma_prefetch_desc(&P.mq);
+  tma_prefetch_desc(&P.mk);
+  tma_prefetch_desc(&P.mv);
+  tma_prefetch_desc(&P.mdo);
+}
+
+// Two rings: the tiles that the last product of a step reads (K, or Q) are
+// held longest and get one stage more than the others (V, or dO).
 template <int D>
-__global__ void __launch_bounds__(128) packed_dq_kernel(const __grid_constant__ PackedArgs P) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kEl = kTile * (D + 8);
-  uint16_t* Qs = reinterpret_cast<uint16_t*>(smem);
-  uint16_t* dOs = Qs + kEl;
-  uint16_t* Os = dOs + kEl;
-  uint16_t* KVs = Os + kEl;  // K0 V0 K1 V1
-  __shared__ float Ds[kTile];
+struct BwdGeo {
+  static constexpr int kTile = tile_bytes<D>();
+  static constexpr int kA = D == 128 ? 3 : 5, kB = D == 128 ? 2 : 4;
+  static constexpr int kSmem = (2 + kA + kB) * kTile;
+};
+
+__device__ __forceinline__ void bar_compute() {  // the computing threads
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
+}
+
+// dQ of 128 query rows of one head, the keys 64 at a time: S = Q K^T,
+// dP = dO V^T, dS = P (dP - D) as bf16 over its dP, dQ += dS K.  Q and dO,
+// which every step reads, stay in TMEM as left operands, so that no product
+// reads more than 16 KiB of shared memory per step (with both operands there
+// the 128 x 128 x 16 products took 86 to 116 cycles instead of 64).  TMEM:
+// Q, dO (D / 2 columns each), dQ (D), two buffers of S and dP (64 columns
+// each); warps 0..7 take the even steps, 8..15 the odd ones.  The kernel also
+// writes D = dO . O for the dK/dV kernel.
+constexpr int kStep = 64;  // keys of a step
+
+template <int D>
+struct DqGeo {
+  static constexpr int kTile = kStep * D * 2;
+  static constexpr int kStages = D == 128 ? 6 : 8;  // of a K and a V tile
+  static constexpr int kSmem = 2 * kStages * kTile;
+  static constexpr int kFirst = kStages - 3 * kRows / (2 * kStep);  // stages before Q, dO, O
+  static constexpr uint32_t kQ = 0, kDo = D / 2, kDq = D, kS = 256, kDp = 384;  // TMEM columns
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_constant__ BwdTc P) {
+  using G = DqGeo<D>;
+  constexpr int NS = G::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t q_full, q_ready, kv_full[NS], kv_empty[NS], aux, s_full[2], ds_full[2], done,
+      drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ float dsum[4][kRows];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0 && lane == 0) prefetch_maps(P);
+  pdl_wait_then_release();
+  // (before anything is set up: the grid covers the most tiles there could be)
   PackedTile x;
-  const int h = blockIdx.x % P.H;
-  if (!find_tile(P.S, false, blockIdx.x / P.H, kTile, x)) return;
-  const int kh = h / (P.H / P.KV);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, qd = lane & 3;
-  const int m0 = warp * 16, r0 = x.t * kTile;
-  const uint16_t* k = P.k + x.k0 * P.ks + kh * D;
-  const uint16_t* v = P.v + x.k0 * P.vs + kh * D;
-  const int tiles = (key_limit(P.S, x, min(r0 + kTile, x.lq) - 1) + kTile - 1) / kTile;
-  load_rows<D>(Qs, P.q + x.q0 * P.qs + h * D, r0, x.lq, P.qs);
-  load_rows<D>(dOs, P.dout + x.q0 * P.dos + h * D, r0, x.lq, P.dos);
-  load_rows<D>(Os, P.o + x.q0 * P.os + h * D, r0, x.lq, P.os);
-  cp_async_commit();
-  if (tiles) {
-    load_rows<D>(KVs, k, 0, x.lk, P.ks);
-    load_rows<D>(KVs + kEl, v, 0, x.lk, P.vs);
+  if (!find_tile(P.S, false, blockIdx.x / P.H, kRows, x)) return;
+  if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&q_ready, kComputeWarps);
+    mbar_init(&aux, 1);
+    mbar_init(&drain, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&ds_full[b], kComputeWarps / 2);
+    }
+    mbar_init(&done, 1);
+    abort_flag = 0;
+    fence_mbar_init();
   }
-  cp_async_commit();
-  cp_async_wait<1>();
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
-  {  // D = dout . o, two threads a row
-    const int row = threadIdx.x >> 1, half = threadIdx.x & 1;
-    const uint32_t* a = reinterpret_cast<const uint32_t*>(dOs + row * (D + 8) + half * (D / 2));
-    const uint32_t* b = reinterpret_cast<const uint32_t*>(Os + row * (D + 8) + half * (D / 2));
-    float sum = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < D / 4; ++i) {
-      sum += __uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16);
-      sum += __uint_as_float(a[i] & 0xFFFF0000u) * __uint_as_float(b[i] & 0xFFFF0000u);
+  tc_fence_after();
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
+  volatile int* abort_p = &abort_flag;
+  // the swizzled tiles need the alignment asked for
+  if ((smem_u32(smem) & 1023u) || tmem_slot != tmem) {
+    if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
+    if (warp == kMmaWarp) tmem_dealloc(tmem_slot, 512);
+    return;
+  }
+
+  const int h = blockIdx.x % P.H, kh = h / (P.H / P.KV);
+  const int r0 = x.t * kRows;
+  const int n = (key_limit(P.S, x, min(r0 + kRows, x.lq) - 1) + kStep - 1) / kStep;
+  int last_load = -1;
+  bool q_loaded = false, mma_issued = false;
+  // Q, dO and O of the 128 rows come through the last stages of the ring
+  uint8_t* first_tile = smem + G::kFirst * 2 * G::kTile;
+
+  if (warp == kLoadWarp && n) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&q_full, 3 * kRows * D * 2);
+      tma_tile<D>(first_tile, &P.mq, &q_full, h * D, x.q0 + r0);
+      tma_tile<D>(first_tile + kRows * D * 2, &P.mdo, &q_full, h * D, x.q0 + r0);
+      tma_tile<D>(first_tile + 2 * kRows * D * 2, &P.mo, &q_full, h * D, x.q0 + r0);
     }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    if (!half) {
-      Ds[row] = sum;
-      if (r0 + row < x.lq) P.D[static_cast<int64_t>(h) * P.S.Tq + x.q0 + r0 + row] = sum;
+    q_loaded = true;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % NS, row = i * kStep;
+      // the first tiles' stages
+      if (i == G::kFirst && !warp_wait(&q_ready, 0, abort_p, kAtFlagLoad)) break;
+      if (i >= NS && !warp_wait(&kv_empty[s], (i / NS) - 1, abort_p, kAtFlagLoad)) break;
+      uint8_t* st = smem + s * 2 * G::kTile;
+      const bool tail = row + kStep > x.lk;  // dS is 0 there; K must be finite
+      uint64_t* bar = tail ? &aux : &kv_full[s];
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, 2 * G::kTile);
+        tma_tile<D, kStep>(st, &P.mk, bar, kh * D, x.k0 + row);
+        tma_tile<D, kStep>(st + G::kTile, &P.mv, bar, kh * D, x.k0 + row);
+      }
+      if (tail) {
+        __syncwarp();
+        if (!tail_landed(&aux, 0, abort_p)) break;
+        zero_rows<D, kStep>(st, x.lk - row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[s]);
+      }
+      last_load = i;
+    }
+  } else if (warp == kMmaWarp && n) {
+    // As in the forward, a condition is tested before the products that
+    // precede its use, and waited for only if that test failed.
+    auto wait = [&](uint64_t* bar, int phase) {
+      return warp_wait(bar, phase, abort_p, kAtFlagMma);
+    };
+    auto stage = [&](int i) { return smem + (i % NS) * 2 * G::kTile; };
+    auto scores = [&](int i) {  // S and dP of step i into their buffer (one thread)
+      const uint32_t b = (i & 1) * kStep;
+      mma_txyt<D, kStep>(tmem + G::kS + b, tmem + G::kQ, stage(i));
+      mma_txyt<D, kStep>(tmem + G::kDp + b, tmem + G::kDo, stage(i) + G::kTile);
+      umma_commit(&s_full[i & 1]);
+    };
+    bool ok = wait(&q_ready, 0);
+    tc_fence_after();
+    for (int i = 0; i < 2 && i < n && ok; ++i) {
+      ok = wait(&kv_full[i % NS], i / NS);
+      if (!ok) break;
+      mma_issued = true;
+      if (elect_one()) scores(i);
+      __syncwarp();
+    }
+    bool ready = false;
+    for (int i = 0; i < n && ok; ++i) {
+      const bool more = i + 2 < n;
+      ok = (!more || wait(&kv_full[(i + 2) % NS], (i + 2) / NS)) &&
+           (ready || wait(&ds_full[i & 1], i >> 1));
+      if (!ok) break;
+      ready = i + 1 < n && mbar_test(&ds_full[(i + 1) & 1], ((i + 1) >> 1) & 1);
+      ready = __all_sync(0xffffffffu, ready);
+      tc_fence_after();
+      // dQ += dS K: 16 keys in the first 8 of every 16 columns of the buffer
+      if (elect_one()) {
+        mma_tay<D, kStep>(tmem + G::kDq, tmem + G::kDp + (i & 1) * kStep, 16, stage(i), i > 0);
+        umma_commit(&kv_empty[i % NS]);
+        if (more) scores(i + 2);
+      }
+      __syncwarp();
+    }
+    if (ok && elect_one()) umma_commit(&done);
+    __syncwarp();
+  } else if (warp < kComputeWarps) {
+    const int part = warp >> 2, q4 = warp & 3, tid = q4 * 32 + lane, row = r0 + tid;
+    const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
+    const bool in = row < x.lq;
+    const int64_t at = static_cast<int64_t>(h) * P.S.Tq + x.q0 + row;
+    {  // this quarter of the row: Q and dO into TMEM, dO . O
+      constexpr int W = D / 8;  // 32-bit words
+      uint32_t qw[W], gw[W];
+      float sum = 0.0f;
+      if (n) warp_wait(&q_full, 0, abort_p, kAtFlagCompute);  // giving up shows in the next wait
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        // 16-byte piece of the row in its swizzled box
+        const int piece = part * (D / 32) + i;
+        const uint8_t* at16 = first_tile + (piece >> 3) * kBoxBytes + tid * 128 +
+                              (((piece & 7) ^ (tid & 7)) * 16);
+        uint4 a = make_uint4(0, 0, 0, 0), b = a, c = a;
+        if (n) {
+          a = *reinterpret_cast<const uint4*>(at16);
+          b = *reinterpret_cast<const uint4*>(at16 + kRows * D * 2);
+          c = *reinterpret_cast<const uint4*>(at16 + 2 * kRows * D * 2);
+        }
+        qw[4 * i] = a.x, qw[4 * i + 1] = a.y, qw[4 * i + 2] = a.z, qw[4 * i + 3] = a.w;
+        gw[4 * i] = b.x, gw[4 * i + 1] = b.y, gw[4 * i + 2] = b.z, gw[4 * i + 3] = b.w;
+        const uint32_t ow[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t u = gw[4 * i + e], v = ow[e];
+          sum = __fmaf_rn(__uint_as_float(u << 16), __uint_as_float(v << 16), sum);
+          sum = __fmaf_rn(__uint_as_float(u & 0xFFFF0000u), __uint_as_float(v & 0xFFFF0000u), sum);
+        }
+      }
+      if constexpr (W == 16) {
+        tmem_st16(tmem + G::kQ + part * W + lanes, qw);
+        tmem_st16(tmem + G::kDo + part * W + lanes, gw);
+      } else {
+        tmem_st8(tmem + G::kQ + part * W + lanes, qw);
+        tmem_st8(tmem + G::kDo + part * W + lanes, gw);
+      }
+      dsum[part][tid] = sum;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      // the rows are in registers and TMEM: their stages may be refilled
+      if (lane == 0) mbar_arrive(&q_ready);
+    }
+    bar_compute();
+    const float Dr = (dsum[0][tid] + dsum[1][tid]) + (dsum[2][tid] + dsum[3][tid]);
+    if (in && part == 0) P.D[at] = Dr;
+    const float lse2 = in ? P.lse[at] * kLog2e : 0.0f;
+    const int limit = in ? key_limit(P.S, x, row) : 0;
+    const uint64_t c2 = f32x2_pack(P.c, P.c), l2 = f32x2_pack(-lse2, -lse2),
+                   d2 = f32x2_pack(-Dr, -Dr);
+    const int buf = part >> 1;  // the buffer, and so the steps, of this warp
+    const uint32_t S_p = tmem + G::kS + part * 32 + lanes, dP_p = tmem + G::kDp + part * 32 + lanes;
+    bool ok = true;
+    for (int i = buf; i < n; i += 2) {
+      const int lim = limit - i * kStep - (part & 1) * 32;
+      ok = warp_wait(&s_full[buf], i >> 1, abort_p, kAtFlagCompute);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[32];
+      load_quarter(S_p, s);
+      uint64_t p[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        p[e] = ex2_pair<false>(f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, l2));
+      load_quarter(dP_p, s);
+      uint32_t ds[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        ds[e] = f32x2_to_bf16x2(f32x2_mul_rn(
+            p[e], f32x2_add_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), d2)));
+      if (__any_sync(0xffffffffu, lim < 32)) {  // select: what is masked may be infinite or NaN
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          ds[e] &= (2 * e < lim ? 0x0000FFFFu : 0u) | (2 * e + 1 < lim ? 0xFFFF0000u : 0u);
+      }
+      // 16 keys (8 columns) at the start of each 16 columns of the buffer
+      tmem_st8(dP_p, ds);
+      tmem_st8(dP_p + 16, ds + 8);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full[buf]);
+    }
+    if (ok && n) ok = warp_wait(&done, 0, abort_p, kAtFlagCompute);
+    if (ok && part * 32 < D) {
+      tc_fence_after();
+      uint32_t o[32];
+      if (n) {
+        load_quarter(tmem + G::kDq + part * 32 + lanes, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+      }
+      uint4 v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = pack8_scaled(o + 8 * c, P.scale);
+      const int first = r0 + q4 * 32;  // all products are done: the ring stages the rows
+      put_rows<4>(smem + warp * 2048, v,
+                  P.dq + static_cast<int64_t>(x.q0 + first) * P.dqs + h * D + part * 32,
+                  P.dqs * 2, x.lq - first);
     }
   }
+
   __syncthreads();
-  const float c = P.scale * kLog2e;
-  const int rows[2] = {r0 + m0 + g, r0 + m0 + g + 8};
-  float lse2[2], Dr[2];
-  int lim[2];
-#pragma unroll
-  for (int hr = 0; hr < 2; ++hr) {
-    const bool in = rows[hr] < x.lq;
-    lse2[hr] = in ? P.lse[static_cast<int64_t>(h) * P.S.Tq + x.q0 + rows[hr]] * kLog2e : 0.0f;
-    Dr[hr] = Ds[m0 + g + 8 * hr];
-    lim[hr] = in ? key_limit(P.S, x, rows[hr]) : 0;
+  if (*abort_p && warp == kLoadWarp && lane == 0) {
+    volatile int never = 0;
+    if (q_loaded) mbar_wait(&q_full, 0, &never, &g_attn_flags, kAtFlagDrain);
+    for (int i = max(0, last_load - NS + 1); i <= last_load; ++i)
+      if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
   }
-  float acc[D / 8][4];
-  zero<D>(acc);
-  for (int kt = 0; kt < tiles; ++kt) {
-    const uint16_t* Ks = KVs + ((kt & 1) * 2) * kEl;
-    if (kt + 1 < tiles) {
-      uint16_t* Kn = KVs + (((kt + 1) & 1) * 2) * kEl;
-      load_rows<D>(Kn, k, (kt + 1) * kTile, x.lk, P.ks);
-      load_rows<D>(Kn + kEl, v, (kt + 1) * kTile, x.lk, P.vs);
+  if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
+    volatile int never = 0;
+    umma_commit(&drain);
+    mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dK, dV of 128 keys of one KV head, over one share of the group's query
+// heads and, in each, the query tiles that see the keys, in order.  The
+// scores are computed transposed (a thread owns a key row, 64 of the tile's
+// 128 queries), so that P^T and dS^T, written as bf16 over the scores they
+// came from, are the tensor-memory operands of dV += P^T dO and dK += dS^T Q.
+// TMEM: S^T, dP^T (128 columns each), dV, dK (D each).  While the threads
+// compute P^T the tensor cores run the tile before's dK product and this
+// tile's dP^T; while they compute dS^T, dV and the next S^T.
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_constant__ BwdTc P) {
+  using G = BwdGeo<D>;
+  constexpr int NA = G::kA, NB = G::kB;  // Q, dO
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t kv_full, q_full[NA], ld_full[2], q_empty[NA], do_full[NB], do_empty[NB], aux,
+      s_full, dp_full, p_full, ds_full, done, drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ __align__(16) float nlse[2][kRows], nD[2][kRows];  // -lse log2(e), -D
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = P.KV * P.splits;
+  if (warp == 0 && lane == 0) prefetch_maps(P);
+  pdl_wait_then_release();
+  // (before anything is set up: the grid covers the most tiles there could be)
+  PackedTile x;
+  if (!find_tile(P.S, true, blockIdx.x / per, kRows, x)) return;
+  if (threadIdx.x == 0) {
+    mbar_init(&kv_full, 1);
+    mbar_init(&aux, 1);
+    mbar_init(&drain, 1);
+    for (int i = 0; i < NA; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
     }
-    cp_async_commit();
-    cp_async_wait<1>();
-    __syncthreads();
-    float s[8][4], dp[8][4];
-    gemm_xyt<D>(s, Qs, m0, Ks);
-    gemm_xyt<D>(dp, dOs, m0, Ks + kEl);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int i = 0; i < 2; ++i) mbar_init(&ld_full[i], 32);
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&do_full[i], 1);
+      mbar_init(&do_empty[i], 1);
+    }
+    mbar_init(&s_full, 1);
+    mbar_init(&dp_full, 1);
+    mbar_init(&done, 1);
+    mbar_init(&p_full, kComputeWarps);
+    mbar_init(&ds_full, kComputeWarps);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
+  volatile int* abort_p = &abort_flag;
+  // the swizzled tiles need the alignment asked for
+  if ((smem_u32(smem) & 1023u) || tmem_slot != tmem) {
+    if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
+    if (warp == kMmaWarp) tmem_dealloc(tmem_slot, 512);
+    return;
+  }
+
+  const int share = blockIdx.x % per;
+  const int kh = share / P.splits, split = share % P.splits;
+  const int grp = P.H / P.KV;
+  const int h0 = kh * grp + grp * split / P.splits, h1 = kh * grp + grp * (split + 1) / P.splits;
+  const int c0 = x.t * kRows;
+  // the first query that sees the tile's first key, and so the first tile
+  const int qt0 = (P.S.causal ? max(c0 - (x.lk - x.lq), 0) : 0) / kRows;
+  const int per_head = max((x.lq + kRows - 1) / kRows - qt0, 0);
+  const int n = per_head * (h1 - h0);
+  int last_a = -1, last_b = -1;
+  bool kv_loaded = false, mma_issued = false;
+  uint8_t* ring = smem + 2 * G::kTile;
+
+  if (warp == kLoadWarp && n) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&kv_full, 2 * G::kTile);
+      tma_tile<D>(smem, &P.mk, &kv_full, kh * D, x.k0 + c0);
+      tma_tile<D>(smem + G::kTile, &P.mv, &kv_full, kh * D, x.k0 + c0);
+    }
+    kv_loaded = true;
+    int h = h0, qt = qt0, tails = 0;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % NA, v = i % NB, row = qt * kRows;
+      const bool tail = row + kRows > x.lq;  // P, dS are 0 there; Q, dO must be finite
+      auto load = [&](uint8_t* st, const CUtensorMap* map, uint64_t* full) {
+        uint64_t* bar = tail ? &aux : full;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, G::kTile);
+          tma_tile<D>(st, map, bar, h * D, x.q0 + row);
+        }
+      };
+      auto patch = [&](uint8_t* st, uint64_t* full) {
+        if (!tail) return true;
+        __syncwarp();
+        if (!tail_landed(&aux, tails & 1, abort_p)) return false;
+        ++tails;
+        zero_rows<D>(st, x.lq - row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+        return true;
+      };
+      if (i >= NA && !warp_wait(&q_empty[s], (i / NA) - 1, abort_p, kAtFlagLoad)) break;
+      load(ring + s * G::kTile, &P.mq, &q_full[s]);
+      float a[4], b[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int hr = e >> 1, key = kt * kTile + j * 8 + 2 * qd + (e & 1);
-        const float p = key < lim[hr] ? exp2f(s[j][e] * c - lse2[hr]) : 0.0f;
-        s[j][e] = key < lim[hr] ? p * (dp[j][e] - Dr[hr]) : 0.0f;
+        const int j = lane + 32 * e;
+        const int64_t at = static_cast<int64_t>(h) * P.S.Tq + x.q0 + row + j;
+        a[e] = row + j < x.lq ? P.lse[at] * -kLog2e : 0.0f;
+        b[e] = row + j < x.lq ? -P.D[at] : 0.0f;
       }
-    gemm_py<D>(acc, s, Ks);
-    __syncthreads();
-  }
+      // their slot was last read for tile i - 2, before its dK product
+      if (i >= 2 && !warp_wait(&q_empty[(i - 2) % NA], (i - 2) / NA, abort_p, kAtFlagLoad)) {
+        last_a = i;
+        break;
+      }
 #pragma unroll
-  for (int hr = 0; hr < 2; ++hr) {
-    if (rows[hr] >= x.lq) continue;
-    uint16_t* dst = P.dq + (x.q0 + rows[hr]) * P.dqs + h * D;
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-      *reinterpret_cast<uint32_t*>(dst + n * 8 + 2 * qd) =
-          pack_bf16(acc[n][2 * hr] * P.scale, acc[n][2 * hr + 1] * P.scale);
-  }
-}
-
-// ---------------------------------------------------------------- dK, dV
-// A CTA takes one key tile, one KV head and one share of the group's query
-// heads, which it adds in order; with several shares the fp32 sums go to
-// `part` and packed_kv_reduce adds the shares in order.
-template <int D>
-__global__ void __launch_bounds__(128) packed_dkdv_kernel(const __grid_constant__ PackedArgs P) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kEl = kTile * (D + 8);
-  uint16_t* Ks = reinterpret_cast<uint16_t*>(smem);
-  uint16_t* Vs = Ks + kEl;
-  uint16_t* QD = Vs + kEl;  // Q0 dO0 Q1 dO1
-  float* LD = reinterpret_cast<float*>(QD + 4 * kEl);  // per buffer: lse [64], D [64]
-  const int per = P.KV * P.splits;
-  const int kh = blockIdx.x % per / P.splits, split = blockIdx.x % per % P.splits;
-  PackedTile x;
-  if (!find_tile(P.S, true, blockIdx.x / per, kTile, x)) return;
-  const int G = P.H / P.KV;
-  const int h0 = kh * G + G * split / P.splits, h1 = kh * G + G * (split + 1) / P.splits;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, qd = lane & 3;
-  const int m0 = warp * 16, c0 = x.t * kTile;
-  // the first query that sees the tile's first key, and so the first query tile
-  const int first = P.S.causal ? max(c0 - (x.lk - x.lq), 0) : 0;
-  const int qt0 = first / kTile, qt1 = (x.lq + kTile - 1) / kTile;
-  const int per_head = max(qt1 - qt0, 0), n = per_head * (h1 - h0);
-  auto stage = [&](int i, int b) {
-    const int h = h0 + i / per_head, qt = qt0 + i % per_head;
-    uint16_t* q = QD + (b * 2) * kEl;
-    load_rows<D>(q, P.q + x.q0 * P.qs + h * D, qt * kTile, x.lq, P.qs);
-    load_rows<D>(q + kEl, P.dout + x.q0 * P.dos + h * D, qt * kTile, x.lq, P.dos);
-    for (int j = threadIdx.x; j < kTile; j += blockDim.x) {
-      const int row = qt * kTile + j;
-      const int64_t at = static_cast<int64_t>(h) * P.S.Tq + x.q0 + row;
-      LD[b * 128 + j] = row < x.lq ? P.lse[at] * kLog2e : 0.0f;
-      LD[b * 128 + 64 + j] = row < x.lq ? P.D[at] : 0.0f;
+      for (int e = 0; e < 4; ++e) {
+        nlse[i & 1][lane + 32 * e] = a[e];
+        nD[i & 1][lane + 32 * e] = b[e];
+      }
+      mbar_arrive(&ld_full[i & 1]);
+      if (!patch(ring + s * G::kTile, &q_full[s])) break;
+      last_a = i;
+      if (i >= NB && !warp_wait(&do_empty[v], (i / NB) - 1, abort_p, kAtFlagLoad)) break;
+      load(ring + (NA + v) * G::kTile, &P.mdo, &do_full[v]);
+      if (!patch(ring + (NA + v) * G::kTile, &do_full[v])) break;
+      last_b = i;
+      if (++qt == qt0 + per_head) {
+        qt = qt0;
+        ++h;
+      }
     }
-  };
-  load_rows<D>(Ks, P.k + x.k0 * P.ks + kh * D, c0, x.lk, P.ks);
-  load_rows<D>(Vs, P.v + x.k0 * P.vs + kh * D, c0, x.lk, P.vs);
-  if (n) stage(0, 0);
-  cp_async_commit();
-  const float c = P.scale * kLog2e;
-  const int keys[2] = {c0 + m0 + g, c0 + m0 + g + 8};
-  float dk[D / 8][4], dv[D / 8][4];
-  zero<D>(dk);
-  zero<D>(dv);
-  for (int i = 0; i < n; ++i) {
-    const int b = i & 1, qt = qt0 + i % per_head;
-    const uint16_t* Qs = QD + (b * 2) * kEl;
-    const uint16_t* dOs = Qs + kEl;
-    const float* lse_s = LD + b * 128;
-    const float* D_s = lse_s + 64;
-    if (i + 1 < n) stage(i + 1, b ^ 1);
-    cp_async_commit();
-    cp_async_wait<1>();
-    __syncthreads();
-    float s[8][4];
-    gemm_xyt<D>(s, Ks, m0, Qs);  // S^T = K Q^T
-    // an entry is on if the key exists and the query, which exists, sees it
-    auto on = [&](int j, int e) {
-      const int key = keys[e >> 1], row = qt * kTile + j * 8 + 2 * qd + (e & 1);
-      return key < x.lk && row < x.lq && (!P.S.causal || key <= row + x.lk - x.lq);
+  } else if (warp == kMmaWarp && n) {
+    // As in the forward, conditions are tested before the products that
+    // precede their use.
+    auto wait = [&](uint64_t* bar, int phase) {
+      return warp_wait(bar, phase, abort_p, kAtFlagMma);
     };
+    auto test = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0;
+    };
+    auto Q = [&](int i) { return ring + (i % NA) * G::kTile; };
+    auto dO = [&](int i) { return ring + (NA + i % NB) * G::kTile; };
+    auto scores = [&](int i) {  // S^T = K Q^T (one thread)
+      mma_xyt<D>(tmem, smem, Q(i));
+      umma_commit(&s_full);
+    };
+    auto dprobs = [&](int i) {  // dP^T = V dO^T
+      mma_xyt<D>(tmem + 128, smem + G::kTile, dO(i));
+      umma_commit(&dp_full);
+    };
+    bool ok = wait(&kv_full, 0) && wait(&q_full[0], 0) && wait(&do_full[0], 0);
+    if (ok) {
+      mma_issued = true;
+      if (elect_one()) {
+        scores(0);
+        dprobs(0);
+      }
+      __syncwarp();
+    }
+    bool q_in = false;
+    for (int i = 0; i < n && ok; ++i) {
+      const bool more = i + 1 < n;
+      ok = (!more || q_in || wait(&q_full[(i + 1) % NA], (i + 1) / NA)) && wait(&p_full, i);
+      if (!ok) break;
+      const bool do_in = more && test(&do_full[(i + 1) % NB], (i + 1) / NB);
+      tc_fence_after();
+      if (elect_one()) {
+        mma_ay<D, 32>(tmem + 256, tmem, 32, dO(i), i > 0);  // dV += P^T dO
+        umma_commit(&do_empty[i % NB]);
+        if (more) scores(i + 1);
+      }
+      __syncwarp();
+      ok = (!more || do_in || wait(&do_full[(i + 1) % NB], (i + 1) / NB)) && wait(&ds_full, i);
+      if (!ok) break;
+      q_in = i + 2 < n && test(&q_full[(i + 2) % NA], (i + 2) / NA);
+      tc_fence_after();
+      if (elect_one()) {
+        mma_ay<D, 32>(tmem + 256 + D, tmem + 128, 32, Q(i), i > 0);  // dK += dS^T Q
+        umma_commit(&q_empty[i % NA]);
+        if (more) dprobs(i + 1);
+      }
+      __syncwarp();
+    }
+    if (ok && elect_one()) umma_commit(&done);
+    __syncwarp();
+  } else if (warp < kComputeWarps) {
+    const int part = warp >> 2, q4 = warp & 3, key = c0 + q4 * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t S_p = tmem + part * 32 + lanes, dP_p = S_p + 128;
+    const bool in = key < x.lk;
+    // query rows of the sequence that see this key: [first, lq)
+    const int first = in ? (P.S.causal ? max(key - (x.lk - x.lq), 0) : 0) : x.lq;
+    const uint64_t c2 = f32x2_pack(P.c, P.c);
+    bool ok = true;
+    int qt = qt0;
+    for (int i = 0; i < n; ++i) {
+      const int s = i & 1;
+      // bit b of keep: query b of this thread's 32 sees the key
+      const int lo = first - qt * kRows - part * 32, hi = x.lq - qt * kRows - part * 32;
+      const uint32_t keep = (hi >= 32 ? ~0u : hi > 0 ? (1u << hi) - 1 : 0u) &
+                            (lo <= 0 ? ~0u : lo < 32 ? ~0u << lo : 0u);
+      const bool mask = __any_sync(0xffffffffu, keep != ~0u);
+      if (++qt == qt0 + per_head) qt = qt0;
+      ok = warp_wait(&ld_full[s], i >> 1, abort_p, kAtFlagCompute) &&
+           warp_wait(&s_full, i, abort_p, kAtFlagCompute);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t v[32];
+      load_quarter(S_p, v);
+      uint64_t p[16];
+      uint32_t w[16];
+      const ulonglong2* ls = reinterpret_cast<const ulonglong2*>(nlse[s] + part * 32);
+      auto drop = [&] {  // select: what is masked may be infinite or NaN
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+        for (int e = 0; e < 16; ++e)
+          w[e] &= ((keep >> (2 * e)) & 1 ? 0x0000FFFFu : 0u) |
+                  ((keep >> (2 * e)) & 2 ? 0xFFFF0000u : 0u);
+      };
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        s[j][e] = on(j, e) ? exp2f(s[j][e] * c - lse_s[j * 8 + 2 * qd + (e & 1)]) : 0.0f;
-    gemm_py<D>(dv, s, dOs);  // dV += P^T dO
-    float dp[8][4];
-    gemm_xyt<D>(dp, Vs, m0, dOs);  // dP^T = V dO^T
+      for (int e = 0; e < 16; e += 2) {
+        const ulonglong2 l4 = ls[e / 2];
+        const uint64_t y0 = f32x2_fma_rn(f32x2_pack_bits(v[2 * e], v[2 * e + 1]), c2, l4.x);
+        const uint64_t y1 = f32x2_fma_rn(f32x2_pack_bits(v[2 * e + 2], v[2 * e + 3]), c2, l4.y);
+        p[e] = e % kPolyOf < kPolyPart ? ex2_pair<true>(y0) : ex2_pair<false>(y0);
+        p[e + 1] = (e + 1) % kPolyOf < kPolyPart ? ex2_pair<true>(y1) : ex2_pair<false>(y1);
+        w[e] = f32x2_to_bf16x2(p[e]);
+        w[e + 1] = f32x2_to_bf16x2(p[e + 1]);
+      }
+      if (mask) drop();
+      tmem_st16(S_p, w);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full);
+      ok = warp_wait(&dp_full, i, abort_p, kAtFlagCompute);
+      if (!ok) break;
+      tc_fence_after();
+      load_quarter(dP_p, v);
+      const ulonglong2* ds = reinterpret_cast<const ulonglong2*>(nD[s] + part * 32);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        s[j][e] = on(j, e) ? s[j][e] * (dp[j][e] - D_s[j * 8 + 2 * qd + (e & 1)]) : 0.0f;
-    gemm_py<D>(dk, s, Qs);  // dK += dS^T Q
-    __syncthreads();
-  }
-#pragma unroll
-  for (int hr = 0; hr < 2; ++hr) {
-    if (keys[hr] >= x.lk) continue;
-    const int64_t tok = x.k0 + keys[hr];
-    if (P.splits > 1) {
+      for (int e = 0; e < 8; ++e) {
+        const ulonglong2 d4 = ds[e];
+        w[2 * e] = f32x2_to_bf16x2(f32x2_mul_rn(
+            p[2 * e], f32x2_add_rn(f32x2_pack_bits(v[4 * e], v[4 * e + 1]), d4.x)));
+        w[2 * e + 1] = f32x2_to_bf16x2(f32x2_mul_rn(
+            p[2 * e + 1], f32x2_add_rn(f32x2_pack_bits(v[4 * e + 2], v[4 * e + 3]), d4.y)));
+      }
+      if (mask) drop();
+      tmem_st16(dP_p, w);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full);
+    }
+    if (ok && n) ok = warp_wait(&done, 0, abort_p, kAtFlagCompute);
+    if (ok) {
+      tc_fence_after();
+      // eight warps write dV, eight dK, half of the columns each
+      const int which = part >> 1, col = (part & 1) * (D / 2);  // 1: dK
+      const uint32_t src = tmem + 256 + which * D + col + lanes;
+      const int first = c0 + q4 * 32;  // all products are done: the ring stages the rows
+      const int64_t tok = x.k0 + first;
       const int64_t one = static_cast<int64_t>(P.S.Tk) * P.KV * D;
-      float* pk = P.part + 2 * split * one + (tok * P.KV + kh) * D;
+      uint8_t* stage = ring + warp * 4096;
+      uint4 v[D / 16];
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        *reinterpret_cast<float2*>(pk + n * 8 + 2 * qd) =
-            make_float2(dk[n][2 * hr], dk[n][2 * hr + 1]);
-        *reinterpret_cast<float2*>(pk + one + n * 8 + 2 * qd) =
-            make_float2(dv[n][2 * hr], dv[n][2 * hr + 1]);
+      for (int b = 0; b < D / 64; ++b) {
+        uint32_t o[32];
+        if (n) {
+          load_quarter(src + 32 * b, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (P.splits > 1) {
+          uint4 u[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            u[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          put_rows<8>(stage, u,
+                      P.part + (2 * split + 1 - which) * one + (tok * P.KV + kh) * D + col + 32 * b,
+                      static_cast<int64_t>(P.KV) * D * 4, x.lk - first);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            v[4 * b + c] = pack8_scaled(o + 8 * c, which ? P.scale : 1.0f);
+        }
       }
-    } else {
-      uint16_t* pk = P.dk + tok * P.dks + kh * D;
-      uint16_t* pv = P.dv + tok * P.dvs + kh * D;
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        *reinterpret_cast<uint32_t*>(pk + n * 8 + 2 * qd) =
-            pack_bf16(dk[n][2 * hr] * P.scale, dk[n][2 * hr + 1] * P.scale);
-        *reinterpret_cast<uint32_t*>(pv + n * 8 + 2 * qd) =
-            pack_bf16(dv[n][2 * hr], dv[n][2 * hr + 1]);
+      if (P.splits == 1) {
+        const int64_t pitch = which ? P.dks : P.dvs;
+        put_rows<D / 16>(stage, v, (which ? P.dk : P.dv) + tok * pitch + kh * D + col, pitch * 2,
+                         x.lk - first);
       }
     }
   }
+
+  __syncthreads();
+  if (*abort_p && warp == kLoadWarp && lane == 0) {
+    volatile int never = 0;
+    if (kv_loaded) mbar_wait(&kv_full, 0, &never, &g_attn_flags, kAtFlagDrain);
+    for (int i = max(0, last_a - NA + 1); i <= last_a; ++i)
+      if (!mbar_wait(&q_full[i % NA], (i / NA) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+    for (int i = max(0, last_b - NB + 1); i <= last_b; ++i)
+      if (!mbar_wait(&do_full[i % NB], (i / NB) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+  }
+  if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
+    volatile int never = 0;
+    umma_commit(&drain);
+    mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
-// dK, dV of every token that belongs to a sequence, the shares added in order
+// dK, dV of every token that belongs to a sequence (those between the first
+// length and the last), the shares added in order: eight elements a thread
 template <int D>
-__global__ void __launch_bounds__(256) packed_kv_reduce_kernel(const __grid_constant__ PackedArgs P) {
-  PackedTile x;
-  if (!find_tile(P.S, true, blockIdx.x, kTile, x)) return;
-  const int rows = min(kTile, x.lk - x.t * kTile);
+__global__ void __launch_bounds__(256) packed_kv_reduce(const __grid_constant__ BwdTc P) {
+  pdl_wait_then_release();
+  const int t0 = min(max(__ldg(P.S.cu_k), 0), P.S.Tk);
+  const int t1 = min(__ldg(P.S.cu_k + P.S.n_seq), P.S.Tk);
+  const int row8 = P.KV * (D / 8);
   const int64_t one = static_cast<int64_t>(P.S.Tk) * P.KV * D;
-  const int per_row = P.KV * (D / 4);
-  for (int i = threadIdx.x; i < rows * per_row; i += 256) {
-    const int64_t tok = x.k0 + x.t * kTile + i / per_row;
-    const int e = (i % per_row) * 4;  // element of the token's KV * D
+  const int64_t items = static_cast<int64_t>(max(t1 - t0, 0)) * row8;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < items;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t tok = t0 + i / row8;
+    const int e = static_cast<int>(i % row8) * 8;  // element of the token's KV * D
     const float* p = P.part + tok * P.KV * D + e;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    float a[8] = {}, b[8] = {};
     for (int s = 0; s < P.splits; ++s) {
-      const float4 y = *reinterpret_cast<const float4*>(p + 2 * s * one);
-      const float4 z = *reinterpret_cast<const float4*>(p + (2 * s + 1) * one);
-      a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
-      b.x += z.x, b.y += z.y, b.z += z.z, b.w += z.w;
+      const float4* y = reinterpret_cast<const float4*>(p + 2 * s * one);
+      const float4* z = reinterpret_cast<const float4*>(p + (2 * s + 1) * one);
+      const float4 y0 = y[0], y1 = y[1], z0 = z[0], z1 = z[1];
+      a[0] += y0.x, a[1] += y0.y, a[2] += y0.z, a[3] += y0.w;
+      a[4] += y1.x, a[5] += y1.y, a[6] += y1.z, a[7] += y1.w;
+      b[0] += z0.x, b[1] += z0.y, b[2] += z0.z, b[3] += z0.w;
+      b[4] += z1.x, b[5] += z1.y, b[6] += z1.z, b[7] += z1.w;
     }
-    *reinterpret_cast<uint2*>(P.dk + tok * P.dks + e) = make_uint2(
-        pack_bf16(a.x * P.scale, a.y * P.scale), pack_bf16(a.z * P.scale, a.w * P.scale));
-    *reinterpret_cast<uint2*>(P.dv + tok * P.dvs + e) =
-        make_uint2(pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+    uint32_t u[4], v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u[j] = f32x2_to_bf16x2(f32x2_pack(a[2 * j] * P.scale, a[2 * j + 1] * P.scale));
+      v[j] = f32x2_to_bf16x2(f32x2_pack(b[2 * j], b[2 * j + 1]));
+    }
+    *reinterpret_cast<uint4*>(P.dk + tok * P.dks + e) = make_uint4(u[0], u[1], u[2], u[3]);
+    *reinterpret_cast<uint4*>(P.dv + tok * P.dvs + e) = make_uint4(v[0], v[1], v[2], v[3]);
   }
-}
-
-int sm_count() {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
-// the most tiles of `rows` tokens that n_seq sequences of T tokens can have
-int64_t most_tiles(int64_t T, int n_seq, int rows) { return T / rows + std::min<int64_t>(n_seq, T); }
-
-// shares of a KV group's query heads: enough CTAs for two per SM
-int head_splits(int64_t Tk, int H, int KV) {
-  const int64_t tiles = (Tk + kTile - 1) / kTile * KV;
-  const int64_t want = (2 * sm_count() + tiles - 1) / tiles;
-  return static_cast<int>(std::min<int64_t>(H / KV, std::max<int64_t>(want, 1)));
 }
 
 // Raise a kernel's dynamic shared memory limit, once per device.
@@ -517,103 +1122,136 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
   return e;
 }
 
-PackedArgs args_of(const hsnf4_packed_attention& a) {
-  PackedArgs P{};
-  P.q = static_cast<const uint16_t*>(a.q);
-  P.k = static_cast<const uint16_t*>(a.k);
-  P.v = static_cast<const uint16_t*>(a.v);
-  P.qs = a.q_stride;
-  P.ks = a.k_stride;
-  P.vs = a.v_stride;
-  P.S.cu_q = a.cu_q;
-  P.S.cu_k = a.cu_k;
-  P.S.Tq = static_cast<int>(a.Tq);
-  P.S.Tk = static_cast<int>(a.Tk);
-  P.S.n_seq = a.n_seq;
-  P.H = a.H;
-  P.KV = a.KV;
-  P.S.causal = a.causal;
-  P.scale = a.scale;
-  P.splits = 1;
-  return P;
+bool map_rows(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t stride,
+              int box = kRows) {
+  return encode_tma_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, cols, rows, stride * 2, 64, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D>
-cudaError_t fwd(const PackedArgs& P, cudaStream_t st) {
+int64_t most_tiles(int64_t T, int n_seq, int rows) { return T / rows + std::min<int64_t>(n_seq, T); }
+
+template <int D, int NQ>
+cudaError_t fwd_tc(const FwdTc& P, cudaStream_t st) {
+  using G = FwdGeo<D, NQ>;
   static std::atomic<uint64_t> done{0};
-  const int smem = 5 * kTile * (D + 8) * 2;
-  cudaError_t e = allow_smem(packed_fwd_kernel<D>, smem, done);
+  const cudaError_t e = allow_smem(packed_fwd_tc<D, NQ>, G::kSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = most_tiles(P.S.Tq, P.S.n_seq, kTile) * P.H;
-  count_launch();
-  packed_fwd_kernel<D><<<static_cast<unsigned>(grid), 128, smem, st>>>(P);
-  return cudaGetLastError();
+  const int64_t grid = most_tiles(P.S.Tq, P.S.n_seq, NQ * kRows) * P.H;
+  return launch_pdl(packed_fwd_tc<D, NQ>, dim3(static_cast<unsigned>(grid)), dim3(G::kThreads),
+                    G::kSmem, st, P);
+}
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+// shares of a KV group's query heads, so that there are CTAs for every SM
+int head_splits(int64_t Tk, int H, int KV) {
+  const int64_t tiles = (Tk + kRows - 1) / kRows * KV;
+  const int64_t want = (sm_count() + tiles - 1) / tiles;
+  return static_cast<int>(std::min<int64_t>(H / KV, std::max<int64_t>(want, 1)));
 }
 
 template <int D>
-cudaError_t bwd(const PackedArgs& P, cudaStream_t st) {
+cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws,
+                   cudaStream_t st) {
   static std::atomic<uint64_t> done_q{0}, done_kv{0};
-  const int el = kTile * (D + 8) * 2;
-  const int smem_q = 7 * el, smem_kv = 6 * el + 2 * 2 * 64 * 4;
-  cudaError_t e = allow_smem(packed_dq_kernel<D>, smem_q, done_q);
-  if (e == cudaSuccess) e = allow_smem(packed_dkdv_kernel<D>, smem_kv, done_kv);
-  if (e != cudaSuccess) return e;
-  const int64_t kt = most_tiles(P.S.Tk, P.S.n_seq, kTile);
-  count_launch();
-  packed_dq_kernel<D><<<static_cast<unsigned>(most_tiles(P.S.Tq, P.S.n_seq, kTile) * P.H), 128, smem_q,
-                        st>>>(P);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  count_launch();
-  packed_dkdv_kernel<D><<<static_cast<unsigned>(kt * P.KV * P.splits), 128, smem_kv, st>>>(P);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || P.splits == 1) return e;
-  count_launch();
-  packed_kv_reduce_kernel<D><<<static_cast<unsigned>(kt), 256, 0, st>>>(P);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
-// D [H, Tq] fp32, then the shares' fp32 dK, dV
-size_t packed_workspace_bytes(int64_t Tq, int64_t Tk, int n_seq, int H, int KV, int d) {
-  if (!getenv("HX")) return packed_tc_workspace_bytes(Tq, Tk, n_seq, H, KV, d);
-  const int splits = head_splits(Tk, H, KV);
-  size_t n = round_up(static_cast<size_t>(H) * Tq * 4, 256);
-  if (splits > 1) n += static_cast<size_t>(splits) * 2 * Tk * KV * d * 4;
-  return n;
-}
-
-cudaError_t launch_packed_fwd(const hsnf4_packed_attention& a, void* o, int64_t o_stride,
-                              float* lse, cudaStream_t st) {
-  if (!getenv("HX")) return launch_packed_fwd_tc(a, o, o_stride, lse, st);
-  PackedArgs P = args_of(a);
-  P.out = static_cast<uint16_t*>(o);
-  P.os = o_stride;
-  P.lse = lse;
-  return a.head_dim == 128 ? fwd<128>(P, st) : fwd<64>(P, st);
-}
-
-cudaError_t launch_packed_bwd(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws,
-                              cudaStream_t st) {
-  if (!getenv("HX")) return launch_packed_bwd_tc(a, b, ws, st);
-  PackedArgs P = args_of(a);
-  P.o = static_cast<const uint16_t*>(b.o);
-  P.os = b.o_stride;
-  P.lse = const_cast<float*>(b.lse);
-  P.dout = static_cast<const uint16_t*>(b.dout);
-  P.dos = b.do_stride;
+  BwdTc P;
+  memset(&P, 0, sizeof P);
+  const int64_t wq = static_cast<int64_t>(a.H) * D, wk = static_cast<int64_t>(a.KV) * D;
+  if (!map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride, kStep) ||
+      !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride, kStep) ||
+      !map_rows(&P.mq, a.q, wq, a.Tq, a.q_stride) ||
+      !map_rows(&P.mdo, b.dout, wq, a.Tq, b.do_stride) ||
+      !map_rows(&P.mo, b.o, wq, a.Tq, b.o_stride))
+    return cudaErrorInvalidValue;
+  P.lse = b.lse;
+  P.D = static_cast<float*>(ws);
+  P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                    round_up(static_cast<size_t>(a.H) * a.Tq * 4, 256));
   P.dq = static_cast<uint16_t*>(b.dq);
   P.dk = static_cast<uint16_t*>(b.dk);
   P.dv = static_cast<uint16_t*>(b.dv);
   P.dqs = b.dq_stride;
   P.dks = b.dk_stride;
   P.dvs = b.dv_stride;
+  P.S = {a.cu_q, a.cu_k, static_cast<int>(a.Tq), static_cast<int>(a.Tk), a.n_seq, a.causal};
+  P.H = a.H;
+  P.KV = a.KV;
   P.splits = head_splits(a.Tk, a.H, a.KV);
-  P.D = static_cast<float*>(ws);
-  P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
-                                    round_up(static_cast<size_t>(a.H) * a.Tq * 4, 256));
-  return a.head_dim == 128 ? bwd<128>(P, st) : bwd<64>(P, st);
+  P.scale = a.scale;
+  P.c = a.scale * kLog2e;
+  cudaError_t e = allow_smem(packed_dq_tc<D>, DqGeo<D>::kSmem, done_q);
+  if (e == cudaSuccess) e = allow_smem(packed_dkdv_tc<D>, BwdGeo<D>::kSmem, done_kv);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(packed_dq_tc<D>,
+                 dim3(static_cast<unsigned>(most_tiles(a.Tq, a.n_seq, kRows) * a.H)),
+                 dim3(kTcThreads), DqGeo<D>::kSmem, st, P);
+  if (e != cudaSuccess) return e;
+  if (!map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride) || !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride))
+    return cudaErrorInvalidValue;
+  e = launch_pdl(packed_dkdv_tc<D>, dim3(static_cast<unsigned>(most_tiles(a.Tk, a.n_seq, kRows) *
+                                                               a.KV * P.splits)),
+                 dim3(kTcThreads), BwdGeo<D>::kSmem, st, P);
+  if (e != cudaSuccess || P.splits == 1) return e;
+  const int64_t items = a.Tk * a.KV * (D / 8);
+  const int64_t grid = std::min<int64_t>((items + 255) / 256, static_cast<int64_t>(sm_count()) * 8);
+  return launch_pdl(packed_kv_reduce<D>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, P);
+}
+
+}  // namespace
+
+// D [H, Tq] fp32, then the shares' fp32 dK, dV
+size_t packed_workspace_bytes(int64_t Tq, int64_t Tk, int n_seq, int H, int KV, int d) {
+  const int splits = head_splits(Tk, H, KV);
+  size_t n = round_up(static_cast<size_t>(H) * Tq * 4, 256);
+  if (splits > 1) n += static_cast<size_t>(splits) * 2 * Tk * KV * d * 4;
+  return n;
+}
+
+cudaError_t launch_packed_bwd(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws,
+                                 cudaStream_t st) {
+  return a.head_dim == 128 ? bwd_tc<128>(a, b, ws, st) : bwd_tc<64>(a, b, ws, st);
+}
+
+cudaError_t launch_packed_fwd(const hsnf4_packed_attention& a, void* o, int64_t o_stride,
+                                 float* lse, cudaStream_t st) {
+  FwdTc P;
+  memset(&P, 0, sizeof P);
+  const int64_t wq = static_cast<int64_t>(a.H) * a.head_dim,
+                wk = static_cast<int64_t>(a.KV) * a.head_dim;
+  if (!map_rows(&P.mq, a.q, wq, a.Tq, a.q_stride) || !map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride) ||
+      !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride))
+    return cudaErrorInvalidValue;
+  P.out = static_cast<uint16_t*>(o);
+  P.os = o_stride;
+  P.lse = lse;
+  P.S = {a.cu_q, a.cu_k, static_cast<int>(a.Tq), static_cast<int>(a.Tk), a.n_seq, a.causal};
+  P.H = a.H;
+  P.KV = a.KV;
+  P.c = a.scale * kLog2e;
+  // One query tile per CTA unless the sequences are long on average.  28/4
+  // heads, head_dim 128, causal, one tile against two: 64 sequences of 64
+  // tokens 49 / 99 us, 16 of 512 70 / 84, one of 4096 117 / 118, one of 8192
+  // 429 / 406, one of 16384 (32/8 heads) 1940 / 1770.
+  const bool two = a.Tq >= 6144 * static_cast<int64_t>(a.n_seq);
+  if (a.head_dim == 128) return two ? fwd_tc<128, 2>(P, st) : fwd_tc<128, 1>(P, st);
+  return two ? fwd_tc<64, 2>(P, st) : fwd_tc<64, 1>(P, st);
+}
+
+cudaError_t read_attn_flags(uint32_t* flags) {
+  unsigned int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_attn_flags, sizeof v);
+  if (e != cudaSuccess) return e;
+  *flags = v;
+  if (v) {
+    const unsigned int z = 0;
+    e = cudaMemcpyToSymbol(g_attn_flags, &z, sizeof z);
+  }
+  return e;
 }
 
 }  // namespace hsnf4

@@ -203,11 +203,6 @@ struct PackedBwd {
 size_t packed_workspace_bytes(int64_t Tq, int64_t Tk, int n_seq, int H, int KV, int d);
 cudaError_t launch_packed_fwd(const hsnf4_packed_attention& a, void* o, int64_t o_stride,
                               float* lse, cudaStream_t st);
-cudaError_t launch_packed_fwd_tc(const hsnf4_packed_attention& a, void* o, int64_t o_stride,
-                                 float* lse, cudaStream_t st);
-size_t packed_tc_workspace_bytes(int64_t Tq, int64_t Tk, int n_seq, int H, int KV, int d);
-cudaError_t launch_packed_bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws,
-                                 cudaStream_t st);
 cudaError_t read_attn_flags(uint32_t* flags);
 cudaError_t launch_packed_bwd(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws,
                               cudaStream_t st);
