@@ -41,7 +41,8 @@ struct Entry {  // one tensor, in the device table
   int64_t n;
   int64_t chunk0;  // its first chunk
   int32_t dtype;
-  int32_t vec;  // g and out are 16-byte aligned
+  int16_t shift;     // elements of g past a 16-byte boundary: chunks start that much before g
+  int16_t same;      // out is as far past one: 16-byte stores
 };
 
 struct NormParams {
@@ -97,7 +98,8 @@ struct Type<HSNF4_F16> {
 };
 
 // The CTA's part [c0, c1) of all chunks, tensor by tensor, in order or from
-// the end: f(entry, first element, elements).
+// the end: f(entry, first element), the first element at a 16-byte boundary
+// (before the tensor's start in its first chunk).
 template <typename F>
 __device__ __forceinline__ void walk(const NormParams& P, int64_t c0, int64_t c1, bool back, F f) {
   __shared__ int found;
@@ -119,82 +121,88 @@ __device__ __forceinline__ void walk(const NormParams& P, int64_t c0, int64_t c1
     } else {
       while (e + 1 < P.n && P.table[e + 1].chunk0 <= c) x = P.table[++e];
     }
-    const int ce = chunk_elems(x.dtype);
-    const int64_t at = (c - x.chunk0) * ce;
-    const int64_t left = x.n - at;
-    f(x, at, static_cast<int>(left < ce ? left : ce));
+    f(x, (c - x.chunk0) * chunk_elems(x.dtype) - x.shift);
   }
 }
 
 // sum of squares of a chunk, this thread's share
 template <int DT>
-__device__ __forceinline__ double squares(const Entry& x, int64_t at, int m) {
+__device__ __forceinline__ double squares(const Entry& x, int64_t at) {
   using Ty = Type<DT>;
   using S = typename Ty::S;
-  constexpr int V = Ty::kVec;
-  const S* g = static_cast<const S*>(x.g) + at;
+  constexpr int V = Ty::kVec, kLoads = kChunkBytes / 16 / kThreads;
+  const S* g = static_cast<const S*>(x.g);
   double sum = 0.0;
-  const int vecs = x.vec ? m / V : 0;
-  constexpr int kLoads = kChunkBytes / 16 / kThreads;
   uint4 v[kLoads];
+  const bool whole = at >= 0 && at + kLoads * kThreads * V <= x.n;
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const int i = threadIdx.x + j * kThreads;
-    v[j] = i < vecs ? __ldg(reinterpret_cast<const uint4*>(g) + i) : make_uint4(0, 0, 0, 0);
+    const int64_t e0 = at + (threadIdx.x + j * kThreads) * V;
+    if (whole || (e0 >= 0 && e0 + V <= x.n)) v[j] = __ldg(reinterpret_cast<const uint4*>(g + e0));
   }
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    if (threadIdx.x + j * kThreads >= vecs) break;
-    const S* e = reinterpret_cast<const S*>(&v[j]);
-    float s = 0.0f;
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-      const float f = Ty::up(e[q]);
-      s = __fmaf_rn(f, f, s);
-    }
-    if (s > 1e-30f && s < 1e38f) {
-      sum += s;
-    } else {
+    const int64_t e0 = at + (threadIdx.x + j * kThreads) * V;
+    if (whole || (e0 >= 0 && e0 + V <= x.n)) {
+      const S* e = reinterpret_cast<const S*>(&v[j]);
+      float s = 0.0f;
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        const double f = Ty::up(e[q]);
-        sum += f * f;
+        const float f = Ty::up(e[q]);
+        s = __fmaf_rn(f, f, s);
       }
+      if (s > 1e-30f && s < 1e38f) {
+        sum += s;
+      } else {
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          const double f = Ty::up(e[q]);
+          sum += f * f;
+        }
+      }
+    } else {  // the tensor's ends
+      for (int q = 0; q < V; ++q)
+        if (e0 + q >= 0 && e0 + q < x.n) {
+          const double f = Ty::up(g[e0 + q]);
+          sum += f * f;
+        }
     }
-  }
-  for (int i = vecs * V + threadIdx.x; i < m; i += kThreads) {
-    const double f = Ty::up(g[i]);
-    sum += f * f;
   }
   return sum;
 }
 
 template <int DT>
-__device__ __forceinline__ void scale_chunk(const Entry& x, int64_t at, int m, float coef) {
+__device__ __forceinline__ void scale_chunk(const Entry& x, int64_t at, float coef) {
   using Ty = Type<DT>;
   using S = typename Ty::S;
-  constexpr int V = Ty::kVec;
-  const S* g = static_cast<const S*>(x.g) + at;
-  S* out = static_cast<S*>(x.out) + at;
-  const int vecs = x.vec ? m / V : 0;
-  constexpr int kLoads = kChunkBytes / 16 / kThreads;
+  constexpr int V = Ty::kVec, kLoads = kChunkBytes / 16 / kThreads;
+  const S* g = static_cast<const S*>(x.g);
+  S* out = static_cast<S*>(x.out);
   uint4 v[kLoads];
+  const bool whole = at >= 0 && at + kLoads * kThreads * V <= x.n;
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const int i = threadIdx.x + j * kThreads;
-    if (i < vecs) v[j] = reinterpret_cast<const uint4*>(g)[i];
+    const int64_t e0 = at + (threadIdx.x + j * kThreads) * V;
+    if (whole || (e0 >= 0 && e0 + V <= x.n)) v[j] = *reinterpret_cast<const uint4*>(g + e0);
   }
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const int i = threadIdx.x + j * kThreads;
-    if (i >= vecs) break;
-    S* e = reinterpret_cast<S*>(&v[j]);
+    const int64_t e0 = at + (threadIdx.x + j * kThreads) * V;
+    if (whole || (e0 >= 0 && e0 + V <= x.n)) {
+      S* e = reinterpret_cast<S*>(&v[j]);
 #pragma unroll
-    for (int q = 0; q < V; ++q) e[q] = Ty::down(__fmul_rn(Ty::up(e[q]), coef));
-    reinterpret_cast<uint4*>(out)[i] = v[j];
+      for (int q = 0; q < V; ++q) e[q] = Ty::down(__fmul_rn(Ty::up(e[q]), coef));
+      if (x.same) {
+        *reinterpret_cast<uint4*>(out + e0) = v[j];
+      } else {
+#pragma unroll
+        for (int q = 0; q < V; ++q) out[e0 + q] = e[q];
+      }
+    } else {
+      for (int q = 0; q < V; ++q)
+        if (e0 + q >= 0 && e0 + q < x.n) out[e0 + q] = Ty::down(__fmul_rn(Ty::up(g[e0 + q]), coef));
+    }
   }
-  for (int i = vecs * V + threadIdx.x; i < m; i += kThreads)
-    out[i] = Ty::down(__fmul_rn(Ty::up(g[i]), coef));
 }
 
 __device__ __forceinline__ void my_range(const NormParams& P, int64_t& c0, int64_t& c1) {
@@ -210,13 +218,13 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const NormParams P)
   my_range(P, c0, c1);
   double sum = 0.0;
   if (c0 < c1)
-    walk(P, c0, c1, false, [&](const Entry& x, int64_t at, int m) {
+    walk(P, c0, c1, false, [&](const Entry& x, int64_t at) {
       if (x.dtype == HSNF4_F32)
-        sum += squares<HSNF4_F32>(x, at, m);
+        sum += squares<HSNF4_F32>(x, at);
       else if (x.dtype == HSNF4_BF16)
-        sum += squares<HSNF4_BF16>(x, at, m);
+        sum += squares<HSNF4_BF16>(x, at);
       else
-        sum += squares<HSNF4_F16>(x, at, m);
+        sum += squares<HSNF4_F16>(x, at);
     });
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) P.partial[blockIdx.x] = sum;
@@ -239,14 +247,14 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const NormParams P
   int64_t c0, c1;
   my_range(P, c0, c1);
   if (c0 < c1)
-    walk(P, c0, c1, true, [&](const Entry& x, int64_t at, int m) {
+    walk(P, c0, c1, true, [&](const Entry& x, int64_t at) {
       if (coef == 1.0f && x.g == x.out) return;  // nothing to clip, in place
       if (x.dtype == HSNF4_F32)
-        scale_chunk<HSNF4_F32>(x, at, m, coef);
+        scale_chunk<HSNF4_F32>(x, at, coef);
       else if (x.dtype == HSNF4_BF16)
-        scale_chunk<HSNF4_BF16>(x, at, m, coef);
+        scale_chunk<HSNF4_BF16>(x, at, coef);
       else
-        scale_chunk<HSNF4_F16>(x, at, m, coef);
+        scale_chunk<HSNF4_F16>(x, at, coef);
     });
 }
 
@@ -273,9 +281,13 @@ cudaError_t fill_grad_table(const hsnf4_grad* grads, int n, void* table, int64_t
   int64_t c = 0;
   for (int i = 0; i < n; ++i) {
     const hsnf4_grad& g = grads[i];
-    const int ce = chunk_elems(g.dtype);
-    e[i] = {g.g, g.out, g.n, c, g.dtype, aligned16(g.g) && aligned16(g.out) ? 1 : 0};
-    c += (g.n + ce - 1) / ce;
+    const int ce = chunk_elems(g.dtype), size = kChunkBytes / ce;
+    const uintptr_t off = reinterpret_cast<uintptr_t>(g.g) & 15u;
+    const int shift = static_cast<int>(off) / size;
+    const bool same = off == (reinterpret_cast<uintptr_t>(g.out) & 15u);
+    e[i] = {g.g, g.out, g.n, c, g.dtype, static_cast<int16_t>(shift),
+            static_cast<int16_t>(same)};
+    if (g.n) c += (g.n + shift + ce - 1) / ce;
   }
   *chunks = c;
   // pageable source: the copy has left it when the call returns

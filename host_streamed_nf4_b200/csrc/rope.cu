@@ -14,10 +14,12 @@
 // sincospif in fp32; the rotation is fp32 and is rounded once to bf16.
 //
 // Bound by memory: 4 bytes per element of q and k.  A CTA takes one token or
-// more (few heads: as many as fill its threads), puts the tokens' cos and sin
-// into shared memory once, and every head reads them from there; a thread's
-// q/k values are in flight while the angles are computed.
+// more (at most 16) and puts the tokens' cos and sin into shared memory once.
+// A thread keeps its place in the head and walks the heads and tokens, its
+// first loads in flight while the angles are computed.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "internal.h"
 
@@ -37,6 +39,9 @@ struct RopeParams {
   int64_t T;
   int H, KV, d, half;
   int tokens;        // per CTA
+  int par;           // of them at once
+  int step;          // heads a token's threads take at once
+  int half_pow2;     // half, rounded up to a power of two
   int per_head;      // 16-byte items of a head: rotation items, then pass-through ones
   int rot_items;
   float scale, sign;
@@ -64,86 +69,103 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }
 
 // in and out may be the same memory (each item's thread reads it whole
-// before it writes), so no read-only loads here
-template <bool HALF>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams P) {
-  extern __shared__ float2 cs[];  // [tokens][half]: {s cos, s sin}
+// before it writes), so no read-only loads of them here
+template <bool HALF, int kBatch>
+__global__ void __launch_bounds__(kThreads, kBatch == 1 ? 5 : 4)
+    rope_kernel(const __grid_constant__ RopeParams P) {
+  extern __shared__ __align__(16) float2 cs[];  // [tokens][half]: {s cos, s sin}
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.tokens;
   const int nt = static_cast<int>(P.T - t0 < P.tokens ? P.T - t0 : P.tokens);
-  const int per_token = (P.H + P.KV) * P.per_head;
-  const int items = nt * per_token;
+  const int heads = P.H + P.KV;
+  // this thread: tokens tok, tok + par, ..., item v of heads h0, h0 + step, ...
+  const int tok = threadIdx.x / (P.step * P.per_head);
+  const int rest = threadIdx.x - tok * P.step * P.per_head;
+  const int h0 = rest / P.per_head, v = rest - h0 * P.per_head;
+  const bool turn = v < P.rot_items;
+  const int e0 = turn ? v * 8 : 2 * P.half + (v - P.rot_items) * 8;  // element inside the head
 
-  struct Item {
-    uint16_t* dst;
-    uint4 a, b;
-    int tok, i;  // i: first pair of a rotation item, or -1: pass-through
-  };
-  auto load = [&](int it) {
-    Item x;
-    x.tok = it / per_token;
-    const int r = it - x.tok * per_token;
-    const int head = r / P.per_head, v = r - head * P.per_head;
-    const int w = head < P.H ? 0 : 1;
-    const int64_t h = w ? head - P.H : head, t = t0 + x.tok;
-    int e;  // first element inside the head
-    if (v < P.rot_items) {
-      x.i = HALF ? v * 8 : v * 4;
-      e = v * 8;
-    } else {
-      x.i = -1;
-      e = 2 * P.half + (v - P.rot_items) * 8;
-    }
-    const uint16_t* src = P.in[w] + t * P.in_stride[w] + h * P.d + e;
-    x.dst = P.out[w] + t * P.out_stride[w] + h * P.d + e;
-    x.a = *reinterpret_cast<const uint4*>(src);
-    if (HALF && x.i >= 0) x.b = *reinterpret_cast<const uint4*>(src + P.half);
-    return x;
-  };
-  auto store = [&](const Item& x) {
-    if (x.i < 0) {
-      *reinterpret_cast<uint4*>(x.dst) = x.a;
-      return;
-    }
-    const float2* c = cs + x.tok * P.half + x.i;
-    float a[8], b[8];
-    unpack8(x.a, a);
-    if (HALF) {
-      unpack8(x.b, b);
+  uint4 a[kBatch], b[kBatch];
+  auto load = [&](int tl, int h1) {
+    const uint16_t* q = P.in[0] + (t0 + tl) * P.in_stride[0] + e0;
+    const uint16_t* k = P.in[1] + (t0 + tl) * P.in_stride[1] + e0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 k = c[e];
-        const float y1 = a[e] * k.x - b[e] * k.y, y2 = b[e] * k.x + a[e] * k.y;
-        a[e] = y1;
-        b[e] = y2;
-      }
-      *reinterpret_cast<uint4*>(x.dst + P.half) = pack8(b);
-    } else {
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = h1 + j * P.step;
+      if (h >= heads) continue;
+      const uint16_t* src = h < P.H ? q + h * P.d : k + (h - P.H) * P.d;
+      a[j] = *reinterpret_cast<const uint4*>(src);
+      if (HALF && turn) b[j] = *reinterpret_cast<const uint4*>(src + P.half);
+    }
+  };
+  const bool any = tok < P.par && tok < nt;
+  if (any) load(tok, h0);
+  {  // this thread's pair i, of tokens tk, tk + stride, ...
+    const int i = threadIdx.x & (P.half_pow2 - 1), stride = blockDim.x / P.half_pow2;
+    if (i < P.half) {
+      const double f = static_cast<double>(P.inv_freq[i]) * 0.31830988618379067154;  // / pi
+      const int32_t* pos = P.pos + static_cast<int64_t>(P.axis[i]) * P.T + t0;
+      for (int tk0 = threadIdx.x / P.half_pow2; tk0 < nt; tk0 += 4 * stride) {
+        int32_t p[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 k = c[e];
-        const float y1 = a[2 * e] * k.x - a[2 * e + 1] * k.y;
-        a[2 * e + 1] = a[2 * e + 1] * k.x + a[2 * e] * k.y;
-        a[2 * e] = y1;
+        for (int j = 0; j < 4; ++j)
+          if (tk0 + j * stride < nt) p[j] = __ldg(pos + tk0 + j * stride);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (tk0 + j * stride >= nt) break;
+          double turns = p[j] * f;
+          turns -= 2.0 * rint(0.5 * turns);
+          float s, c;
+          sincospif(static_cast<float>(turns), &s, &c);
+          cs[(tk0 + j * stride) * P.half + i] = make_float2(P.scale * c, P.sign * P.scale * s);
+        }
       }
     }
-    *reinterpret_cast<uint4*>(x.dst) = pack8(a);
-  };
-
-  Item first;
-  const bool any = static_cast<int>(threadIdx.x) < items;
-  if (any) first = load(threadIdx.x);
-  for (int j = threadIdx.x; j < nt * P.half; j += kThreads) {
-    const int tok = j / P.half, i = j - tok * P.half;
-    const double p = P.pos[static_cast<int64_t>(P.axis[i]) * P.T + t0 + tok];
-    double turn = p * static_cast<double>(P.inv_freq[i]) * 0.31830988618379067154;  // / pi
-    turn -= 2.0 * rint(0.5 * turn);
-    float s, c;
-    sincospif(static_cast<float>(turn), &s, &c);
-    cs[j] = make_float2(P.scale * c, P.sign * P.scale * s);
   }
   __syncthreads();
-  if (any) store(first);
-  for (int it = threadIdx.x + kThreads; it < items; it += kThreads) store(load(it));
+  if (!any) return;
+  for (int tl = tok; tl < nt; tl += P.par) {
+    const float2* c = cs + tl * P.half + (HALF ? v * 8 : v * 4);
+    for (int h1 = h0; h1 < heads; h1 += kBatch * P.step) {
+      if (tl != tok || h1 != h0) load(tl, h1);
+      uint16_t* q = P.out[0] + (t0 + tl) * P.out_stride[0] + e0;
+      uint16_t* k = P.out[1] + (t0 + tl) * P.out_stride[1] + e0;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int h = h1 + j * P.step;
+        if (h >= heads) break;
+        uint16_t* dst = h < P.H ? q + h * P.d : k + (h - P.H) * P.d;
+        if (!turn) {
+          *reinterpret_cast<uint4*>(dst) = a[j];
+          continue;
+        }
+        float x[8];
+        unpack8(a[j], x);
+        if (HALF) {
+          float y[8];
+          unpack8(b[j], y);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float4 w = *reinterpret_cast<const float4*>(c + e);
+            const float y0 = x[e] * w.x - y[e] * w.y, y1 = x[e + 1] * w.z - y[e + 1] * w.w;
+            y[e] = y[e] * w.x + x[e] * w.y;
+            y[e + 1] = y[e + 1] * w.z + x[e + 1] * w.w;
+            x[e] = y0;
+            x[e + 1] = y1;
+          }
+          *reinterpret_cast<uint4*>(dst + P.half) = pack8(y);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 w = c[e];
+            const float y1 = x[2 * e] * w.x - x[2 * e + 1] * w.y;
+            x[2 * e + 1] = x[2 * e + 1] * w.x + x[2 * e] * w.y;
+            x[2 * e] = y1;
+          }
+        }
+        *reinterpret_cast<uint4*>(dst) = pack8(x);
+      }
+    }
+  }
 }
 
 }  // namespace
@@ -174,17 +196,28 @@ cudaError_t launch_rope(const hsnf4_rope& R, const RopeTensors& t, int64_t T, in
     P.inv_freq[i] = R.inv_freq[i];
     P.axis[i] = R.axis[i];
   }
-  const int per_token = (H + KV) * P.per_head;
-  P.tokens = kThreads / per_token;
-  if (P.tokens < 1) P.tokens = 1;
-  if (P.tokens > kMaxTokens) P.tokens = kMaxTokens;
+  // several tokens at once if all their heads fit the threads, else the heads
+  // of one in equal passes; and, in a long sequence, more tokens in turn, so
+  // that each SM gets its CTAs once
+  const int heads = H + KV, per_token = heads * P.per_head;
+  P.par = std::min(std::max(kThreads / per_token, 1), kMaxTokens);
+  const int most = kThreads / P.per_head, passes = (heads + most - 1) / most;
+  P.step = (heads + passes - 1) / passes;
+  int threads = (P.par * P.step * P.per_head + 31) / 32 * 32;
+  for (P.half_pow2 = 8; P.half_pow2 < P.half;) P.half_pow2 *= 2;
+  threads = std::max(threads, P.half_pow2);
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t slots = static_cast<int64_t>(sms) * (passes == 1 ? 5 : 4);
+  const int64_t turns = (T + slots * P.par - 1) / (slots * P.par);
+  P.tokens = P.par * static_cast<int>(std::min<int64_t>(turns, std::max(1, kMaxTokens / P.par)));
   const int64_t grid = (T + P.tokens - 1) / P.tokens;
   const size_t smem = static_cast<size_t>(P.tokens) * P.half * sizeof(float2);
+  const auto kernel = half ? (passes == 1 ? rope_kernel<true, 1> : rope_kernel<true, 2>)
+                           : (passes == 1 ? rope_kernel<false, 1> : rope_kernel<false, 2>);
   count_launch();
-  if (half)
-    rope_kernel<true><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(P);
-  else
-    rope_kernel<false><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(P);
+  kernel<<<static_cast<unsigned>(grid), threads, smem, st>>>(P);
   return cudaGetLastError();
 }
 
