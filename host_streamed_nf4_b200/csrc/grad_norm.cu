@@ -36,13 +36,13 @@ constexpr int kCtasPerSm = 4;
 constexpr double kEps = 1e-6;
 
 struct Entry {  // one tensor, in the device table
-  const void* g;
-  void* out;
-  int64_t n;
+  const uint8_t* g;
+  uint8_t* out;
+  int64_t bytes;
   int64_t chunk0;  // its first chunk
   int32_t dtype;
-  int16_t shift;     // elements of g past a 16-byte boundary: chunks start that much before g
-  int16_t same;      // out is as far past one: 16-byte stores
+  int16_t shift;   // bytes of g past a 16-byte boundary: its chunks start that much before g
+  int16_t same;    // out is as far past one: 16-byte stores
 };
 
 struct NormParams {
@@ -55,10 +55,6 @@ struct NormParams {
   float max_norm;
   int scale;  // second pass: write out (0: the norm only)
 };
-
-__host__ __device__ inline int chunk_elems(int dtype) {
-  return dtype == HSNF4_F32 ? kChunkBytes / 4 : kChunkBytes / 2;
-}
 
 __device__ __forceinline__ double block_sum(double v, double* red) {
 #pragma unroll
@@ -97,53 +93,67 @@ struct Type<HSNF4_F16> {
   static __device__ S down(float x) { return __float2half_rn(x); }
 };
 
-// The CTA's part [c0, c1) of all chunks, tensor by tensor, in order or from
-// the end: f(entry, first element), the first element at a 16-byte boundary
-// (before the tensor's start in its first chunk).
-template <typename F>
-__device__ __forceinline__ void walk(const NormParams& P, int64_t c0, int64_t c1, bool back, F f) {
+// The tensor that holds a chunk (all threads; empty tensors have no chunks
+// and share the next one's first).
+struct Cursor {
+  int e;
+  Entry x;
+};
+
+__device__ __forceinline__ Cursor locate(const NormParams& P, int64_t c) {
   __shared__ int found;
-  // tensors whose first chunk is <= c: the last of them (empty tensors have
-  // no chunks and share the next one's first) holds c
-  const int64_t start = back ? c1 - 1 : c0;
   int count = 0;
-  for (int i = threadIdx.x; i < P.n; i += kThreads) count += P.table[i].chunk0 <= start;
+  for (int i = threadIdx.x; i < P.n; i += kThreads) count += P.table[i].chunk0 <= c;
   if (threadIdx.x == 0) found = 0;
   __syncthreads();
   if (count) atomicAdd(&found, count);
   __syncthreads();
-  int e = found - 1;
-  Entry x = P.table[e];
-  for (int64_t i = 0; i < c1 - c0; ++i) {
-    const int64_t c = back ? c1 - 1 - i : c0 + i;
-    if (back) {
-      while (c < x.chunk0) x = P.table[--e];
-    } else {
-      while (e + 1 < P.n && P.table[e + 1].chunk0 <= c) x = P.table[++e];
-    }
-    f(x, (c - x.chunk0) * chunk_elems(x.dtype) - x.shift);
+  Cursor k;
+  k.e = found - 1;
+  k.x = P.table[k.e];
+  return k;
+}
+
+__device__ __forceinline__ void move_to(const NormParams& P, Cursor& k, int64_t c) {
+  while (c < k.x.chunk0) k.x = P.table[--k.e];
+  while (k.e + 1 < P.n && P.table[k.e + 1].chunk0 <= c) k.x = P.table[++k.e];
+}
+
+constexpr int kLoads = kChunkBytes / 16 / kThreads;
+
+// A chunk's 16-byte pieces of this thread: piece j at byte at(j) of the
+// tensor; those that lie in it wholly are loaded.
+struct Piece {
+  int64_t first;  // byte of piece 0
+  bool whole;     // the chunk lies in the tensor wholly
+  __device__ Piece(const Entry& x, int64_t c) {
+    const int64_t b = (c - x.chunk0) * kChunkBytes - x.shift;
+    first = b + threadIdx.x * 16;
+    whole = b >= 0 && b + kChunkBytes <= x.bytes;
   }
+  __device__ int64_t at(int j) const { return first + j * (kThreads * 16); }
+  __device__ bool in(const Entry& x, int j) const {
+    return whole || (at(j) >= 0 && at(j) + 16 <= x.bytes);
+  }
+};
+
+__device__ __forceinline__ void load_chunk(const Entry& x, const Piece& p, uint4 (&v)[kLoads]) {
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j)
+    if (p.in(x, j)) v[j] = *reinterpret_cast<const uint4*>(x.g + p.at(j));
 }
 
 // sum of squares of a chunk, this thread's share
 template <int DT>
-__device__ __forceinline__ double squares(const Entry& x, int64_t at) {
+__device__ __forceinline__ double squares(const Entry& x, const Piece& p,
+                                          const uint4 (&v)[kLoads]) {
   using Ty = Type<DT>;
   using S = typename Ty::S;
-  constexpr int V = Ty::kVec, kLoads = kChunkBytes / 16 / kThreads;
-  const S* g = static_cast<const S*>(x.g);
+  constexpr int V = Ty::kVec;
   double sum = 0.0;
-  uint4 v[kLoads];
-  const bool whole = at >= 0 && at + kLoads * kThreads * V <= x.n;
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const int64_t e0 = at + (threadIdx.x + j * kThreads) * V;
-    if (whole || (e0 >= 0 && e0 + V <= x.n)) v[j] = __ldg(reinterpret_cast<const uint4*>(g + e0));
-  }
-#pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    const int64_t e0 = at + (threadIdx.x + j * kThreads) * V;
-    if (whole || (e0 >= 0 && e0 + V <= x.n)) {
+    if (p.in(x, j)) {
       const S* e = reinterpret_cast<const S*>(&v[j]);
       float s = 0.0f;
 #pragma unroll
@@ -161,9 +171,9 @@ __device__ __forceinline__ double squares(const Entry& x, int64_t at) {
         }
       }
     } else {  // the tensor's ends
-      for (int q = 0; q < V; ++q)
-        if (e0 + q >= 0 && e0 + q < x.n) {
-          const double f = Ty::up(g[e0 + q]);
+      for (int64_t b = p.at(j); b < p.at(j) + 16; b += sizeof(S))
+        if (b >= 0 && b < x.bytes) {
+          const double f = Ty::up(*reinterpret_cast<const S*>(x.g + b));
           sum += f * f;
         }
     }
@@ -172,90 +182,99 @@ __device__ __forceinline__ double squares(const Entry& x, int64_t at) {
 }
 
 template <int DT>
-__device__ __forceinline__ void scale_chunk(const Entry& x, int64_t at, float coef) {
+__device__ __forceinline__ void scale_chunk(const Entry& x, const Piece& p, uint4 (&v)[kLoads],
+                                            float coef) {
   using Ty = Type<DT>;
   using S = typename Ty::S;
-  constexpr int V = Ty::kVec, kLoads = kChunkBytes / 16 / kThreads;
-  const S* g = static_cast<const S*>(x.g);
-  S* out = static_cast<S*>(x.out);
-  uint4 v[kLoads];
-  const bool whole = at >= 0 && at + kLoads * kThreads * V <= x.n;
+  constexpr int V = Ty::kVec;
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const int64_t e0 = at + (threadIdx.x + j * kThreads) * V;
-    if (whole || (e0 >= 0 && e0 + V <= x.n)) v[j] = *reinterpret_cast<const uint4*>(g + e0);
-  }
-#pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    const int64_t e0 = at + (threadIdx.x + j * kThreads) * V;
-    if (whole || (e0 >= 0 && e0 + V <= x.n)) {
+    if (p.in(x, j)) {
       S* e = reinterpret_cast<S*>(&v[j]);
 #pragma unroll
       for (int q = 0; q < V; ++q) e[q] = Ty::down(__fmul_rn(Ty::up(e[q]), coef));
+      uint8_t* out = x.out + p.at(j);
       if (x.same) {
-        *reinterpret_cast<uint4*>(out + e0) = v[j];
+        *reinterpret_cast<uint4*>(out) = v[j];
       } else {
 #pragma unroll
-        for (int q = 0; q < V; ++q) out[e0 + q] = e[q];
+        for (int q = 0; q < V; ++q) reinterpret_cast<S*>(out)[q] = e[q];
       }
     } else {
-      for (int q = 0; q < V; ++q)
-        if (e0 + q >= 0 && e0 + q < x.n) out[e0 + q] = Ty::down(__fmul_rn(Ty::up(g[e0 + q]), coef));
+      for (int64_t b = p.at(j); b < p.at(j) + 16; b += sizeof(S))
+        if (b >= 0 && b < x.bytes)
+          *reinterpret_cast<S*>(x.out + b) =
+              Ty::down(__fmul_rn(Ty::up(*reinterpret_cast<const S*>(x.g + b)), coef));
     }
   }
 }
 
+// the CTA's part [c0, c1) of all chunks
 __device__ __forceinline__ void my_range(const NormParams& P, int64_t& c0, int64_t& c1) {
   const int64_t q = P.chunks / gridDim.x, r = P.chunks % gridDim.x, b = blockIdx.x;
   c0 = b * q + (b < r ? b : r);
   c1 = c0 + q + (b < r ? 1 : 0);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const NormParams P) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_norm_kernel(const NormParams P) {
   __shared__ double red[kThreads / 32];
   pdl_wait_then_release();
   int64_t c0, c1;
   my_range(P, c0, c1);
   double sum = 0.0;
-  if (c0 < c1)
-    walk(P, c0, c1, false, [&](const Entry& x, int64_t at) {
-      if (x.dtype == HSNF4_F32)
-        sum += squares<HSNF4_F32>(x, at);
-      else if (x.dtype == HSNF4_BF16)
-        sum += squares<HSNF4_BF16>(x, at);
+  if (c0 < c1) {
+    Cursor k = locate(P, c0);
+    for (int64_t c = c0; c < c1; ++c) {
+      move_to(P, k, c);
+      const Piece p(k.x, c);
+      uint4 v[kLoads];
+      load_chunk(k.x, p, v);
+      if (k.x.dtype == HSNF4_F32)
+        sum += squares<HSNF4_F32>(k.x, p, v);
+      else if (k.x.dtype == HSNF4_BF16)
+        sum += squares<HSNF4_BF16>(k.x, p, v);
       else
-        sum += squares<HSNF4_F16>(x, at);
-    });
+        sum += squares<HSNF4_F16>(k.x, p, v);
+    }
+  }
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) P.partial[blockIdx.x] = sum;
 }
 
 // the norm from the partial sums (each CTA adds them all, in one order), and
-// the scaling
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const NormParams P) {
+// the scaling, from the end of the CTA's part; the first chunk is in flight
+// while the sums are added
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const NormParams P) {
   __shared__ double red[kThreads / 32];
   pdl_wait_then_release();
   double sum = 0.0;
   for (int i = threadIdx.x; i < P.parts; i += kThreads) sum += P.partial[i];
+  int64_t c0 = 0, c1 = 0;
+  if (P.scale) my_range(P, c0, c1);
+  Cursor k;
+  uint4 v[kLoads];
+  if (c0 < c1) {
+    k = locate(P, c1 - 1);
+    load_chunk(k.x, Piece(k.x, c1 - 1), v);
+  }
   const float norm = static_cast<float>(sqrt(block_sum(sum, red)));
   if (blockIdx.x == 0 && threadIdx.x == 0) *P.norm = norm;
-  if (!P.scale) return;
   // a NaN norm stays a NaN factor, an infinite one makes it 0
-  double c = isinf(P.max_norm) ? 1.0 : P.max_norm / (static_cast<double>(norm) + kEps);
-  if (c > 1.0) c = 1.0;
-  const float coef = static_cast<float>(c);
-  int64_t c0, c1;
-  my_range(P, c0, c1);
-  if (c0 < c1)
-    walk(P, c0, c1, true, [&](const Entry& x, int64_t at) {
-      if (coef == 1.0f && x.g == x.out) return;  // nothing to clip, in place
-      if (x.dtype == HSNF4_F32)
-        scale_chunk<HSNF4_F32>(x, at, coef);
-      else if (x.dtype == HSNF4_BF16)
-        scale_chunk<HSNF4_BF16>(x, at, coef);
-      else
-        scale_chunk<HSNF4_F16>(x, at, coef);
-    });
+  double f = isinf(P.max_norm) ? 1.0 : P.max_norm / (static_cast<double>(norm) + kEps);
+  if (f > 1.0) f = 1.0;
+  const float coef = static_cast<float>(f);
+  for (int64_t c = c1 - 1; c >= c0; --c) {
+    move_to(P, k, c);
+    if (coef == 1.0f && k.x.g == k.x.out) continue;  // nothing to clip, in place
+    const Piece p(k.x, c);
+    if (c < c1 - 1) load_chunk(k.x, p, v);
+    if (k.x.dtype == HSNF4_F32)
+      scale_chunk<HSNF4_F32>(k.x, p, v, coef);
+    else if (k.x.dtype == HSNF4_BF16)
+      scale_chunk<HSNF4_BF16>(k.x, p, v, coef);
+    else
+      scale_chunk<HSNF4_F16>(k.x, p, v, coef);
+  }
 }
 
 int grid_of(int64_t chunks) {
@@ -281,13 +300,12 @@ cudaError_t fill_grad_table(const hsnf4_grad* grads, int n, void* table, int64_t
   int64_t c = 0;
   for (int i = 0; i < n; ++i) {
     const hsnf4_grad& g = grads[i];
-    const int ce = chunk_elems(g.dtype), size = kChunkBytes / ce;
-    const uintptr_t off = reinterpret_cast<uintptr_t>(g.g) & 15u;
-    const int shift = static_cast<int>(off) / size;
-    const bool same = off == (reinterpret_cast<uintptr_t>(g.out) & 15u);
-    e[i] = {g.g, g.out, g.n, c, g.dtype, static_cast<int16_t>(shift),
-            static_cast<int16_t>(same)};
-    if (g.n) c += (g.n + shift + ce - 1) / ce;
+    const int64_t bytes = g.n * (g.dtype == HSNF4_F32 ? 4 : 2);
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(g.g) & 15u);
+    const bool same = shift == static_cast<int>(reinterpret_cast<uintptr_t>(g.out) & 15u);
+    e[i] = {static_cast<const uint8_t*>(g.g), static_cast<uint8_t*>(g.out), bytes, c, g.dtype,
+            static_cast<int16_t>(shift), static_cast<int16_t>(same)};
+    if (g.n) c += (bytes + shift + kChunkBytes - 1) / kChunkBytes;
   }
   *chunks = c;
   // pageable source: the copy has left it when the call returns
