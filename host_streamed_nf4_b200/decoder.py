@@ -13,7 +13,12 @@ pre-norm decoder layer of those families around its seven LoRA projections:
     h1 = h0 + lora_o(att)     b = rmsnorm(h1)          m = silu(lora_gate(b)) lora_up(b)
     h2 = h1 + lora_down(m)
 
-(causal grouped-query attention, head_dim 128, no rotary embedding).  The
+(causal grouped-query attention, head_dim 128).  By default the T tokens are
+one sequence without rotary positions; `rope` turns q and k to `positions`
+(several axes for images and video), and `seq_lens` packs several sequences,
+each attending to itself alone.  After a step (and, with several ranks, the
+sum of the gradients over them) `clip_grads` scales the adapter gradients by
+their global norm.  The
 forward keeps only each block's input; the backward of a block recomputes
 its layers' forward from that input with the same weights (the block is in
 its ring slot for the backward visit anyway) and the same dropout masks (the
@@ -39,7 +44,11 @@ Q, K, V, O, GATE, UP, DOWN = range(7)
 
 
 class DecoderStack(LayerStack):
-    def __init__(self, family: synth.Family, n_layers: int, T: int, **kw):
+    def __init__(self, family: synth.Family, n_layers: int, T: int, *, rope=None, positions=None,
+                 seq_lens=None, **kw):
+        """rope: an hsnf4.Rope of the family's head_dim; positions: int32
+        [n_axes, T] on the device (default: each sequence counts from 0, on
+        every axis).  seq_lens: lengths of the packed sequences, T together."""
         if family.head_dim != 128:
             raise ValueError("the attention kernels take head_dim 128")
         kw.setdefault("grouping", "decoder")
@@ -49,6 +58,18 @@ class DecoderStack(LayerStack):
         dev, f = self.device, family
         h, I, H, KV, d = f.hidden, f.inter, f.heads, f.kv_heads, f.head_dim
         self.H, self.KV = H, KV
+        if rope is not None and rope.head_dim != d:
+            raise ValueError(f"rope has head_dim {rope.head_dim}, the family {d}")
+        lens = [T] if seq_lens is None else [int(n) for n in seq_lens]
+        if sum(lens) != T or min(lens) < 0:
+            raise ValueError(f"seq_lens {lens} do not add up to T = {T}")
+        self.rope, self.positions, self.cu = rope, positions, None
+        if rope is not None and positions is None:
+            count = torch.cat([torch.arange(n, dtype=torch.int32) for n in lens])
+            self.positions = count.repeat(rope.n_axes, 1).to(dev)
+        if seq_lens is not None:
+            ends = torch.tensor([0] + lens).cumsum(0)
+            self.cu = ends.to(torch.int32).to(dev)
         seed = kw.get("seed", 42)
         data_seed = kw.get("data_seed") or seed
         g = _gen(dev, seed, 3_000_000)
@@ -83,8 +104,10 @@ class DecoderStack(LayerStack):
                    "db_u": bf(T, h), "dh1": bf(T, h), "datt": bf(T, H * d), "dq": bf(T, H * d),
                    "dk": bf(T, KV * d), "dv": bf(T, KV * d), "da_q": bf(T, h), "da_k": bf(T, h),
                    "da_v": bf(T, h), "dh_a": bf(T, h), "dh_b": bf(T, h),
-                   "scratch": torch.empty(hsnf4.attention_scratch_bytes(T, H), dtype=torch.uint8,
-                                          device=dev)}
+                   "scratch": torch.empty(
+                       hsnf4.attention_scratch_bytes(T, H) if self.cu is None else
+                       hsnf4.attention_packed_workspace_bytes(T, T, len(lens), H, KV, d),
+                       dtype=torch.uint8, device=dev)}
         torch.cuda.synchronize(dev)
 
     # ------------------------------------------------------------ one layer
@@ -108,8 +131,14 @@ class DecoderStack(LayerStack):
         s["h0"] = h0  # the input stays alive (block input or a kept layer output)
         hsnf4.rmsnorm_fwd(s["h0"], self.g1[l], EPS, y=s["a"], stream=st)
         self._lora_fwd(w, l, (Q, K, V), (s["a"],) * 3, (s["q"], s["k"], s["v"]))
-        hsnf4.attention_fwd(s["q"], s["k"], s["v"], self.H, self.KV, o=s["att"], lse=s["lse"],
-                            stream=st)
+        if self.rope is not None:  # in place: the backward needs the turned q and k only
+            hsnf4.rope_fwd(self.rope, self.positions, s["q"], s["k"], s["q"], s["k"], stream=st)
+        if self.cu is not None:
+            hsnf4.attention_packed_fwd(s["q"], s["k"], s["v"], self.cu, self.H, self.KV,
+                                       o=s["att"], lse=s["lse"], stream=st)
+        else:
+            hsnf4.attention_fwd(s["q"], s["k"], s["v"], self.H, self.KV, o=s["att"],
+                                lse=s["lse"], stream=st)
         self._lora_fwd(w, l, (O,), (s["att"],), (s["o"],))
         hsnf4.rmsnorm_fwd(s["h0"], self.g2[l], EPS, res=s["o"], h_out=s["h1"], y=s["b"],
                           stream=st)
@@ -129,9 +158,17 @@ class DecoderStack(LayerStack):
         hsnf4.rmsnorm_bwd(s["h1"], self.g2[l], (gs["db_g"], gs["db_u"]), EPS, dres=dh2,
                           dx=gs["dh1"], stream=st)
         self._lora_bwd(w, l, (O,), (s["att"],), (gs["dh1"],), (gs["datt"],))
-        hsnf4.attention_bwd(s["q"], s["k"], s["v"], s["att"], s["lse"], gs["datt"], self.H,
-                            self.KV, dq=gs["dq"], dk=gs["dk"], dv=gs["dv"], scratch=gs["scratch"],
-                            stream=st)
+        if self.cu is not None:
+            hsnf4.attention_packed_bwd(s["q"], s["k"], s["v"], s["att"], s["lse"], gs["datt"],
+                                       self.cu, self.H, self.KV, dq=gs["dq"], dk=gs["dk"],
+                                       dv=gs["dv"], workspace=gs["scratch"], stream=st)
+        else:
+            hsnf4.attention_bwd(s["q"], s["k"], s["v"], s["att"], s["lse"], gs["datt"], self.H,
+                                self.KV, dq=gs["dq"], dk=gs["dk"], dv=gs["dv"],
+                                scratch=gs["scratch"], stream=st)
+        if self.rope is not None:
+            hsnf4.rope_bwd(self.rope, self.positions, gs["dq"], gs["dk"], gs["dq"], gs["dk"],
+                           stream=st)
         self._lora_bwd(w, l, (Q, K, V), (s["a"],) * 3, (gs["dq"], gs["dk"], gs["dv"]),
                        (gs["da_q"], gs["da_k"], gs["da_v"]))
         hsnf4.rmsnorm_bwd(s["h0"], self.g1[l], (gs["da_q"], gs["da_k"], gs["da_v"]), EPS,

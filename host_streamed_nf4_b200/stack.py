@@ -173,6 +173,7 @@ class LayerStack:
         self.ws_f = torch.empty(ws_f, dtype=torch.uint8, device=dev)
         self.ws_b = torch.empty(ws_b, dtype=torch.uint8, device=dev)
         self._prefetched = False
+        self._grad_set = None
         torch.cuda.synchronize(dev)
 
     # ------------------------------------------------------------------ setup
@@ -378,6 +379,17 @@ class LayerStack:
         self._bwd_block(ws, 0, record)
         self.streamer.release(0, self.compute)
         self.step_idx += 1
+
+    def clip_grads(self, max_norm: float, norm=None) -> torch.Tensor:
+        """Scale every adapter gradient of the last step by min(1, max_norm /
+        (their global norm + 1e-6)), on the compute stream; returns the norm
+        before that (a device scalar).  With several ranks, after their
+        gradients are summed."""
+        if self._grad_set is None:
+            self._grad_set = hsnf4.GradSet([self.grad_flat], stream=self.compute)
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=self.device)
+        return hsnf4.grad_clip(self._grad_set, max_norm, norm=norm, stream=self.compute)
 
     # ------------------------------------------------------------------ checks
 

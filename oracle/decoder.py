@@ -19,6 +19,10 @@ those families, with causal grouped-query attention and no rotary embedding
     m  = silu(lora_gate(b)) * lora_up(b)
     h2 = h1 + lora_down(m)
 
+A layer may also turn q and k to rotary positions (angle a = position times
+frequency, pairs (i, i + d/2): x1 cos a - x2 sin a, x2 cos a + x1 sin a) and
+hold several sequences, each attending to itself alone.
+
 Backward from dh2 through every module, in the reverse order.  The compute
 dtype is bf16 (the workloads' dtype): every module's output, and every sum
 of gradient branches, is rounded once to bf16 (`rnd`); inside a module the
@@ -79,6 +83,8 @@ class Layer:
     g2: np.ndarray
     lin: dict = field(default_factory=dict)  # name -> Linear
     alpha: float = 32.0
+    angles: np.ndarray | None = None  # [T, d / 2], or no rotary positions
+    lens: list | None = None          # lengths of the sequences, or one of T
 
 
 def _fwd(L: Linear, X: np.ndarray, alpha: float):
@@ -109,6 +115,21 @@ def _bwd(L: Linear, X: np.ndarray, dY: np.ndarray, alpha: float):
     return dX.astype(np.float64), dA, dB
 
 
+def rotate(x: np.ndarray, heads: int, angles: np.ndarray, sign: int = 1) -> np.ndarray:
+    """x [T, heads * d] with each head turned by its token's angles (sign -1:
+    the transpose, which is the gradient's way back)."""
+    T, half = angles.shape
+    x = np.asarray(x, np.float64).reshape(T, heads, 2 * half)
+    c, s = np.cos(angles)[:, None], sign * np.sin(angles)[:, None]
+    a, b = x[..., :half], x[..., half:]
+    return np.concatenate([a * c - b * s, b * c + a * s], -1).reshape(T, -1)
+
+
+def _sequences(layer: Layer, T: int):
+    ends = np.cumsum([T] if layer.lens is None else layer.lens)
+    return [slice(e - n, e) for e, n in zip(ends, [T] if layer.lens is None else layer.lens)]
+
+
 def layer_forward(layer: Layer, h0: np.ndarray, rnd=rnd_bf16) -> dict:
     """All activations of one layer (doubles holding bf16 values unless
     rnd is the identity).  h0 [T, hidden]."""
@@ -118,8 +139,11 @@ def layer_forward(layer: Layer, h0: np.ndarray, rnd=rnd_bf16) -> dict:
     s["a"] = rnd(rmsnorm_fwd(h0, layer.g1, EPS))
     for n in ("q", "k", "v"):
         s[n] = rnd(_fwd(layer.lin[n], s["a"], layer.alpha)[0])
-    att, _ = attention_fwd(s["q"], s["k"], s["v"], H, KV, d, 1.0 / np.sqrt(d))
-    s["att"] = rnd(att)
+    if layer.angles is not None:
+        s["q"], s["k"] = rnd(rotate(s["q"], H, layer.angles)), rnd(rotate(s["k"], KV, layer.angles))
+    s["att"] = rnd(np.concatenate(
+        [attention_fwd(s["q"][r], s["k"][r], s["v"][r], H, KV, d, 1.0 / np.sqrt(d))[0]
+         for r in _sequences(layer, h0.shape[0])]))
     s["o"] = rnd(_fwd(layer.lin["o"], s["att"], layer.alpha)[0])
     s["h1"] = rnd(h0 + s["o"])
     s["b"] = rnd(rmsnorm_fwd(s["h1"], layer.g2, EPS))
@@ -146,7 +170,11 @@ def layer_backward(layer: Layer, s: dict, dh2: np.ndarray, rnd=rnd_bf16):
     dh1 = rnd(dh2 + rmsnorm_bwd(s["h1"], layer.g2, db, EPS))
     datt, *g["o"] = _bwd(layer.lin["o"], s["att"], dh1, al)
     datt = rnd(datt)
-    dq, dk, dv = attention_bwd(s["q"], s["k"], s["v"], datt, H, KV, d, 1.0 / np.sqrt(d))
+    dq, dk, dv = (np.concatenate(x) for x in zip(
+        *[attention_bwd(s["q"][r], s["k"][r], s["v"][r], datt[r], H, KV, d, 1.0 / np.sqrt(d))
+          for r in _sequences(layer, dh2.shape[0])]))
+    if layer.angles is not None:
+        dq, dk = rotate(rnd(dq), H, layer.angles, -1), rotate(rnd(dk), KV, layer.angles, -1)
     da = 0.0
     for n, dy in (("q", rnd(dq)), ("k", rnd(dk)), ("v", rnd(dv))):
         dx, *g[n] = _bwd(layer.lin[n], s["a"], dy, al)
