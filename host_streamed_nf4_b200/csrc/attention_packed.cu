@@ -448,11 +448,11 @@ struct BwdTc {
   CUtensorMap mq, mk, mv, mdo, mo;  // boxes of 128 rows (mk, mv in the dQ kernel: of kStep)
   const float* lse;
   float* D;     // [H, Tq]: written by the dQ kernel, read by the dK/dV kernel
-  float* part;  // [splits][2][Tk][KV][d] partial dK, dV (splits > 1)
+  float4* part;  // shares' dK, dV sums: [key tile][KV][splits], part_size each
   uint16_t *dq, *dk, *dv;
   int64_t dqs, dks, dvs;
   PackedSeqs S;
-  int H, KV, splits;
+  int H, KV, splits, limit;  // splits: the most shares of a KV group's heads; limit: see tile_shares
   float scale, c;  // c = scale * log2(e)
 };
 
@@ -750,6 +750,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
   }
 }
 
+// the first query tile that sees the keys of tile x
+__device__ __forceinline__ int first_query_tile(const PackedSeqs& S, const PackedTile& x) {
+  return (S.causal ? max(x.t * kRows - (x.lk - x.lq), 0) : 0) / kRows;
+}
+
+// Shares that a key tile's query heads are cut into: so many that none has
+// more than `limit` query tiles to go through, within the grid's `splits`.  A
+// long sequence among short ones would otherwise keep one CTA busy long after
+// the others (8150 tokens in 17 sequences, the longest 1855: 168 us of 350).
+__device__ __forceinline__ int tile_shares(const BwdTc& P, const PackedTile& x) {
+  const int all = max((x.lq + kRows - 1) / kRows - first_query_tile(P.S, x), 0) * (P.H / P.KV);
+  return min(max((all + P.limit - 1) / P.limit, 1), P.splits);
+}
+
+// A share's fp32 sums of a tile and KV head, as float4: dV and dK of 128 keys.
+template <int D>
+__host__ __device__ constexpr int64_t part_size() {
+  return 2 * kRows * D / 4;
+}
+template <int D>
+__device__ __forceinline__ int64_t part_at(const BwdTc& P, int slot, int kh, int split) {
+  return ((static_cast<int64_t>(slot) * P.KV + kh) * P.splits + split) * part_size<D>();
+}
+
 // dK, dV of 128 keys of one KV head, over one share of the group's query
 // heads and, in each, the query tiles that see the keys, in order.  The
 // scores are computed transposed (a thread owns a key row, 64 of the tile's
@@ -769,12 +793,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
   __shared__ int abort_flag;
   __shared__ __align__(16) float nlse[2][kRows], nD[2][kRows];  // -lse log2(e), -D
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = P.KV * P.splits;
+  const int per = P.KV * P.splits, kh = blockIdx.x % per / P.splits,
+            split = blockIdx.x % per % P.splits;
   if (warp == 0 && lane == 0) prefetch_maps(P);
   pdl_wait_then_release();
-  // (before anything is set up: the grid covers the most tiles there could be)
+  // (before anything is set up: the grid covers the most tiles and shares)
   PackedTile x;
   if (!find_tile(P.S, true, blockIdx.x / per, kRows, x)) return;
+  const int shares = tile_shares(P, x);
+  if (split >= shares) return;
   if (threadIdx.x == 0) {
     mbar_init(&kv_full, 1);
     mbar_init(&aux, 1);
@@ -812,13 +839,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
     return;
   }
 
-  const int share = blockIdx.x % per;
-  const int kh = share / P.splits, split = share % P.splits;
   const int grp = P.H / P.KV;
-  const int h0 = kh * grp + grp * split / P.splits, h1 = kh * grp + grp * (split + 1) / P.splits;
+  const int h0 = kh * grp + grp * split / shares, h1 = kh * grp + grp * (split + 1) / shares;
   const int c0 = x.t * kRows;
-  // the first query that sees the tile's first key, and so the first tile
-  const int qt0 = (P.S.causal ? max(c0 - (x.lk - x.lq), 0) : 0) / kRows;
+  const int qt0 = first_query_tile(P.S, x);
   const int per_head = max((x.lq + kRows - 1) / kRows - qt0, 0);
   const int n = per_head * (h1 - h0);
   int last_a = -1, last_b = -1;
@@ -1015,10 +1039,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
       // eight warps write dV, eight dK, half of the columns each
       const int which = part >> 1, col = (part & 1) * (D / 2);  // 1: dK
       const uint32_t src = tmem + 256 + which * D + col + lanes;
-      const int first = c0 + q4 * 32;  // all products are done: the ring stages the rows
-      const int64_t tok = x.k0 + first;
-      const int64_t one = static_cast<int64_t>(P.S.Tk) * P.KV * D;
-      uint8_t* stage = ring + warp * 4096;
+      const int first = c0 + q4 * 32;
+      float4* share = P.part + part_at<D>(P, blockIdx.x / per, kh, split) + warp * (D * 4) + lane;
       uint4 v[D / 16];
 #pragma unroll
       for (int b = 0; b < D / 64; ++b) {
@@ -1029,23 +1051,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (P.splits > 1) {
-          uint4 u[8];
+        if (shares > 1) {  // in the threads' order, which packed_kv_reduce shares
 #pragma unroll
           for (int c = 0; c < 8; ++c)
-            u[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-          put_rows<8>(stage, u,
-                      P.part + (2 * split + 1 - which) * one + (tok * P.KV + kh) * D + col + 32 * b,
-                      static_cast<int64_t>(P.KV) * D * 4, x.lk - first);
+            share[(8 * b + c) * 32] =
+                make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                            __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             v[4 * b + c] = pack8_scaled(o + 8 * c, which ? P.scale : 1.0f);
         }
       }
-      if (P.splits == 1) {
+      if (shares == 1) {  // all products are done: the ring stages the rows
         const int64_t pitch = which ? P.dks : P.dvs;
-        put_rows<D / 16>(stage, v, (which ? P.dk : P.dv) + tok * pitch + kh * D + col, pitch * 2,
+        put_rows<D / 16>(ring + warp * 4096, v,
+                         (which ? P.dk : P.dv) + (x.k0 + first) * pitch + kh * D + col, pitch * 2,
                          x.lk - first);
       }
     }
@@ -1073,39 +1094,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
   }
 }
 
-// dK, dV of every token that belongs to a sequence (those between the first
-// length and the last), the shares added in order: eight elements a thread
+// dK, dV of the key tiles with several shares, which are added in order: a
+// CTA takes a tile and KV head, its warps and lanes as the kernel's above
 template <int D>
-__global__ void __launch_bounds__(256) packed_kv_reduce(const __grid_constant__ BwdTc P) {
+__global__ void __launch_bounds__(32 * kComputeWarps)
+    packed_kv_reduce(const __grid_constant__ BwdTc P) {
+  __shared__ __align__(16) uint8_t stage[kComputeWarps * 2048];
   pdl_wait_then_release();
-  const int t0 = min(max(__ldg(P.S.cu_k), 0), P.S.Tk);
-  const int t1 = min(__ldg(P.S.cu_k + P.S.n_seq), P.S.Tk);
-  const int row8 = P.KV * (D / 8);
-  const int64_t one = static_cast<int64_t>(P.S.Tk) * P.KV * D;
-  const int64_t items = static_cast<int64_t>(max(t1 - t0, 0)) * row8;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < items;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t tok = t0 + i / row8;
-    const int e = static_cast<int>(i % row8) * 8;  // element of the token's KV * D
-    const float* p = P.part + tok * P.KV * D + e;
-    float a[8] = {}, b[8] = {};
-    for (int s = 0; s < P.splits; ++s) {
-      const float4* y = reinterpret_cast<const float4*>(p + 2 * s * one);
-      const float4* z = reinterpret_cast<const float4*>(p + (2 * s + 1) * one);
-      const float4 y0 = y[0], y1 = y[1], z0 = z[0], z1 = z[1];
-      a[0] += y0.x, a[1] += y0.y, a[2] += y0.z, a[3] += y0.w;
-      a[4] += y1.x, a[5] += y1.y, a[6] += y1.z, a[7] += y1.w;
-      b[0] += z0.x, b[1] += z0.y, b[2] += z0.z, b[3] += z0.w;
-      b[4] += z1.x, b[5] += z1.y, b[6] += z1.z, b[7] += z1.w;
-    }
-    uint32_t u[4], v[4];
+  PackedTile x;
+  const int kh = blockIdx.x % P.KV, slot = blockIdx.x / P.KV;
+  if (!find_tile(P.S, true, slot, kRows, x)) return;
+  const int shares = tile_shares(P, x);
+  if (shares == 1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = warp >> 2, which = part >> 1, first = x.t * kRows + (warp & 3) * 32;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u[j] = f32x2_to_bf16x2(f32x2_pack(a[2 * j] * P.scale, a[2 * j + 1] * P.scale));
-      v[j] = f32x2_to_bf16x2(f32x2_pack(b[2 * j], b[2 * j + 1]));
+  for (int b = 0; b < D / 64; ++b) {
+    const float4* p = P.part + part_at<D>(P, slot, kh, 0) + warp * (D * 4) + 8 * b * 32 + lane;
+    float4 sum[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sum[c] = p[c * 32];
+#pragma unroll 2
+    for (int s = 1; s < shares; ++s) {
+      p += part_size<D>();
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float4 y = p[c * 32];
+        sum[c].x += y.x, sum[c].y += y.y, sum[c].z += y.z, sum[c].w += y.w;
+      }
     }
-    *reinterpret_cast<uint4*>(P.dk + tok * P.dks + e) = make_uint4(u[0], u[1], u[2], u[3]);
-    *reinterpret_cast<uint4*>(P.dv + tok * P.dvs + e) = make_uint4(v[0], v[1], v[2], v[3]);
+    uint4 v[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      v[c] = pack8_scaled(reinterpret_cast<const uint32_t*>(sum + 2 * c), which ? P.scale : 1.0f);
+    const int64_t pitch = which ? P.dks : P.dvs;
+    put_rows<4>(stage + warp * 2048, v,
+                (which ? P.dk : P.dv) + (x.k0 + first) * pitch + kh * D + (part & 1) * (D / 2) +
+                    32 * b,
+                pitch * 2, x.lk - first);
   }
 }
 
@@ -1148,11 +1174,20 @@ int sm_count() {
   return sms;
 }
 
-// shares of a KV group's query heads, so that there are CTAs for every SM
-int head_splits(int64_t Tk, int H, int KV) {
-  const int64_t tiles = (Tk + kRows - 1) / kRows * KV;
-  const int64_t want = (sm_count() + tiles - 1) / tiles;
-  return static_cast<int>(std::min<int64_t>(H / KV, std::max<int64_t>(want, 1)));
+// The most shares of a KV group's query heads: with four CTAs per SM and more
+// the order of the tiles (longest first) evens them out, below that up to
+// twice as many as would fill them.
+int head_splits(int64_t Tk, int n_seq, int H, int KV) {
+  const int64_t tiles = most_tiles(Tk, n_seq, kRows) * KV, full = 4 * sm_count();
+  if (tiles >= full) return 1;
+  return static_cast<int>(std::min<int64_t>(H / KV, 2 * ((full + tiles - 1) / tiles)));
+}
+
+// Query tiles per share: an SM's part of them all, were the sequences equal.
+int share_limit(const hsnf4_packed_attention& a) {
+  const int64_t mean = (a.Tq / a.n_seq + kRows - 1) / kRows, tiles = (a.Tk + kRows - 1) / kRows;
+  const int64_t all = a.H * tiles * (a.causal ? (mean + 1) / 2 : mean);
+  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(all / sm_count(), 4), 1 << 30));
 }
 
 template <int D>
@@ -1170,7 +1205,7 @@ cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws
     return cudaErrorInvalidValue;
   P.lse = b.lse;
   P.D = static_cast<float*>(ws);
-  P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+  P.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) +
                                     round_up(static_cast<size_t>(a.H) * a.Tq * 4, 256));
   P.dq = static_cast<uint16_t*>(b.dq);
   P.dk = static_cast<uint16_t*>(b.dk);
@@ -1181,7 +1216,8 @@ cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws
   P.S = {a.cu_q, a.cu_k, static_cast<int>(a.Tq), static_cast<int>(a.Tk), a.n_seq, a.causal};
   P.H = a.H;
   P.KV = a.KV;
-  P.splits = head_splits(a.Tk, a.H, a.KV);
+  P.splits = head_splits(a.Tk, a.n_seq, a.H, a.KV);
+  P.limit = share_limit(a);
   P.scale = a.scale;
   P.c = a.scale * kLog2e;
   cudaError_t e = allow_smem(packed_dq_tc<D>, DqGeo<D>::kSmem, done_q);
@@ -1197,18 +1233,19 @@ cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws
                                                                a.KV * P.splits)),
                  dim3(kTcThreads), BwdGeo<D>::kSmem, st, P);
   if (e != cudaSuccess || P.splits == 1) return e;
-  const int64_t items = a.Tk * a.KV * (D / 8);
-  const int64_t grid = std::min<int64_t>((items + 255) / 256, static_cast<int64_t>(sm_count()) * 8);
-  return launch_pdl(packed_kv_reduce<D>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, P);
+  return launch_pdl(packed_kv_reduce<D>,
+                    dim3(static_cast<unsigned>(most_tiles(a.Tk, a.n_seq, kRows) * a.KV)),
+                    dim3(32 * kComputeWarps), 0, st, P);
 }
 
 }  // namespace
 
 // D [H, Tq] fp32, then the shares' fp32 dK, dV
 size_t packed_workspace_bytes(int64_t Tq, int64_t Tk, int n_seq, int H, int KV, int d) {
-  const int splits = head_splits(Tk, H, KV);
+  const int splits = head_splits(Tk, n_seq, H, KV);
   size_t n = round_up(static_cast<size_t>(H) * Tq * 4, 256);
-  if (splits > 1) n += static_cast<size_t>(splits) * 2 * Tk * KV * d * 4;
+  if (splits > 1)
+    n += static_cast<size_t>(most_tiles(Tk, n_seq, kRows)) * KV * splits * 2 * kRows * d * 4;
   return n;
 }
 
