@@ -46,6 +46,7 @@ constexpr int kPolyOf = 8, kPolyPart = 2;
 constexpr int kComputeWarps = 16;  // four per SM sub-partition
 constexpr int kTcThreads = 32 * (kComputeWarps + 2);
 constexpr int kMmaWarp = kComputeWarps, kLoadWarp = kComputeWarps + 1;
+constexpr int kPatchWarp = kComputeWarps + 2;  // dK/dV kernel only
 
 // A wait of the whole loading warp, which leaves whole when it gives up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, volatile int* abort,
@@ -783,11 +784,12 @@ __device__ __forceinline__ int64_t part_at(const BwdTc& P, int slot, int kh, int
 // compute P^T the tensor cores run the tile before's dK product and this
 // tile's dP^T; while they compute dS^T, dV and the next S^T.
 template <int D>
-__global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_constant__ BwdTc P) {
+__global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __grid_constant__ BwdTc P) {
   using G = BwdGeo<D>;
   constexpr int NA = G::kA, NB = G::kB;  // Q, dO
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ uint64_t kv_full, q_full[NA], ld_full[2], q_empty[NA], do_full[NB], do_empty[NB], aux,
+  __shared__ uint64_t kv_full, q_full[NA], ld_full[2], q_empty[NA], do_full[NB], do_empty[NB], q_raw[NA],
+      do_raw[NB],
       s_full, dp_full, p_full, ds_full, done, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -804,15 +806,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
   if (split >= shares) return;
   if (threadIdx.x == 0) {
     mbar_init(&kv_full, 1);
-    mbar_init(&aux, 1);
     mbar_init(&drain, 1);
     for (int i = 0; i < NA; ++i) {
       mbar_init(&q_full[i], 1);
+      mbar_init(&q_raw[i], 1);
       mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&ld_full[i], 32);
     for (int i = 0; i < NB; ++i) {
       mbar_init(&do_full[i], 1);
+      mbar_init(&do_raw[i], 1);
       mbar_init(&do_empty[i], 1);
     }
     mbar_init(&s_full, 1);
@@ -856,30 +859,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
       tma_tile<D>(smem + G::kTile, &P.mv, &kv_full, kh * D, x.k0 + c0);
     }
     kv_loaded = true;
-    int h = h0, qt = qt0, tails = 0;
+    int h = h0, qt = qt0;
     for (int i = 0; i < n; ++i) {
       const int s = i % NA, v = i % NB, row = qt * kRows;
-      const bool tail = row + kRows > x.lq;  // P, dS are 0 there; Q, dO must be finite
-      auto load = [&](uint8_t* st, const CUtensorMap* map, uint64_t* full) {
-        uint64_t* bar = tail ? &aux : full;
+      const bool tail = row + kRows > x.lq;  // goes through the patching warp
+      auto load = [&](uint8_t* st, const CUtensorMap* map, uint64_t* bar) {
         if (lane == 0) {
           mbar_arrive_expect_tx(bar, G::kTile);
           tma_tile<D>(st, map, bar, h * D, x.q0 + row);
         }
       };
-      auto patch = [&](uint8_t* st, uint64_t* full) {
-        if (!tail) return true;
-        __syncwarp();
-        if (!tail_landed(&aux, tails & 1, abort_p)) return false;
-        ++tails;
-        zero_rows<D>(st, x.lq - row);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full);
-        return true;
-      };
       if (i >= NA && !warp_wait(&q_empty[s], (i / NA) - 1, abort_p, kAtFlagLoad)) break;
-      load(ring + s * G::kTile, &P.mq, &q_full[s]);
+      load(ring + s * G::kTile, &P.mq, tail ? &q_raw[s] : &q_full[s]);
+      last_a = i;
       float a[4], b[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -889,25 +881,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dkdv_tc(const __grid_con
         b[e] = row + j < x.lq ? -P.D[at] : 0.0f;
       }
       // their slot was last read for tile i - 2, before its dK product
-      if (i >= 2 && !warp_wait(&q_empty[(i - 2) % NA], (i - 2) / NA, abort_p, kAtFlagLoad)) {
-        last_a = i;
-        break;
-      }
+      if (i >= 2 && !warp_wait(&q_empty[(i - 2) % NA], (i - 2) / NA, abort_p, kAtFlagLoad)) break;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         nlse[i & 1][lane + 32 * e] = a[e];
         nD[i & 1][lane + 32 * e] = b[e];
       }
       mbar_arrive(&ld_full[i & 1]);
-      if (!patch(ring + s * G::kTile, &q_full[s])) break;
-      last_a = i;
       if (i >= NB && !warp_wait(&do_empty[v], (i / NB) - 1, abort_p, kAtFlagLoad)) break;
-      load(ring + (NA + v) * G::kTile, &P.mdo, &do_full[v]);
-      if (!patch(ring + (NA + v) * G::kTile, &do_full[v])) break;
+      load(ring + (NA + v) * G::kTile, &P.mdo, tail ? &do_raw[v] : &do_full[v]);
       last_b = i;
       if (++qt == qt0 + per_head) {
         qt = qt0;
         ++h;
+      }
+    }
+  } else if (warp == kPatchWarp && n) {
+    // The rows behind the sequence in each head's last query tile: P and dS
+    // are 0 there, Q and dO must be finite.  (A warp of its own: the loader
+    // would wait for every such tile instead of running ahead, 3.7 us a tile
+    // where each is one.)
+    const int row = (qt0 + per_head - 1) * kRows;
+    uint32_t q_phase = 0, do_phase = 0;  // a bit per stage
+    if (row + kRows > x.lq) {
+      for (int i = per_head - 1; i < n; i += per_head) {
+        const int s = i % NA, v = i % NB;
+        if (!tail_landed(&q_raw[s], (q_phase >> s) & 1, abort_p)) break;
+        q_phase ^= 1u << s;
+        zero_rows<D>(ring + s * G::kTile, x.lq - row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[s]);
+        if (!tail_landed(&do_raw[v], (do_phase >> v) & 1, abort_p)) break;
+        do_phase ^= 1u << v;
+        zero_rows<D>(ring + (NA + v) * G::kTile, x.lq - row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&do_full[v]);
       }
     }
   } else if (warp == kMmaWarp && n) {
@@ -1231,7 +1241,7 @@ cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws
     return cudaErrorInvalidValue;
   e = launch_pdl(packed_dkdv_tc<D>, dim3(static_cast<unsigned>(most_tiles(a.Tk, a.n_seq, kRows) *
                                                                a.KV * P.splits)),
-                 dim3(kTcThreads), BwdGeo<D>::kSmem, st, P);
+                 dim3(kTcThreads + 32), BwdGeo<D>::kSmem, st, P);
   if (e != cudaSuccess || P.splits == 1) return e;
   return launch_pdl(packed_kv_reduce<D>,
                     dim3(static_cast<unsigned>(most_tiles(a.Tk, a.n_seq, kRows) * a.KV)),
