@@ -473,61 +473,78 @@ struct BwdGeo {
   static constexpr int kSmem = (2 + kA + kB) * kTile;
 };
 
-__device__ __forceinline__ void bar_compute() {  // the computing threads
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
-}
-
 // dQ of 128 query rows of one head, the keys 64 at a time: S = Q K^T,
 // dP = dO V^T, dS = P (dP - D) as bf16 over its dP, dQ += dS K.  Q and dO,
-// which every step reads, stay in TMEM as left operands, so that no product
-// reads more than 16 KiB of shared memory per step (with both operands there
-// the 128 x 128 x 16 products took 86 to 116 cycles instead of 64).  TMEM:
-// Q, dO (D / 2 columns each), dQ (D), two buffers of S and dP (64 columns
-// each); warps 0..7 take the even steps, 8..15 the odd ones.  The kernel also
-// writes D = dO . O for the dK/dV kernel.
+// which every step reads, stay in TMEM as left operands, so that a 64-key
+// product takes 32 cycles per 16 columns (48 with both operands in shared
+// memory).  TMEM: Q, dO (D / 2 columns each), dQ (D), two buffers of S and dP
+// (64 columns each); warps 0..7 take the even steps, 8..15 the odd ones.  The
+// kernel also writes D = dO . O for the dK/dV kernel.
+//
+// Persistent: a CTA takes a tile (query tile, head) of every gridDim.x.  One ring of stages runs through all of them (per tile Q, dO, O, then a
+// K and a V tile per step), so the loader, which also finds the tiles, is
+// ahead in the next tile while this one's results are written: 4.8 us of
+// start and end per tile became 1.6.
 constexpr int kStep = 64;  // keys of a step
 
 template <int D>
 struct DqGeo {
-  static constexpr int kTile = kStep * D * 2;
-  static constexpr int kStages = D == 128 ? 6 : 8;  // of a K and a V tile
-  static constexpr int kSmem = 2 * kStages * kTile;
-  static constexpr int kFirst = kStages - 3 * kRows / (2 * kStep);  // stages before Q, dO, O
+  static constexpr int kTile = kStep * D * 2;       // K or V of a step; Q, dO, O take two
+  static constexpr int kStages = D == 128 ? 6 : 8;  // of two such tiles
+  static constexpr int kRing = kStages * 2 * kTile;
+  static constexpr int kSmem = kRing + kComputeWarps * 2048;  // and staged rows
   static constexpr uint32_t kQ = 0, kDo = D / 2, kDq = D, kS = 256, kDp = 384;  // TMEM columns
 };
+
+// What the loader tells the other warps of a tile; n: its steps, -1: no more.
+struct DqTile {
+  int q0, lq, k0, lk, r0, h, n;
+};
+
+// A vote over the computing threads, which also orders their shared-memory
+// accesses around it.
+__device__ __forceinline__ bool compute_any(bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "n"(32 * kComputeWarps)
+      : "memory");
+  return r != 0;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_constant__ BwdTc P) {
   using G = DqGeo<D>;
   constexpr int NS = G::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ uint64_t q_full, q_ready, kv_full[NS], kv_empty[NS], aux, s_full[2], ds_full[2], done,
-      drain;
+  __shared__ uint64_t full[NS], empty[NS], aux, tile_full[2], tile_empty[2], q_ready, s_full[2],
+      ds_full[2], done, drain;
+  __shared__ DqTile tiles[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float dsum[4][kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0 && lane == 0) prefetch_maps(P);
-  pdl_wait_then_release();
-  // (before anything is set up: the grid covers the most tiles there could be)
-  PackedTile x;
-  if (!find_tile(P.S, false, blockIdx.x / P.H, kRows, x)) return;
   if (threadIdx.x == 0) {
-    mbar_init(&q_full, 1);
-    mbar_init(&q_ready, kComputeWarps);
     mbar_init(&aux, 1);
     mbar_init(&drain, 1);
+    mbar_init(&q_ready, kComputeWarps);
+    mbar_init(&done, 1);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
     }
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&tile_full[b], 1);
+      mbar_init(&tile_empty[b], kComputeWarps + 1);
       mbar_init(&s_full[b], 1);
       mbar_init(&ds_full[b], kComputeWarps / 2);
     }
-    mbar_init(&done, 1);
     abort_flag = 0;
     fence_mbar_init();
+    prefetch_maps(P);
   }
   if (warp == kMmaWarp) {
     tmem_alloc(&tmem_slot, 512);
@@ -538,205 +555,264 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
   volatile int* abort_p = &abort_flag;
+  pdl_wait_then_release();
   // the swizzled tiles need the alignment asked for
   if ((smem_u32(smem) & 1023u) || tmem_slot != tmem) {
     if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
     if (warp == kMmaWarp) tmem_dealloc(tmem_slot, 512);
     return;
   }
+  auto stage = [&](uint32_t e) { return smem + e % NS * (2 * G::kTile); };
+  uint32_t loads = 0;  // ring entries issued (loader)
+  bool mma_issued = false;
 
-  const int h = blockIdx.x % P.H, kh = h / (P.H / P.KV);
-  const int r0 = x.t * kRows;
-  const int n = (key_limit(P.S, x, min(r0 + kRows, x.lq) - 1) + kStep - 1) / kStep;
-  int last_load = -1;
-  bool q_loaded = false, mma_issued = false;
-  // Q, dO and O of the 128 rows come through the last stages of the ring
-  uint8_t* first_tile = smem + G::kFirst * 2 * G::kTile;
-
-  if (warp == kLoadWarp && n) {
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&q_full, 3 * kRows * D * 2);
-      tma_tile<D>(first_tile, &P.mq, &q_full, h * D, x.q0 + r0);
-      tma_tile<D>(first_tile + kRows * D * 2, &P.mdo, &q_full, h * D, x.q0 + r0);
-      tma_tile<D>(first_tile + 2 * kRows * D * 2, &P.mo, &q_full, h * D, x.q0 + r0);
-    }
-    q_loaded = true;
-    for (int i = 0; i < n; ++i) {
-      const int s = i % NS, row = i * kStep;
-      // the first tiles' stages
-      if (i == G::kFirst && !warp_wait(&q_ready, 0, abort_p, kAtFlagLoad)) break;
-      if (i >= NS && !warp_wait(&kv_empty[s], (i / NS) - 1, abort_p, kAtFlagLoad)) break;
-      uint8_t* st = smem + s * 2 * G::kTile;
-      const bool tail = row + kStep > x.lk;  // dS is 0 there; K must be finite
-      uint64_t* bar = tail ? &aux : &kv_full[s];
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar, 2 * G::kTile);
-        tma_tile<D, kStep>(st, &P.mk, bar, kh * D, x.k0 + row);
-        tma_tile<D, kStep>(st + G::kTile, &P.mv, bar, kh * D, x.k0 + row);
-      }
-      if (tail) {
-        __syncwarp();
-        if (!tail_landed(&aux, 0, abort_p)) break;
-        zero_rows<D, kStep>(st, x.lk - row);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&kv_full[s]);
-      }
-      last_load = i;
-    }
-  } else if (warp == kMmaWarp && n) {
-    // As in the forward, a condition is tested before the products that
-    // precede its use, and waited for only if that test failed.
-    auto wait = [&](uint64_t* bar, int phase) {
-      return warp_wait(bar, phase, abort_p, kAtFlagMma);
-    };
-    auto stage = [&](int i) { return smem + (i % NS) * 2 * G::kTile; };
-    auto scores = [&](int i) {  // S and dP of step i into their buffer (one thread)
-      const uint32_t b = (i & 1) * kStep;
-      mma_txyt<D, kStep>(tmem + G::kS + b, tmem + G::kQ, stage(i));
-      mma_txyt<D, kStep>(tmem + G::kDp + b, tmem + G::kDo, stage(i) + G::kTile);
-      umma_commit(&s_full[i & 1]);
-    };
-    bool ok = wait(&q_ready, 0);
-    tc_fence_after();
-    for (int i = 0; i < 2 && i < n && ok; ++i) {
-      ok = wait(&kv_full[i % NS], i / NS);
-      if (!ok) break;
-      mma_issued = true;
-      if (elect_one()) scores(i);
-      __syncwarp();
-    }
-    bool ready = false;
-    for (int i = 0; i < n && ok; ++i) {
-      const bool more = i + 2 < n;
-      ok = (!more || wait(&kv_full[(i + 2) % NS], (i + 2) / NS)) &&
-           (ready || wait(&ds_full[i & 1], i >> 1));
-      if (!ok) break;
-      ready = i + 1 < n && mbar_test(&ds_full[(i + 1) & 1], ((i + 1) >> 1) & 1);
-      ready = __all_sync(0xffffffffu, ready);
-      tc_fence_after();
-      // dQ += dS K: 16 keys in the first 8 of every 16 columns of the buffer
-      if (elect_one()) {
-        mma_tay<D, kStep>(tmem + G::kDq, tmem + G::kDp + (i & 1) * kStep, 16, stage(i), i > 0);
-        umma_commit(&kv_empty[i % NS]);
-        if (more) scores(i + 2);
-      }
-      __syncwarp();
-    }
-    if (ok && elect_one()) umma_commit(&done);
-    __syncwarp();
-  } else if (warp < kComputeWarps) {
-    const int part = warp >> 2, q4 = warp & 3, tid = q4 * 32 + lane, row = r0 + tid;
-    const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
-    const bool in = row < x.lq;
-    const int64_t at = static_cast<int64_t>(h) * P.S.Tq + x.q0 + row;
-    {  // this quarter of the row: Q and dO into TMEM, dO . O
-      constexpr int W = D / 8;  // 32-bit words
-      uint32_t qw[W], gw[W];
-      float sum = 0.0f;
-      if (n) warp_wait(&q_full, 0, abort_p, kAtFlagCompute);  // giving up shows in the next wait
-#pragma unroll
-      for (int i = 0; i < W / 4; ++i) {
-        // 16-byte piece of the row in its swizzled box
-        const int piece = part * (D / 32) + i;
-        const uint8_t* at16 = first_tile + (piece >> 3) * kBoxBytes + tid * 128 +
-                              (((piece & 7) ^ (tid & 7)) * 16);
-        uint4 a = make_uint4(0, 0, 0, 0), b = a, c = a;
-        if (n) {
-          a = *reinterpret_cast<const uint4*>(at16);
-          b = *reinterpret_cast<const uint4*>(at16 + kRows * D * 2);
-          c = *reinterpret_cast<const uint4*>(at16 + 2 * kRows * D * 2);
-        }
-        qw[4 * i] = a.x, qw[4 * i + 1] = a.y, qw[4 * i + 2] = a.z, qw[4 * i + 3] = a.w;
-        gw[4 * i] = b.x, gw[4 * i + 1] = b.y, gw[4 * i + 2] = b.z, gw[4 * i + 3] = b.w;
-        const uint32_t ow[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t u = gw[4 * i + e], v = ow[e];
-          sum = __fmaf_rn(__uint_as_float(u << 16), __uint_as_float(v << 16), sum);
-          sum = __fmaf_rn(__uint_as_float(u & 0xFFFF0000u), __uint_as_float(v & 0xFFFF0000u), sum);
-        }
-      }
-      if constexpr (W == 16) {
-        tmem_st16(tmem + G::kQ + part * W + lanes, qw);
-        tmem_st16(tmem + G::kDo + part * W + lanes, gw);
-      } else {
-        tmem_st8(tmem + G::kQ + part * W + lanes, qw);
-        tmem_st8(tmem + G::kDo + part * W + lanes, gw);
-      }
-      dsum[part][tid] = sum;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      // the rows are in registers and TMEM: their stages may be refilled
-      if (lane == 0) mbar_arrive(&q_ready);
-    }
-    bar_compute();
-    const float Dr = (dsum[0][tid] + dsum[1][tid]) + (dsum[2][tid] + dsum[3][tid]);
-    if (in && part == 0) P.D[at] = Dr;
-    const float lse2 = in ? P.lse[at] * kLog2e : 0.0f;
-    const int limit = in ? key_limit(P.S, x, row) : 0;
-    const uint64_t c2 = f32x2_pack(P.c, P.c), l2 = f32x2_pack(-lse2, -lse2),
-                   d2 = f32x2_pack(-Dr, -Dr);
-    const int buf = part >> 1;  // the buffer, and so the steps, of this warp
-    const uint32_t S_p = tmem + G::kS + part * 32 + lanes, dP_p = tmem + G::kDp + part * 32 + lanes;
+  if (warp == kLoadWarp) {
+    uint32_t e = 0, tails = 0;
     bool ok = true;
-    for (int i = buf; i < n; i += 2) {
-      const int lim = limit - i * kStep - (part & 1) * 32;
-      ok = warp_wait(&s_full[buf], i >> 1, abort_p, kAtFlagCompute);
+    // entry e's stage, free: its barrier
+    auto slot_free = [&] {
+      return e < NS || warp_wait(&empty[e % NS], e / NS - 1, abort_p, kAtFlagLoad);
+    };
+    auto rows = [&](const CUtensorMap* map, int col, int row) {  // 128 rows of Q, dO or O
+      ok = ok && slot_free();
+      if (!ok) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[e % NS], 2 * G::kTile);
+        tma_tile<D>(stage(e), map, &full[e % NS], col, row);
+      }
+      loads = ++e;
+    };
+    for (int k = 0; ok; ++k) {
+      // to and fro over the tiles, which get shorter along a sequence
+      const int item = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      PackedTile x;
+      const int h = item % P.H, kh = h / (P.H / P.KV);
+      const bool more = find_tile(P.S, false, item / P.H, kRows, x);
+      const int r0 = x.t * kRows;
+      const int n =
+          more ? (key_limit(P.S, x, min(r0 + kRows, x.lq) - 1) + kStep - 1) / kStep : -1;
+      ok = k < 2 || warp_wait(&tile_empty[k & 1], (k >> 1) - 1, abort_p, kAtFlagLoad);
       if (!ok) break;
-      tc_fence_after();
-      uint32_t s[32];
-      load_quarter(S_p, s);
-      uint64_t p[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        p[e] = ex2_pair<false>(f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, l2));
-      load_quarter(dP_p, s);
-      uint32_t ds[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        ds[e] = f32x2_to_bf16x2(f32x2_mul_rn(
-            p[e], f32x2_add_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), d2)));
-      if (__any_sync(0xffffffffu, lim < 32)) {  // select: what is masked may be infinite or NaN
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          ds[e] &= (2 * e < lim ? 0x0000FFFFu : 0u) | (2 * e + 1 < lim ? 0xFFFF0000u : 0u);
+      if (lane == 0) {
+        tiles[k & 1] = {x.q0, x.lq, x.k0, x.lk, r0, h, n};
+        mbar_arrive(&tile_full[k & 1]);
       }
-      // 16 keys (8 columns) at the start of each 16 columns of the buffer
-      tmem_st8(dP_p, ds);
-      tmem_st8(dP_p + 16, ds + 8);
-      tmem_wait_st();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ds_full[buf]);
-    }
-    if (ok && n) ok = warp_wait(&done, 0, abort_p, kAtFlagCompute);
-    if (ok && part * 32 < D) {
-      tc_fence_after();
-      uint32_t o[32];
-      if (n) {
-        load_quarter(tmem + G::kDq + part * 32 + lanes, o);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0;
+      if (!more) break;
+      if (n == 0) continue;
+      rows(&P.mq, h * D, x.q0 + r0);
+      rows(&P.mdo, h * D, x.q0 + r0);
+      rows(&P.mo, h * D, x.q0 + r0);
+      for (int i = 0; i < n && ok; ++i) {
+        ok = slot_free();
+        if (!ok) break;
+        const int row = i * kStep;
+        const bool tail = row + kStep > x.lk;  // dS is 0 there; K must be finite
+        uint64_t* bar = tail ? &aux : &full[e % NS];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, 2 * G::kTile);
+          tma_tile<D, kStep>(stage(e), &P.mk, bar, kh * D, x.k0 + row);
+          tma_tile<D, kStep>(stage(e) + G::kTile, &P.mv, bar, kh * D, x.k0 + row);
+        }
+        if (tail) {
+          __syncwarp();
+          ok = tail_landed(&aux, tails++ & 1, abort_p);
+          if (!ok) break;
+          zero_rows<D, kStep>(stage(e), x.lk - row);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[e % NS]);
+        }
+        loads = ++e;
       }
-      uint4 v[4];
+    }
+  } else if (warp == kMmaWarp) {
+    // A condition is tested before the products that precede its use, and
+    // waited for only if that test failed: a poll queues behind the products
+    // this warp has issued.
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      return warp_wait(bar, phase & 1, abort_p, kAtFlagMma);
+    };
+    uint32_t e = 0, g = 0, busy = 0;  // ring entries, steps, tiles with steps so far
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      ok = wait(&tile_full[k & 1], k >> 1);
+      if (!ok) break;
+      const int n = tiles[k & 1].n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tile_empty[k & 1]);
+      if (n < 0) break;
+      if (n == 0) continue;
+      e += 3;  // Q, dO, O
+      auto scores = [&](int i) {  // S and dP of step i into their buffer (one thread)
+        const uint32_t b = ((g + i) & 1) * kStep;
+        mma_txyt<D, kStep>(tmem + G::kS + b, tmem + G::kQ, stage(e + i));
+        mma_txyt<D, kStep>(tmem + G::kDp + b, tmem + G::kDo, stage(e + i) + G::kTile);
+        umma_commit(&s_full[(g + i) & 1]);
+      };
+      ok = wait(&q_ready, busy++);
+      tc_fence_after();
+      for (int i = 0; i < 2 && i < n && ok; ++i) {
+        ok = wait(&full[(e + i) % NS], (e + i) / NS);
+        if (!ok) break;
+        mma_issued = true;
+        if (elect_one()) scores(i);
+        __syncwarp();
+      }
+      bool ready = false;
+      for (int i = 0; i < n && ok; ++i) {
+        const bool more = i + 2 < n;
+        const uint32_t gs = g + i;
+        ok = (!more || wait(&full[(e + i + 2) % NS], (e + i + 2) / NS)) &&
+             (ready || wait(&ds_full[gs & 1], gs >> 1));
+        if (!ok) break;
+        ready = i + 1 < n && mbar_test(&ds_full[(gs + 1) & 1], ((gs + 1) >> 1) & 1);
+        ready = __all_sync(0xffffffffu, ready);
+        tc_fence_after();
+        // dQ += dS K: 16 keys in the first 8 of every 16 columns of the buffer
+        if (elect_one()) {
+          mma_tay<D, kStep>(tmem + G::kDq, tmem + G::kDp + (gs & 1) * kStep, 16, stage(e + i),
+                            i > 0);
+          umma_commit(&empty[(e + i) % NS]);
+          if (more) scores(i + 2);
+          if (i + 1 == n) umma_commit(&done);
+        }
+        __syncwarp();
+      }
+      e += n;
+      g += n;
+    }
+  } else if (warp < kComputeWarps) {
+    // a row per four threads: a quarter of its columns at the start and the
+    // end, 32 of its keys in between
+    const int part = warp >> 2, q4 = warp & 3, tid = q4 * 32 + lane, buf = part >> 1;
+    const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t S_p = tmem + G::kS + part * 32 + lanes, dP_p = tmem + G::kDp + part * 32 + lanes;
+    const uint64_t c2 = f32x2_pack(P.c, P.c);
+    uint32_t e = 0, g = 0, busy = 0;
+    bool ok = true;
+    for (int k = 0;; ++k) {
+      // all computing warps go on or leave together: their votes must match
+      ok = ok && warp_wait(&tile_full[k & 1], k >> 1, abort_p, kAtFlagCompute);
+      const DqTile x = tiles[k & 1];
+      if (compute_any(!ok) || x.n < 0) break;
+      const int row = x.r0 + tid, n = x.n;
+      const bool in = row < x.lq;
+      const int64_t at = static_cast<int64_t>(x.h) * P.S.Tq + x.q0 + row;
+      const float lse2 = in ? P.lse[at] * kLog2e : 0.0f;
+      float sum = 0.0f;
+      if (n) {  // this quarter of the row: Q and dO into TMEM, dO . O
+        constexpr int W = D / 8;  // 32-bit words
+        uint32_t qw[W], gw[W];
+        for (int i = 0; i < 3 && ok; ++i)
+          ok = warp_wait(&full[(e + i) % NS], (e + i) / NS, abort_p, kAtFlagCompute);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = pack8_scaled(o + 8 * c, P.scale);
-      const int first = r0 + q4 * 32;  // all products are done: the ring stages the rows
-      put_rows<4>(smem + warp * 2048, v,
-                  P.dq + static_cast<int64_t>(x.q0 + first) * P.dqs + h * D + part * 32,
-                  P.dqs * 2, x.lq - first);
+        for (int i = 0; i < W / 4; ++i) {
+          // 16-byte piece of the row in its swizzled box
+          const int piece = part * (D / 32) + i;
+          const int off = (piece >> 3) * kBoxBytes + tid * 128 + (((piece & 7) ^ (tid & 7)) * 16);
+          const uint4 a = *reinterpret_cast<const uint4*>(stage(e) + off);
+          const uint4 b = *reinterpret_cast<const uint4*>(stage(e + 1) + off);
+          const uint4 c = *reinterpret_cast<const uint4*>(stage(e + 2) + off);
+          qw[4 * i] = a.x, qw[4 * i + 1] = a.y, qw[4 * i + 2] = a.z, qw[4 * i + 3] = a.w;
+          gw[4 * i] = b.x, gw[4 * i + 1] = b.y, gw[4 * i + 2] = b.z, gw[4 * i + 3] = b.w;
+          const uint32_t ow[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t u = gw[4 * i + j], v = ow[j];
+            sum = __fmaf_rn(__uint_as_float(u << 16), __uint_as_float(v << 16), sum);
+            sum = __fmaf_rn(__uint_as_float(u & 0xFFFF0000u), __uint_as_float(v & 0xFFFF0000u),
+                            sum);
+          }
+        }
+        if constexpr (W == 16) {
+          tmem_st16(tmem + G::kQ + part * W + lanes, qw);
+          tmem_st16(tmem + G::kDo + part * W + lanes, gw);
+        } else {
+          tmem_st8(tmem + G::kQ + part * W + lanes, qw);
+          tmem_st8(tmem + G::kDo + part * W + lanes, gw);
+        }
+        dsum[part][tid] = sum;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&q_ready);
+      } else {
+        dsum[part][tid] = 0.0f;
+      }
+      if (compute_any(!ok)) break;
+      // every warp has its rows of Q, dO and O: the stages may be refilled
+      if (n && threadIdx.x < 3) mbar_arrive(&empty[(e + threadIdx.x) % NS]);
+      const float Dr = (dsum[0][tid] + dsum[1][tid]) + (dsum[2][tid] + dsum[3][tid]);
+      if (in && part == 0) P.D[at] = Dr;
+      if (n) {
+        int limit = 0;  // keys that the row sees
+        if (in) limit = P.S.causal ? min(max(row + x.lk - x.lq + 1, 0), x.lk) : x.lk;
+        const uint64_t l2 = f32x2_pack(-lse2, -lse2), d2 = f32x2_pack(-Dr, -Dr);
+        for (int i = (g ^ buf) & 1; i < n; i += 2) {
+          const uint32_t gs = g + i;
+          const int lim = limit - i * kStep - (part & 1) * 32;
+          ok = warp_wait(&s_full[buf], (gs >> 1) & 1, abort_p, kAtFlagCompute);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t s[32];
+          load_quarter(S_p, s);
+          uint64_t p[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            p[j] = ex2_pair<false>(f32x2_fma_rn(f32x2_pack_bits(s[2 * j], s[2 * j + 1]), c2, l2));
+          load_quarter(dP_p, s);
+          uint32_t ds[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            ds[j] = f32x2_to_bf16x2(f32x2_mul_rn(
+                p[j], f32x2_add_rn(f32x2_pack_bits(s[2 * j], s[2 * j + 1]), d2)));
+          if (__any_sync(0xffffffffu, lim < 32)) {  // select: what is masked may be infinite or NaN
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              ds[j] &= (2 * j < lim ? 0x0000FFFFu : 0u) | (2 * j + 1 < lim ? 0xFFFF0000u : 0u);
+          }
+          // 16 keys (8 columns) at the start of each 16 columns of the buffer
+          tmem_st8(dP_p, ds);
+          tmem_st8(dP_p + 16, ds + 8);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ds_full[buf]);
+        }
+        ok = ok && warp_wait(&done, busy++ & 1, abort_p, kAtFlagCompute);
+        tc_fence_after();
+        e += 3 + n;
+        g += n;
+      }
+      if (ok && part * 32 < D) {
+        uint32_t o[32];
+        if (n) {
+          load_quarter(tmem + G::kDq + part * 32 + lanes, o);
+          tc_fence_before();  // the next tile's products come after its q_ready
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0;
+        }
+        uint4 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = pack8_scaled(o + 8 * c, P.scale);
+        const int first = x.r0 + q4 * 32;
+        put_rows<4>(smem + G::kRing + warp * 2048, v,
+                    P.dq + static_cast<int64_t>(x.q0 + first) * P.dqs + x.h * D + part * 32,
+                    P.dqs * 2, x.lq - first);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tile_empty[k & 1]);
     }
   }
 
-  __syncthreads();
+  __syncthreads();  // every thread sees the final abort word
   if (*abort_p && warp == kLoadWarp && lane == 0) {
+    // drain what this CTA started before its shared memory and TMEM go away
     volatile int never = 0;
-    if (q_loaded) mbar_wait(&q_full, 0, &never, &g_attn_flags, kAtFlagDrain);
-    for (int i = max(0, last_load - NS + 1); i <= last_load; ++i)
-      if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+    for (uint32_t i = loads > NS ? loads - NS : 0; i < loads; ++i)
+      if (!mbar_wait(&full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
   }
   if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
     volatile int never = 0;
@@ -1193,11 +1269,12 @@ int head_splits(int64_t Tk, int n_seq, int H, int KV) {
   return static_cast<int>(std::min<int64_t>(H / KV, 2 * ((full + tiles - 1) / tiles)));
 }
 
-// Query tiles per share: an SM's part of them all, were the sequences equal.
+// Query tiles per share: an SM's part of them all, were the sequences equal,
+// and three more, which cost about as much as a share's start and end.
 int share_limit(const hsnf4_packed_attention& a) {
   const int64_t mean = (a.Tq / a.n_seq + kRows - 1) / kRows, tiles = (a.Tk + kRows - 1) / kRows;
-  const int64_t all = a.H * tiles * (a.causal ? (mean + 1) / 2 : mean);
-  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(all / sm_count(), 4), 1 << 30));
+  const int64_t all = a.H * tiles * (a.causal ? mean + 1 : 2 * mean) / 2;
+  return static_cast<int>(std::min<int64_t>(all / sm_count() + 3, 1 << 30));
 }
 
 template <int D>
@@ -1233,8 +1310,9 @@ cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws
   cudaError_t e = allow_smem(packed_dq_tc<D>, DqGeo<D>::kSmem, done_q);
   if (e == cudaSuccess) e = allow_smem(packed_dkdv_tc<D>, BwdGeo<D>::kSmem, done_kv);
   if (e != cudaSuccess) return e;
+  const int64_t items = most_tiles(a.Tq, a.n_seq, kRows) * a.H;
   e = launch_pdl(packed_dq_tc<D>,
-                 dim3(static_cast<unsigned>(most_tiles(a.Tq, a.n_seq, kRows) * a.H)),
+                 dim3(static_cast<unsigned>(std::min<int64_t>(items, sm_count()))),
                  dim3(kTcThreads), DqGeo<D>::kSmem, st, P);
   if (e != cudaSuccess) return e;
   if (!map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride) || !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride))
