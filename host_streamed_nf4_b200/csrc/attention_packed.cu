@@ -48,20 +48,44 @@ constexpr int kTcThreads = 32 * (kComputeWarps + 2);
 constexpr int kMmaWarp = kComputeWarps, kLoadWarp = kComputeWarps + 1;
 constexpr int kPatchWarp = kComputeWarps + 2;  // dK/dV kernel only
 
-// A wait of the whole loading warp, which leaves whole when it gives up.
+// mbar_wait with the abort word and the timer looked at every 32 polls only:
+// reading the timer takes hundreds of cycles, by which each wait ended late.
+__device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          unsigned int site) {
+  const uint32_t a = smem_u32(bar);
+  unsigned long long t0 = 0;
+  for (uint32_t k = 1;; ++k) {
+    if (mbar_try_wait(a, parity)) return true;
+    if (k % 32) continue;
+    if (*abort) return false;
+    const unsigned long long t = global_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) {
+      *abort = 1;
+      atomicOr(&g_attn_flags, site);
+      return false;
+    }
+  }
+}
+
+// A wait of a whole warp, which leaves whole when it gives up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, volatile int* abort,
                                           unsigned int site) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort, &g_attn_flags, site));
+  return __all_sync(0xffffffffu, spin_wait(bar, phase & 1, abort, site));
+}
+
+// Whether the phase has completed, without waiting (whole warp).
+__device__ __forceinline__ bool warp_test(uint64_t* bar, int phase) {
+  return __all_sync(0xffffffffu, mbar_test(bar, phase & 1));
 }
 
 // Wait of the whole loading warp for a tile that it will patch.  Giving up,
 // it first lets the copy land (or the limit pass) before the shared memory
 // goes away.
 __device__ __forceinline__ bool tail_landed(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (__all_sync(0xffffffffu, mbar_wait(bar, parity, abort, &g_attn_flags, kAtFlagLoad)))
-    return true;
+  if (warp_wait(bar, parity, abort, kAtFlagLoad)) return true;
   volatile int never = 0;
-  mbar_wait(bar, parity, &never, &g_attn_flags, kAtFlagDrain);
+  spin_wait(bar, parity, &never, kAtFlagDrain);
   return false;
 }
 
@@ -83,6 +107,11 @@ __device__ __forceinline__ bool pair_any(int id, bool v) {
   return r != 0;
 }
 __device__ __forceinline__ bool pair_all(int id, bool v) { return !pair_any(id, !v); }
+
+template <int THREADS>
+__device__ __forceinline__ void bar_compute() {  // the computing threads
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 // 32 columns of this warp's lanes
 __device__ __forceinline__ void load_quarter(uint32_t taddr, uint32_t* r) {
@@ -200,8 +229,7 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
     q_loaded = true;
     for (int i = 0; i < 2 * n; ++i) {
       const int s = i % NS, row = (i >> 1) * kRows;
-      if (i >= NS && !__all_sync(0xffffffffu, mbar_wait(&kv_empty[s], ((i / NS) - 1) & 1, abort_p,
-                                                         &g_attn_flags, kAtFlagLoad)))
+      if (i >= NS && !warp_wait(&kv_empty[s], (i / NS) - 1, abort_p, kAtFlagLoad))
         break;
       uint8_t* st = ring + s * G::kTile;
       const CUtensorMap* map = (i & 1) ? &P.mv : &P.mk;
@@ -292,7 +320,7 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
     bool ok = true;
     for (int j = 0; j < nt[t]; ++j) {
       // both warps of a row leave together: their barriers must match
-      ok = pair_all(pair, mbar_wait(&s_full[t], j & 1, abort_p, &g_attn_flags, kAtFlagCompute));
+      ok = pair_all(pair, warp_wait(&s_full[t], j, abort_p, kAtFlagCompute));
       if (!ok) break;
       tc_fence_after();
       const int lim = limit - j * kRows - half * 64;
@@ -331,8 +359,7 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
         if (j == 0) {
           ref = m == -INFINITY ? 0.0f : m;  // a row without a key: all 0
         } else {
-          ok = pair_all(pair, mbar_wait(&o_full[t], (j - 1) & 1, abort_p, &g_attn_flags,
-                                        kAtFlagCompute));
+          ok = pair_all(pair, warp_wait(&o_full[t], (j - 1), abort_p, kAtFlagCompute));
           if (!ok) break;
           tc_fence_after();
           const float next = fmaxf(ref, m), f = ex2(ref - next);
@@ -389,8 +416,7 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
       l += a0 + a1;
     }
     if (ok && nt[t])
-      ok = pair_all(pair, mbar_wait(&o_full[t], (nt[t] - 1) & 1, abort_p, &g_attn_flags,
-                                    kAtFlagCompute));
+      ok = pair_all(pair, warp_wait(&o_full[t], (nt[t] - 1), abort_p, kAtFlagCompute));
     if (ok) {
       tc_fence_after();
       row_x[half][t][tid] = l;
@@ -426,14 +452,14 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
   if (*abort_p && warp == kLoadWarp && lane == 0) {
     // drain what this CTA started before its shared memory and TMEM go away
     volatile int never = 0;
-    if (q_loaded) mbar_wait(&q_full, 0, &never, &g_attn_flags, kAtFlagDrain);
+    if (q_loaded) spin_wait(&q_full, 0, &never, kAtFlagDrain);
     for (int i = max(0, last_load - NS + 1); i <= last_load; ++i)
-      if (!mbar_wait(&kv_full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+      if (!spin_wait(&kv_full[i % NS], (i / NS) & 1, &never, kAtFlagDrain)) break;
   }
   if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
     volatile int never = 0;
     umma_commit(&drain);
-    mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
+    spin_wait(&drain, 0, &never, kAtFlagDrain);
   }
   tc_fence_before();
   __syncthreads();
@@ -474,336 +500,261 @@ struct BwdGeo {
 };
 
 // dQ of 128 query rows of one head, the keys 64 at a time: S = Q K^T,
-// dP = dO V^T, dS = P (dP - D) as bf16 over its dP, dQ += dS K.  Q and dO,
-// which every step reads, stay in TMEM as left operands, so that a 64-key
-// product takes 32 cycles per 16 columns (48 with both operands in shared
-// memory).  TMEM: Q, dO (D / 2 columns each), dQ (D), two buffers of S and dP
-// (64 columns each); warps 0..7 take the even steps, 8..15 the odd ones.  The
-// kernel also writes D = dO . O for the dK/dV kernel.
+// dP = dO V^T, dS = P (dP - D) as bf16 over its dP, dQ += dS K.  The kernel
+// also writes D = dO . O for the dK/dV kernel.
 //
-// Persistent: a CTA takes a tile (query tile, head) of every gridDim.x.  One ring of stages runs through all of them (per tile Q, dO, O, then a
-// K and a V tile per step), so the loader, which also finds the tiles, is
-// ahead in the next tile while this one's results are written: 4.8 us of
-// start and end per tile became 1.6.
+// Two CTAs per SM (256 TMEM columns each: dQ, S, dP), so that one's start,
+// end and waits hide behind the other's products: a tile's start and end are
+// about 10000 cycles of latency, as much as eight steps.  S of the next step
+// is computed as soon as the threads have read this one's; its dP follows
+// dQ's product, which reads dS.
 constexpr int kStep = 64;  // keys of a step
 
 template <int D>
 struct DqGeo {
-  static constexpr int kTile = kStep * D * 2;       // K or V of a step; Q, dO, O take two
-  static constexpr int kStages = D == 128 ? 6 : 8;  // of two such tiles
-  static constexpr int kRing = kStages * 2 * kTile;
-  static constexpr int kSmem = kRing + kComputeWarps * 2048;  // and staged rows
-  static constexpr uint32_t kQ = 0, kDo = D / 2, kDq = D, kS = 256, kDp = 384;  // TMEM columns
+  static constexpr int kTile = tile_bytes<D>();  // Q, dO, O: 128 rows
+  static constexpr int kHalf = kStep * D * 2;    // K or V of a step
+  static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 1 : 3;  // stages
+  static constexpr int kSmem = 2 * kTile + (kK + kV) * kHalf;
+  static constexpr int kWarps = 8, kThreads = 32 * (kWarps + 2);
+  static constexpr uint32_t kS = D, kDp = D + kStep, kCols = 256;  // TMEM: dQ, S, dP
 };
-
-// What the loader tells the other warps of a tile; n: its steps, -1: no more.
-struct DqTile {
-  int q0, lq, k0, lk, r0, h, n;
-};
-
-// A vote over the computing threads, which also orders their shared-memory
-// accesses around it.
-__device__ __forceinline__ bool compute_any(bool v) {
-  uint32_t r;
-  __syncwarp();
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "n"(32 * kComputeWarps)
-      : "memory");
-  return r != 0;
-}
 
 template <int D>
-__global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_constant__ BwdTc P) {
+__global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
+    packed_dq_tc(const __grid_constant__ BwdTc P) {
   using G = DqGeo<D>;
-  constexpr int NS = G::kStages;
+  constexpr int NK = G::kK, NV = G::kV, kMmaWarp = G::kWarps, kLoadWarp = G::kWarps + 1;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ uint64_t full[NS], empty[NS], aux, tile_full[2], tile_empty[2], q_ready, s_full[2],
-      ds_full[2], done, drain;
-  __shared__ DqTile tiles[2];
+  __shared__ uint64_t q_full, o_full, o_used, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], aux,
+      s_full, s_free, dp_full, ds_full, done, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ float dsum[4][kRows];
+  __shared__ float row_x[kRows];  // dO . O, exchanged between the two threads of a row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0 && lane == 0) prefetch_maps(P);
+  pdl_wait_then_release();
+  // (before anything is set up: the grid covers the most tiles there could be)
+  PackedTile x;
+  if (!find_tile(P.S, false, blockIdx.x / P.H, kRows, x)) return;
   if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&o_full, 1);
+    mbar_init(&o_used, G::kWarps);
     mbar_init(&aux, 1);
     mbar_init(&drain, 1);
-    mbar_init(&q_ready, kComputeWarps);
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    mbar_init(&s_full, 1);
+    mbar_init(&s_free, G::kWarps);
+    mbar_init(&dp_full, 1);
+    mbar_init(&ds_full, G::kWarps);
     mbar_init(&done, 1);
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&tile_full[b], 1);
-      mbar_init(&tile_empty[b], kComputeWarps + 1);
-      mbar_init(&s_full[b], 1);
-      mbar_init(&ds_full[b], kComputeWarps / 2);
-    }
     abort_flag = 0;
     fence_mbar_init();
-    prefetch_maps(P);
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(&tmem_slot, 512);
+    tmem_alloc(&tmem_slot, G::kCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
+  const uint32_t tmem = tmem_slot;
   volatile int* abort_p = &abort_flag;
-  pdl_wait_then_release();
-  // the swizzled tiles need the alignment asked for
-  if ((smem_u32(smem) & 1023u) || tmem_slot != tmem) {
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need the alignment asked for
     if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
-    if (warp == kMmaWarp) tmem_dealloc(tmem_slot, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, G::kCols);
     return;
   }
-  auto stage = [&](uint32_t e) { return smem + e % NS * (2 * G::kTile); };
-  uint32_t loads = 0;  // ring entries issued (loader)
-  bool mma_issued = false;
+  const int h = blockIdx.x % P.H, kh = h / (P.H / P.KV), r0 = x.t * kRows;
+  const int n = (key_limit(P.S, x, min(r0 + kRows, x.lq) - 1) + kStep - 1) / kStep;
+  int last_k = -1, last_v = -1;
+  bool q_loaded = false, mma_issued = false;
+  uint8_t* const Q = smem;
+  uint8_t* const dO = smem + G::kTile;
+  uint8_t* const Ks = smem + 2 * G::kTile;
+  uint8_t* const Vs = Ks + NK * G::kHalf;
+  uint8_t* const O = Vs - G::kHalf;  // the last K stage and the first V stage, before their use
 
-  if (warp == kLoadWarp) {
-    uint32_t e = 0, tails = 0;
-    bool ok = true;
-    // entry e's stage, free: its barrier
-    auto slot_free = [&] {
-      return e < NS || warp_wait(&empty[e % NS], e / NS - 1, abort_p, kAtFlagLoad);
-    };
-    auto rows = [&](const CUtensorMap* map, int col, int row) {  // 128 rows of Q, dO or O
-      ok = ok && slot_free();
-      if (!ok) return;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[e % NS], 2 * G::kTile);
-        tma_tile<D>(stage(e), map, &full[e % NS], col, row);
-      }
-      loads = ++e;
-    };
-    for (int k = 0; ok; ++k) {
-      // to and fro over the tiles, which get shorter along a sequence
-      const int item = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      PackedTile x;
-      const int h = item % P.H, kh = h / (P.H / P.KV);
-      const bool more = find_tile(P.S, false, item / P.H, kRows, x);
-      const int r0 = x.t * kRows;
-      const int n =
-          more ? (key_limit(P.S, x, min(r0 + kRows, x.lq) - 1) + kStep - 1) / kStep : -1;
-      ok = k < 2 || warp_wait(&tile_empty[k & 1], (k >> 1) - 1, abort_p, kAtFlagLoad);
-      if (!ok) break;
-      if (lane == 0) {
-        tiles[k & 1] = {x.q0, x.lq, x.k0, x.lk, r0, h, n};
-        mbar_arrive(&tile_full[k & 1]);
-      }
-      __syncwarp();
-      if (!more) break;
-      if (n == 0) continue;
-      rows(&P.mq, h * D, x.q0 + r0);
-      rows(&P.mdo, h * D, x.q0 + r0);
-      rows(&P.mo, h * D, x.q0 + r0);
-      for (int i = 0; i < n && ok; ++i) {
-        ok = slot_free();
-        if (!ok) break;
-        const int row = i * kStep;
-        const bool tail = row + kStep > x.lk;  // dS is 0 there; K must be finite
-        uint64_t* bar = tail ? &aux : &full[e % NS];
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar, 2 * G::kTile);
-          tma_tile<D, kStep>(stage(e), &P.mk, bar, kh * D, x.k0 + row);
-          tma_tile<D, kStep>(stage(e) + G::kTile, &P.mv, bar, kh * D, x.k0 + row);
-        }
-        if (tail) {
-          __syncwarp();
-          ok = tail_landed(&aux, tails++ & 1, abort_p);
-          if (!ok) break;
-          zero_rows<D, kStep>(stage(e), x.lk - row);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[e % NS]);
-        }
-        loads = ++e;
-      }
+  if (warp == kLoadWarp && n) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&q_full, 2 * G::kTile);
+      tma_tile<D>(Q, &P.mq, &q_full, h * D, x.q0 + r0);
+      tma_tile<D>(dO, &P.mdo, &q_full, h * D, x.q0 + r0);
+      mbar_arrive_expect_tx(&o_full, G::kTile);
+      tma_tile<D>(O, &P.mo, &o_full, h * D, x.q0 + r0);
     }
-  } else if (warp == kMmaWarp) {
-    // A condition is tested before the products that precede its use, and
-    // waited for only if that test failed: a poll queues behind the products
-    // this warp has issued.
-    auto wait = [&](uint64_t* bar, uint32_t phase) {
-      return warp_wait(bar, phase & 1, abort_p, kAtFlagMma);
+    q_loaded = true;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % NK, v = i % NV, row = i * kStep;
+      if (i == NK - 1 && NK > 1 && i > 0 && !warp_wait(&o_used, 0, abort_p, kAtFlagLoad)) break;
+      if (i >= NK && !warp_wait(&k_empty[s], (i / NK) - 1, abort_p, kAtFlagLoad)) break;
+      const bool tail = row + kStep > x.lk;  // dS is 0 there; K must be finite
+      uint64_t* bar = tail ? &aux : &k_full[s];
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, G::kHalf);
+        tma_tile<D, kStep>(Ks + s * G::kHalf, &P.mk, bar, kh * D, x.k0 + row);
+      }
+      if (tail) {
+        __syncwarp();
+        if (!tail_landed(&aux, 0, abort_p)) break;
+        zero_rows<D, kStep>(Ks + s * G::kHalf, x.lk - row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[s]);
+      }
+      last_k = i;
+      if (i == 0 && !warp_wait(&o_used, 0, abort_p, kAtFlagLoad)) break;
+      if (i >= NV && !warp_wait(&v_empty[v], (i / NV) - 1, abort_p, kAtFlagLoad)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&v_full[v], G::kHalf);
+        tma_tile<D, kStep>(Vs + v * G::kHalf, &P.mv, &v_full[v], kh * D, x.k0 + row);
+      }
+      last_v = i;
+    }
+  } else if (warp == kMmaWarp && n) {
+    auto wait = [&](uint64_t* bar, int phase) {
+      return warp_wait(bar, phase, abort_p, kAtFlagMma);
     };
-    uint32_t e = 0, g = 0, busy = 0;  // ring entries, steps, tiles with steps so far
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      ok = wait(&tile_full[k & 1], k >> 1);
-      if (!ok) break;
-      const int n = tiles[k & 1].n;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tile_empty[k & 1]);
-      if (n < 0) break;
-      if (n == 0) continue;
-      e += 3;  // Q, dO, O
-      auto scores = [&](int i) {  // S and dP of step i into their buffer (one thread)
-        const uint32_t b = ((g + i) & 1) * kStep;
-        mma_txyt<D, kStep>(tmem + G::kS + b, tmem + G::kQ, stage(e + i));
-        mma_txyt<D, kStep>(tmem + G::kDp + b, tmem + G::kDo, stage(e + i) + G::kTile);
-        umma_commit(&s_full[(g + i) & 1]);
-      };
-      ok = wait(&q_ready, busy++);
+    auto scores = [&](int i) {  // S = Q K^T
+      if (!wait(&k_full[i % NK], i / NK)) return false;
+      mma_issued = true;
       tc_fence_after();
-      for (int i = 0; i < 2 && i < n && ok; ++i) {
-        ok = wait(&full[(e + i) % NS], (e + i) / NS);
-        if (!ok) break;
-        mma_issued = true;
-        if (elect_one()) scores(i);
-        __syncwarp();
+      if (elect_one()) {
+        mma_xyt_n<D, kStep>(tmem + G::kS, Q, Ks + (i % NK) * G::kHalf);
+        umma_commit(&s_full);
       }
-      bool ready = false;
-      for (int i = 0; i < n && ok; ++i) {
-        const bool more = i + 2 < n;
-        const uint32_t gs = g + i;
-        ok = (!more || wait(&full[(e + i + 2) % NS], (e + i + 2) / NS)) &&
-             (ready || wait(&ds_full[gs & 1], gs >> 1));
-        if (!ok) break;
-        ready = i + 1 < n && mbar_test(&ds_full[(gs + 1) & 1], ((gs + 1) >> 1) & 1);
-        ready = __all_sync(0xffffffffu, ready);
-        tc_fence_after();
-        // dQ += dS K: 16 keys in the first 8 of every 16 columns of the buffer
-        if (elect_one()) {
-          mma_tay<D, kStep>(tmem + G::kDq, tmem + G::kDp + (gs & 1) * kStep, 16, stage(e + i),
-                            i > 0);
-          umma_commit(&empty[(e + i) % NS]);
-          if (more) scores(i + 2);
-          if (i + 1 == n) umma_commit(&done);
+      __syncwarp();
+      return true;
+    };
+    bool ok = wait(&q_full, 0) && scores(0);
+    for (int i = 0; i < n && ok; ++i) {
+      // dQ += dS K of the step before, then this step's dP = dO V^T
+      ok = wait(&v_full[i % NV], i / NV) && (i == 0 || wait(&ds_full, i - 1));
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        if (i > 0) {
+          mma_ay_n<D, 32, kStep>(tmem, tmem + G::kDp, 32, Ks + ((i - 1) % NK) * G::kHalf, i > 1);
+          umma_commit(&k_empty[(i - 1) % NK]);
         }
-        __syncwarp();
+        mma_xyt_n<D, kStep>(tmem + G::kDp, dO, Vs + (i % NV) * G::kHalf);
+        umma_commit(&dp_full);
+        umma_commit(&v_empty[i % NV]);
       }
-      e += n;
-      g += n;
+      __syncwarp();
+      if (i + 1 < n) ok = wait(&s_free, i) && scores(i + 1);
     }
-  } else if (warp < kComputeWarps) {
-    // a row per four threads: a quarter of its columns at the start and the
-    // end, 32 of its keys in between
-    const int part = warp >> 2, q4 = warp & 3, tid = q4 * 32 + lane, buf = part >> 1;
+    ok = ok && wait(&ds_full, n - 1);
+    tc_fence_after();
+    if (ok && elect_one()) {
+      mma_ay_n<D, 32, kStep>(tmem, tmem + G::kDp, 32, Ks + ((n - 1) % NK) * G::kHalf, n > 1);
+      umma_commit(&done);
+    }
+    __syncwarp();
+  } else if (warp < G::kWarps) {
+    // a row per two threads: half of its columns at the start and the end, 32
+    // of each step's keys in between
+    const int part = warp >> 2, q4 = warp & 3, tid = q4 * 32 + lane, row = r0 + tid;
     const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t S_p = tmem + G::kS + part * 32 + lanes, dP_p = tmem + G::kDp + part * 32 + lanes;
-    const uint64_t c2 = f32x2_pack(P.c, P.c);
-    uint32_t e = 0, g = 0, busy = 0;
+    const bool in = row < x.lq;
+    const int64_t at = static_cast<int64_t>(h) * P.S.Tq + x.q0 + row;
+    const float lse = in ? P.lse[at] : 0.0f;
     bool ok = true;
-    for (int k = 0;; ++k) {
-      // all computing warps go on or leave together: their votes must match
-      ok = ok && warp_wait(&tile_full[k & 1], k >> 1, abort_p, kAtFlagCompute);
-      const DqTile x = tiles[k & 1];
-      if (compute_any(!ok) || x.n < 0) break;
-      const int row = x.r0 + tid, n = x.n;
-      const bool in = row < x.lq;
-      const int64_t at = static_cast<int64_t>(x.h) * P.S.Tq + x.q0 + row;
-      const float lse2 = in ? P.lse[at] * kLog2e : 0.0f;
-      float sum = 0.0f;
-      if (n) {  // this quarter of the row: Q and dO into TMEM, dO . O
-        constexpr int W = D / 8;  // 32-bit words
-        uint32_t qw[W], gw[W];
-        for (int i = 0; i < 3 && ok; ++i)
-          ok = warp_wait(&full[(e + i) % NS], (e + i) / NS, abort_p, kAtFlagCompute);
+    float Dr = 0.0f;
+    if (n) {
+      ok = warp_wait(&q_full, 0, abort_p, kAtFlagCompute) &&
+           warp_wait(&o_full, 0, abort_p, kAtFlagCompute);
+#pragma unroll 2
+      for (int i = 0; i < D / 16; ++i) {  // 16-byte pieces of the row in its swizzled boxes
+        const int piece = part * (D / 16) + i;
+        const int off = (piece >> 3) * kBoxBytes + tid * 128 + (((piece & 7) ^ (tid & 7)) * 16);
+        const uint4 a = *reinterpret_cast<const uint4*>(dO + off);
+        const uint4 b = *reinterpret_cast<const uint4*>(O + off);
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < W / 4; ++i) {
-          // 16-byte piece of the row in its swizzled box
-          const int piece = part * (D / 32) + i;
-          const int off = (piece >> 3) * kBoxBytes + tid * 128 + (((piece & 7) ^ (tid & 7)) * 16);
-          const uint4 a = *reinterpret_cast<const uint4*>(stage(e) + off);
-          const uint4 b = *reinterpret_cast<const uint4*>(stage(e + 1) + off);
-          const uint4 c = *reinterpret_cast<const uint4*>(stage(e + 2) + off);
-          qw[4 * i] = a.x, qw[4 * i + 1] = a.y, qw[4 * i + 2] = a.z, qw[4 * i + 3] = a.w;
-          gw[4 * i] = b.x, gw[4 * i + 1] = b.y, gw[4 * i + 2] = b.z, gw[4 * i + 3] = b.w;
-          const uint32_t ow[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t u = gw[4 * i + j], v = ow[j];
-            sum = __fmaf_rn(__uint_as_float(u << 16), __uint_as_float(v << 16), sum);
-            sum = __fmaf_rn(__uint_as_float(u & 0xFFFF0000u), __uint_as_float(v & 0xFFFF0000u),
-                            sum);
-          }
+        for (int e = 0; e < 4; ++e) {
+          Dr = __fmaf_rn(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), Dr);
+          Dr = __fmaf_rn(__uint_as_float(u[e] & 0xFFFF0000u), __uint_as_float(v[e] & 0xFFFF0000u),
+                         Dr);
         }
-        if constexpr (W == 16) {
-          tmem_st16(tmem + G::kQ + part * W + lanes, qw);
-          tmem_st16(tmem + G::kDo + part * W + lanes, gw);
-        } else {
-          tmem_st8(tmem + G::kQ + part * W + lanes, qw);
-          tmem_st8(tmem + G::kDo + part * W + lanes, gw);
-        }
-        dsum[part][tid] = sum;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(&q_ready);
-      } else {
-        dsum[part][tid] = 0.0f;
       }
-      if (compute_any(!ok)) break;
-      // every warp has its rows of Q, dO and O: the stages may be refilled
-      if (n && threadIdx.x < 3) mbar_arrive(&empty[(e + threadIdx.x) % NS]);
-      const float Dr = (dsum[0][tid] + dsum[1][tid]) + (dsum[2][tid] + dsum[3][tid]);
-      if (in && part == 0) P.D[at] = Dr;
-      if (n) {
-        int limit = 0;  // keys that the row sees
-        if (in) limit = P.S.causal ? min(max(row + x.lk - x.lq + 1, 0), x.lk) : x.lk;
-        const uint64_t l2 = f32x2_pack(-lse2, -lse2), d2 = f32x2_pack(-Dr, -Dr);
-        for (int i = (g ^ buf) & 1; i < n; i += 2) {
-          const uint32_t gs = g + i;
-          const int lim = limit - i * kStep - (part & 1) * 32;
-          ok = warp_wait(&s_full[buf], (gs >> 1) & 1, abort_p, kAtFlagCompute);
-          if (!ok) break;
-          tc_fence_after();
-          uint32_t s[32];
-          load_quarter(S_p, s);
-          uint64_t p[16];
+    }
+    // the halves, added in one order (every computing warp comes here)
+    if (part == 1) row_x[tid] = Dr;
+    bar_compute<32 * G::kWarps>();
+    if (part == 0) row_x[tid] = Dr + row_x[tid];
+    bar_compute<32 * G::kWarps>();
+    Dr = row_x[tid];
+    if (n && lane == 0) mbar_arrive(&o_used);  // (after the barriers: O is read)
+    if (in && part == 0) P.D[at] = Dr;
+    const int limit = in ? key_limit(P.S, x, row) : 0;
+    const float lse2 = lse * kLog2e;
+    const uint64_t c2 = f32x2_pack(P.c, P.c), l2 = f32x2_pack(-lse2, -lse2),
+                   d2 = f32x2_pack(-Dr, -Dr);
+    const uint32_t S_p = tmem + G::kS + part * 32 + lanes, dP_p = S_p + kStep;
+    for (int i = 0; i < n && ok; ++i) {
+      const int lim = limit - i * kStep - part * 32;
+      ok = warp_wait(&s_full, i, abort_p, kAtFlagCompute);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[32];
+      load_quarter(S_p, s);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free);
+      uint64_t p[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            p[j] = ex2_pair<false>(f32x2_fma_rn(f32x2_pack_bits(s[2 * j], s[2 * j + 1]), c2, l2));
-          load_quarter(dP_p, s);
-          uint32_t ds[16];
+      for (int e = 0; e < 16; ++e)
+        p[e] = ex2_pair<false>(f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, l2));
+      ok = warp_wait(&dp_full, i, abort_p, kAtFlagCompute);
+      if (!ok) break;
+      tc_fence_after();
+      load_quarter(dP_p, s);
+      uint32_t ds[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            ds[j] = f32x2_to_bf16x2(f32x2_mul_rn(
-                p[j], f32x2_add_rn(f32x2_pack_bits(s[2 * j], s[2 * j + 1]), d2)));
-          if (__any_sync(0xffffffffu, lim < 32)) {  // select: what is masked may be infinite or NaN
+      for (int e = 0; e < 16; ++e)
+        ds[e] = f32x2_to_bf16x2(f32x2_mul_rn(
+            p[e], f32x2_add_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), d2)));
+      if (__any_sync(0xffffffffu, lim < 32)) {  // select: what is masked may be infinite or NaN
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              ds[j] &= (2 * j < lim ? 0x0000FFFFu : 0u) | (2 * j + 1 < lim ? 0xFFFF0000u : 0u);
-          }
-          // 16 keys (8 columns) at the start of each 16 columns of the buffer
-          tmem_st8(dP_p, ds);
-          tmem_st8(dP_p + 16, ds + 8);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ds_full[buf]);
-        }
-        ok = ok && warp_wait(&done, busy++ & 1, abort_p, kAtFlagCompute);
-        tc_fence_after();
-        e += 3 + n;
-        g += n;
+        for (int e = 0; e < 16; ++e)
+          ds[e] &= (2 * e < lim ? 0x0000FFFFu : 0u) | (2 * e + 1 < lim ? 0xFFFF0000u : 0u);
       }
-      if (ok && part * 32 < D) {
+      tmem_st16(dP_p, ds);  // over the first half of this thread's columns
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full);
+    }
+    if (ok && n) ok = warp_wait(&done, 0, abort_p, kAtFlagCompute);
+    if (ok) {
+      tc_fence_after();
+      // all products are done: Q's shared memory stages the rows
+      const int first = r0 + q4 * 32;
+      uint4 v[D / 16];
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) {
         uint32_t o[32];
         if (n) {
-          load_quarter(tmem + G::kDq + part * 32 + lanes, o);
-          tc_fence_before();  // the next tile's products come after its q_ready
+          load_quarter(tmem + part * (D / 2) + 32 * b + lanes, o);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0;
+          for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        uint4 v[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = pack8_scaled(o + 8 * c, P.scale);
-        const int first = x.r0 + q4 * 32;
-        put_rows<4>(smem + G::kRing + warp * 2048, v,
-                    P.dq + static_cast<int64_t>(x.q0 + first) * P.dqs + x.h * D + part * 32,
-                    P.dqs * 2, x.lq - first);
+        for (int c = 0; c < 4; ++c) v[4 * b + c] = pack8_scaled(o + 8 * c, P.scale);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tile_empty[k & 1]);
+      put_rows<D / 16>(Q + warp * (32 * D), v,
+                       P.dq + static_cast<int64_t>(x.q0 + first) * P.dqs + h * D + part * (D / 2),
+                       P.dqs * 2, x.lq - first);
     }
   }
 
@@ -811,19 +762,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) packed_dq_tc(const __grid_const
   if (*abort_p && warp == kLoadWarp && lane == 0) {
     // drain what this CTA started before its shared memory and TMEM go away
     volatile int never = 0;
-    for (uint32_t i = loads > NS ? loads - NS : 0; i < loads; ++i)
-      if (!mbar_wait(&full[i % NS], (i / NS) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+    if (q_loaded) {
+      spin_wait(&q_full, 0, &never, kAtFlagDrain);
+      spin_wait(&o_full, 0, &never, kAtFlagDrain);
+    }
+    for (int i = max(0, last_k - NK + 1); i <= last_k; ++i)
+      if (!spin_wait(&k_full[i % NK], (i / NK) & 1, &never, kAtFlagDrain)) break;
+    for (int i = max(0, last_v - NV + 1); i <= last_v; ++i)
+      if (!spin_wait(&v_full[i % NV], (i / NV) & 1, &never, kAtFlagDrain)) break;
   }
   if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
     volatile int never = 0;
     umma_commit(&drain);
-    mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
+    spin_wait(&drain, 0, &never, kAtFlagDrain);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, G::kCols);
   }
 }
 
@@ -1002,9 +959,6 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
     auto wait = [&](uint64_t* bar, int phase) {
       return warp_wait(bar, phase, abort_p, kAtFlagMma);
     };
-    auto test = [&](uint64_t* bar, int phase) {
-      return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0;
-    };
     auto Q = [&](int i) { return ring + (i % NA) * G::kTile; };
     auto dO = [&](int i) { return ring + (NA + i % NB) * G::kTile; };
     auto scores = [&](int i) {  // S^T = K Q^T (one thread)
@@ -1029,7 +983,7 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
       const bool more = i + 1 < n;
       ok = (!more || q_in || wait(&q_full[(i + 1) % NA], (i + 1) / NA)) && wait(&p_full, i);
       if (!ok) break;
-      const bool do_in = more && test(&do_full[(i + 1) % NB], (i + 1) / NB);
+      const bool do_in = more && warp_test(&do_full[(i + 1) % NB], (i + 1) / NB);
       tc_fence_after();
       if (elect_one()) {
         mma_ay<D, 32>(tmem + 256, tmem, 32, dO(i), i > 0);  // dV += P^T dO
@@ -1039,7 +993,7 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
       __syncwarp();
       ok = (!more || do_in || wait(&do_full[(i + 1) % NB], (i + 1) / NB)) && wait(&ds_full, i);
       if (!ok) break;
-      q_in = i + 2 < n && test(&q_full[(i + 2) % NA], (i + 2) / NA);
+      q_in = i + 2 < n && warp_test(&q_full[(i + 2) % NA], (i + 2) / NA);
       tc_fence_after();
       if (elect_one()) {
         mma_ay<D, 32>(tmem + 256 + D, tmem + 128, 32, Q(i), i > 0);  // dK += dS^T Q
@@ -1161,16 +1115,16 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
   __syncthreads();
   if (*abort_p && warp == kLoadWarp && lane == 0) {
     volatile int never = 0;
-    if (kv_loaded) mbar_wait(&kv_full, 0, &never, &g_attn_flags, kAtFlagDrain);
+    if (kv_loaded) spin_wait(&kv_full, 0, &never, kAtFlagDrain);
     for (int i = max(0, last_a - NA + 1); i <= last_a; ++i)
-      if (!mbar_wait(&q_full[i % NA], (i / NA) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+      if (!spin_wait(&q_full[i % NA], (i / NA) & 1, &never, kAtFlagDrain)) break;
     for (int i = max(0, last_b - NB + 1); i <= last_b; ++i)
-      if (!mbar_wait(&do_full[i % NB], (i / NB) & 1, &never, &g_attn_flags, kAtFlagDrain)) break;
+      if (!spin_wait(&do_full[i % NB], (i / NB) & 1, &never, kAtFlagDrain)) break;
   }
   if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
     volatile int never = 0;
     umma_commit(&drain);
-    mbar_wait(&drain, 0, &never, &g_attn_flags, kAtFlagDrain);
+    spin_wait(&drain, 0, &never, kAtFlagDrain);
   }
   tc_fence_before();
   __syncthreads();
@@ -1310,10 +1264,9 @@ cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws
   cudaError_t e = allow_smem(packed_dq_tc<D>, DqGeo<D>::kSmem, done_q);
   if (e == cudaSuccess) e = allow_smem(packed_dkdv_tc<D>, BwdGeo<D>::kSmem, done_kv);
   if (e != cudaSuccess) return e;
-  const int64_t items = most_tiles(a.Tq, a.n_seq, kRows) * a.H;
   e = launch_pdl(packed_dq_tc<D>,
-                 dim3(static_cast<unsigned>(std::min<int64_t>(items, sm_count()))),
-                 dim3(kTcThreads), DqGeo<D>::kSmem, st, P);
+                 dim3(static_cast<unsigned>(most_tiles(a.Tq, a.n_seq, kRows) * a.H)),
+                 dim3(DqGeo<D>::kThreads), DqGeo<D>::kSmem, st, P);
   if (e != cudaSuccess) return e;
   if (!map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride) || !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride))
     return cudaErrorInvalidValue;

@@ -67,30 +67,28 @@ __device__ __forceinline__ void mma_ay(uint32_t d, uint32_t a, uint32_t stride, 
                  y0 + ((k * 2048) >> 4), idesc, accumulate || k > 0 ? 1u : 0u);
 }
 
-// d[128 x N] = X Y^T over the D columns of a head: X is bf16 in tensor memory
-// (16 columns of the head to 8 TMEM columns), Y a tile of N tokens in boxes of
-// N rows.
+// The two products with a tile of N tokens (boxes of N rows) as the right
+// operand: d[128 x N] = X Y^T, and d[128 x D] (+)= A Y with A as in mma_ay.
 template <int D, int N>
-__device__ __forceinline__ void mma_txyt(uint32_t d, uint32_t x, const uint8_t* Y) {
+__device__ __forceinline__ void mma_xyt_n(uint32_t d, const uint8_t* X, const uint8_t* Y) {
+  const uint64_t x0 = make_sdesc(smem_u32(X), 16, 1024, kLayoutSw128);
   const uint64_t y0 = make_sdesc(smem_u32(Y), 16, 1024, kLayoutSw128);
   constexpr uint32_t idesc = make_idesc_bf16(kRows, N, 0, 0);
 #pragma unroll
   for (int k = 0; k < D / 16; ++k)
-    umma_bf16_ta(d, x + 8 * k, y0 + (((k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc,
-                 k > 0 ? 1u : 0u);
+    umma_bf16(d, x0 + (((k / 4) * kBoxBytes + (k % 4) * 32) >> 4),
+              y0 + (((k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc, k > 0 ? 1u : 0u);
 }
 
-// d[128 x D] (+)= A Y over the N tokens of such a tile; A is bf16 in tensor
-// memory, 16 tokens to 8 columns, `stride` columns from one 16 to the next.
-template <int D, int N>
-__device__ __forceinline__ void mma_tay(uint32_t d, uint32_t a, uint32_t stride, const uint8_t* Y,
-                                        bool accumulate) {
+template <int D, int GROUP, int N>
+__device__ __forceinline__ void mma_ay_n(uint32_t d, uint32_t a, uint32_t stride, const uint8_t* Y,
+                                         bool accumulate) {
   const uint64_t y0 = make_sdesc(smem_u32(Y), N * 128, 1024, kLayoutSw128);
   constexpr uint32_t idesc = make_idesc_bf16(kRows, D, 0, 1);
 #pragma unroll
   for (int k = 0; k < N / 16; ++k)
-    umma_bf16_ta(d, a + k * stride, y0 + ((k * 2048) >> 4), idesc,
-                 accumulate || k > 0 ? 1u : 0u);
+    umma_bf16_ta(d, a + (k * 16 / GROUP) * stride + (k * 16 % GROUP) / 2,
+                 y0 + ((k * 2048) >> 4), idesc, accumulate || k > 0 ? 1u : 0u);
 }
 
 // Part of mma_ay: the 16-token steps `first`, `first` + 1 ... of every group
