@@ -10,8 +10,8 @@
 //   dS_ij = P_ij (dout_i . v_j - D_i)
 //   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dout
 // Scores, statistics and sums are fp32; P and dS are rounded to bf16 as
-// operands of the second products (2^-9 relative, the size of the outputs'
-// own rounding).
+// operands of the second products (2^-8 relative at most, the size of the
+// outputs' own rounding).
 //
 // No atomics: dQ and dK/dV come from two kernels that each recompute P (seven
 // products where five would do with unordered additions), and heads that
@@ -22,7 +22,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "attention_tc.cuh"
 #include "internal.h"
@@ -347,8 +346,6 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
       // (a row behind the sequence holds another's values and has no say)
       const float mt = row < x.lq ? max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3])) * P.c
                                   : -INFINITY;
-      // a NaN or an infinite score: the polynomial would not keep it
-      const bool odd = __any_sync(0xffffffffu, !(mt < INFINITY));
       // The reference of a row's exponentials moves only when a score passes
       // it by 2^8 (fp32 sums and bf16 probabilities lose nothing at that
       // size); then O and the sum are scaled to the new one.
@@ -389,22 +386,13 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
       for (int b = 0; b < 2; ++b) {
         uint32_t s[32], p[16];
         scores(b, s);
-        auto probs = [&](auto poly) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t y =
-                f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, r2);
-            const uint64_t pr = decltype(poly)::value && e % kPolyOf < kPolyPart
-                                    ? ex2_pair<true>(y)
-                                    : ex2_pair<false>(y);
-            sum[e & 1] = f32x2_add_rn(sum[e & 1], pr);
-            p[e] = f32x2_to_bf16x2(pr);
-          }
-        };
-        if (odd)
-          probs(std::false_type());
-        else
-          probs(std::true_type());
+        for (int e = 0; e < 16; ++e) {
+          const uint64_t y = f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, r2);
+          const uint64_t pr = e % kPolyOf < kPolyPart ? ex2_poly<false>(y) : ex2_pair(y);
+          sum[e & 1] = f32x2_add_rn(sum[e & 1], pr);
+          p[e] = f32x2_to_bf16x2(pr);
+        }
         tmem_st16(S_h + 16 * b, p);
         tmem_wait_st();
         tc_fence_before();
@@ -414,6 +402,8 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
       float a0, a1;
       f32x2_unpack(f32x2_add_rn(sum[0], sum[1]), a0, a1);
       l += a0 + a1;
+      // a NaN or an infinite score makes the row NaN (the polynomial gives 0 for it)
+      if (!(mt < INFINITY)) l = NAN;
     }
     if (ok && nt[t])
       ok = pair_all(pair, warp_wait(&o_full[t], (nt[t] - 1), abort_p, kAtFlagCompute));
@@ -594,7 +584,6 @@ __global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
     q_loaded = true;
     for (int i = 0; i < n; ++i) {
       const int s = i % NK, v = i % NV, row = i * kStep;
-      if (i == NK - 1 && NK > 1 && i > 0 && !warp_wait(&o_used, 0, abort_p, kAtFlagLoad)) break;
       if (i >= NK && !warp_wait(&k_empty[s], (i / NK) - 1, abort_p, kAtFlagLoad)) break;
       const bool tail = row + kStep > x.lk;  // dS is 0 there; K must be finite
       uint64_t* bar = tail ? &aux : &k_full[s];
@@ -611,6 +600,7 @@ __global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
         if (lane == 0) mbar_arrive(&k_full[s]);
       }
       last_k = i;
+      // O lies in the last K stage (used from i = NK - 1 on) and the first V stage
       if (i == 0 && !warp_wait(&o_used, 0, abort_p, kAtFlagLoad)) break;
       if (i >= NV && !warp_wait(&v_empty[v], (i / NV) - 1, abort_p, kAtFlagLoad)) break;
       if (lane == 0) {
@@ -713,7 +703,7 @@ __global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
       uint64_t p[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        p[e] = ex2_pair<false>(f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, l2));
+        p[e] = ex2_pair(f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, l2));
       ok = warp_wait(&dp_full, i, abort_p, kAtFlagCompute);
       if (!ok) break;
       tc_fence_after();
@@ -1042,8 +1032,8 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
         const ulonglong2 l4 = ls[e / 2];
         const uint64_t y0 = f32x2_fma_rn(f32x2_pack_bits(v[2 * e], v[2 * e + 1]), c2, l4.x);
         const uint64_t y1 = f32x2_fma_rn(f32x2_pack_bits(v[2 * e + 2], v[2 * e + 3]), c2, l4.y);
-        p[e] = e % kPolyOf < kPolyPart ? ex2_pair<true>(y0) : ex2_pair<false>(y0);
-        p[e + 1] = (e + 1) % kPolyOf < kPolyPart ? ex2_pair<true>(y1) : ex2_pair<false>(y1);
+        p[e] = e % kPolyOf < kPolyPart ? ex2_poly<true>(y0) : ex2_pair(y0);
+        p[e + 1] = (e + 1) % kPolyOf < kPolyPart ? ex2_poly<true>(y1) : ex2_pair(y1);
         w[e] = f32x2_to_bf16x2(p[e]);
         w[e + 1] = f32x2_to_bf16x2(p[e + 1]);
       }

@@ -114,14 +114,17 @@ __device__ __forceinline__ void mma_ay_steps(uint32_t d, uint32_t a, uint32_t st
 // 2^x of two values at once on the fp32 pipe: x = n + f with n the nearest
 // integer (Cody and Waite's reduction), 2^f by a polynomial of degree 4 that
 // is 1 at f = 0 and minimises the relative error on [-1/2, 1/2] (2.9e-6 in
-// fp32; found by linear programming), n added to the exponent.  Below 2^-126
-// the result is 0.  The special-function unit gives 16 results per clock and
-// SM, half of what the tensor cores need beside it, so a share of the
-// exponentials goes this way.
+// fp32; found by linear programming), times 2^n.  x below -127 gives 0; x must
+// be below 128.  KEEP_NAN: NaN stays NaN (it goes through every step but 2^n),
+// for one product more; else it gives 0.
+// The special-function unit gives 16 results per clock and SM, half of what
+// the tensor cores need beside it, so a share of the exponentials goes this way.
+template <bool KEEP_NAN>
 __device__ __forceinline__ uint64_t ex2_poly(uint64_t x) {
   float a, b;
   f32x2_unpack(x, a, b);
-  const uint64_t y = f32x2_pack(fmaxf(a, -127.0f), fmaxf(b, -127.0f));
+  const uint64_t y = KEEP_NAN ? f32x2_pack(max_nan(a, -127.0f), max_nan(b, -127.0f))
+                              : f32x2_pack(fmaxf(a, -127.0f), fmaxf(b, -127.0f));
   const float magic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
   const uint64_t t = f32x2_add_rn(y, f32x2_pack(magic, magic));
   const uint64_t n = f32x2_add_rn(t, f32x2_pack(-magic, -magic));
@@ -134,14 +137,15 @@ __device__ __forceinline__ uint64_t ex2_poly(uint64_t x) {
   float t0, t1, p0, p1;
   f32x2_unpack(t, t0, t1);
   f32x2_unpack(p, p0, p1);
-  return f32x2_pack_bits(__float_as_uint(p0) + (__float_as_uint(t0) << 23),
-                         __float_as_uint(p1) + (__float_as_uint(t1) << 23));
+  if (!KEEP_NAN)  // n added to the exponent
+    return f32x2_pack_bits(__float_as_uint(p0) + (__float_as_uint(t0) << 23),
+                           __float_as_uint(p1) + (__float_as_uint(t1) << 23));
+  return f32x2_mul_rn(p, f32x2_pack_bits((__float_as_uint(t0) << 23) + 0x3F800000u,
+                                         (__float_as_uint(t1) << 23) + 0x3F800000u));
 }
 
-// 2^x of two values, on the special-function unit or the fp32 pipe
-template <bool POLY>
+// 2^x of two values on the special-function unit
 __device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
-  if (POLY) return ex2_poly(x);
   float a, b;
   f32x2_unpack(x, a, b);
   return f32x2_pack(ex2(a), ex2(b));

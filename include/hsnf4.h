@@ -469,7 +469,10 @@ int decoder_rope_bwd(const hsnf4_rope *rope, const int32_t *pos, int64_t T, int 
  * that no query sees gets zero gradients.  Rows outside every sequence are
  * neither read into a result nor written.  Products take bf16 operands with
  * fp32 accumulation (the probabilities and their gradients are rounded to
- * bf16 as operands); softmax statistics are fp32. */
+ * bf16 as operands); softmax statistics are fp32.  A value that is not finite
+ * reaches every result that the formulas give it a part in, and may reach
+ * others of its own sequence and KV head (a causal mask makes factors 0, and
+ * 0 times it is NaN), never those of another sequence or KV head. */
 typedef struct {
   const void *q, *k, *v;  /* bf16; heads contiguous within a token */
   int64_t q_stride, k_stride, v_stride; /* elements between tokens (multiples

@@ -301,6 +301,45 @@ def test_packed_attention_sequences_do_not_meet():
         assert torch.equal(x[:a], y[:a]) and torch.equal(x[b:], y[b:])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [NAN, float("inf")])
+def test_packed_attention_keeps_what_is_not_finite(d, value):
+    """A query, and a key, with a NaN or infinite value: every result that
+    the formula makes NaN is NaN, rows that do not see it stay as they were."""
+    H, KV, lens = 4, 2, [40, 200]
+    q, k, v, do = _attn_inputs(lens, lens, H, KV, d, "plain", 5)
+    cu = _cu(lens)
+
+    def all_of(q, k):
+        o, lse = hsnf4.attention_packed_fwd(q, k, v, cu, H, KV)
+        return [o, lse.T.contiguous()] + list(
+            hsnf4.attention_packed_bwd(q, k, v, o, lse, do, cu, H, KV))
+
+    good = all_of(q, k)
+    for i in range(131, 163):  # all 32 columns that a thread may hold it in
+        bad_q = q.clone()
+        bad_q[i, d + 3] = value  # head 1, of KV head 0; its scores are infinite or NaN
+        o, lse, dq, dk, dv = all_of(bad_q, k)
+        torch.cuda.synchronize()
+        assert o[i, d:2 * d].isnan().all() and dq[i, d:2 * d].isnan().all()
+        assert dk[40:i + 1, :d].isnan().all() and dv[40:i + 1, :d].isnan().all()
+        for x, y, n in ((o, good[0], H), (lse, good[1], H), (dq, good[2], H)):
+            same = (x == y).reshape(240, n, -1)
+            same[i, 1] = True
+            assert same.all()
+        assert torch.equal(dk[:, d:], good[3][:, d:]) and torch.equal(dv[:, d:], good[4][:, d:])
+        assert torch.equal(dk[:40], good[3][:40]) and torch.equal(dv[:40], good[4][:40])
+        assert torch.equal(dv[i + 1:, :d], good[4][i + 1:, :d])
+    bad_k = k.clone()
+    bad_k[140, :d] = NAN
+    o, lse, dq, dk, dv = all_of(q, bad_k)
+    torch.cuda.synchronize()
+    assert o[140:, :2 * d].isnan().all() and lse[140:, :2].isnan().all()
+    assert dq[140:, :2 * d].isnan().all() and dk[140, :d].isnan().all()
+    assert torch.equal(o[:140], good[0][:140]) and torch.equal(lse[:140], good[1][:140])
+    assert dv[40:, :d].isnan().all()  # each of these keys is seen by a query from 140 on
+
+
 def test_packed_attention_malformed_lengths_stay_in_bounds():
     """Cumulative lengths out of order or range are clamped to the tensors;
     what they select is unspecified, what lies outside is untouched."""
