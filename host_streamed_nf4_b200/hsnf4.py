@@ -508,7 +508,11 @@ def _rows(t: torch.Tensor, name: str, index: int, shape) -> int:
     s0, s1 = t.stride()
     if s1 != 1 and shape[1] != 1:
         _bad(t, name, _bf16, index, f"{shape} with contiguous rows")
-    return s0 if shape[0] > 1 else shape[1]
+    if shape[0] <= 1:
+        return shape[1]
+    if s0 < shape[1]:  # an expanded tensor: stride 0 would mean contiguous rows
+        _bad(t, name, _bf16, index, f"{shape} with rows that do not overlap")
+    return s0
 
 
 def _plain(t: torch.Tensor, name: str, index: int, dtype, numel: int) -> int:

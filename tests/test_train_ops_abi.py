@@ -17,6 +17,18 @@ def _refused(rc, status, *words):
         assert w in hsnf4.last_error(), hsnf4.last_error()
 
 
+def test_rows_that_overlap_are_refused():
+    """An expanded tensor has row stride 0, which the library reads as
+    contiguous rows: it would leave the tensor's memory."""
+    one = torch.zeros(1, 64, dtype=torch.bfloat16)
+    assert hsnf4._rows(one, "q", -1, (1, 64)) == 64
+    wide = torch.zeros(5, 96, dtype=torch.bfloat16)
+    assert hsnf4._rows(wide[:, 16:80], "q", -1, (5, 64)) == 96
+    for t in (one.expand(5, 64), wide.view(-1).as_strided((5, 64), (32, 1))):
+        with pytest.raises(ValueError, match="q must be"):
+            hsnf4._rows(t, "q", -1, (5, 64))
+
+
 # ---------------------------------------------------------------- rotary positions
 
 def _rope(**kw):
