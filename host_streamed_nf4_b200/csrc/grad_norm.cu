@@ -308,8 +308,10 @@ cudaError_t fill_grad_table(const hsnf4_grad* grads, int n, void* table, int64_t
     if (g.n) c += (bytes + shift + kChunkBytes - 1) / kChunkBytes;
   }
   *chunks = c;
-  // pageable source: the copy has left it when the call returns
-  return cudaMemcpyAsync(table, e.get(), grad_table_bytes(n), cudaMemcpyHostToDevice, st);
+  const cudaError_t rc =
+      cudaMemcpyAsync(table, e.get(), grad_table_bytes(n), cudaMemcpyHostToDevice, st);
+  // the plan may be used on any stream from here on
+  return rc != cudaSuccess ? rc : cudaStreamSynchronize(st);
 }
 
 cudaError_t launch_grad_norm(const void* table, int n, int64_t chunks, float max_norm, bool scale,

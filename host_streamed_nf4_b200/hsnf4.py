@@ -492,6 +492,16 @@ def _launch(index: int, stream, fn, *args):
         raise HsNf4Error(rc, last_error())
 
 
+def _new(make, shape, dtype, device, stream):
+    """A tensor that a call on `stream` will write, made and owned there: on
+    the current stream its filling could come after the call, and its memory
+    be handed on before it."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def _bad(t, name, dtype, index, shape):
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor, got {t.dtype}")
@@ -567,7 +577,7 @@ def _rope(fn, rope, pos, q, k, q_out, k_out, stream):
         raise ValueError(f"q has {wq} columns, not a multiple of {d}")
     p = _plain(pos, "pos", dev, _i32, rope.n_axes * T)
     if q_out is None:
-        q_out = torch.empty(shape, dtype=_bf16, device=q.device)
+        q_out = _new(torch.empty, shape, _bf16, q.device, stream)
     qs, qos = _rows(q, "q", dev, shape), _rows(q_out, "q_out", dev, shape)
     if k is None:
         _launch(dev, stream, fn, rope._ref, p, T, wq // d, 0, q.data_ptr(), qs, None, 0,
@@ -578,7 +588,7 @@ def _rope(fn, rope, pos, q, k, q_out, k_out, stream):
     if wk % d:
         raise ValueError(f"k has {wk} columns, not a multiple of {d}")
     if k_out is None:
-        k_out = torch.empty(shape, dtype=_bf16, device=q.device)
+        k_out = _new(torch.empty, shape, _bf16, q.device, stream)
     ks, kos = _rows(k, "k", dev, shape), _rows(k_out, "k_out", dev, shape)
     _launch(dev, stream, fn, rope._ref, p, T, wq // d, wk // d, q.data_ptr(), qs, k.data_ptr(), ks,
             q_out.data_ptr(), qos, k_out.data_ptr(), kos)
@@ -628,9 +638,9 @@ def attention_packed_fwd(q, k, v, cu_q, H, KV, causal=True, cu_k=None, scale=Non
     dev, sq, _, _, a = _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale)
     Tq = sq[0]
     if o is None:
-        o = torch.zeros(sq, dtype=_bf16, device=q.device)
+        o = _new(torch.zeros, sq, _bf16, q.device, stream)
     if lse is None:
-        lse = torch.zeros((H, Tq), dtype=_f32, device=q.device)
+        lse = _new(torch.zeros, (H, Tq), _f32, q.device, stream)
     _launch(dev, stream, lib().decoder_attention_packed_fwd, ctypes.byref(a), o.data_ptr(),
             _rows(o, "o", dev, sq), _plain(lse, "lse", dev, _f32, H * Tq))
     return o, lse
@@ -648,14 +658,13 @@ def attention_packed_bwd(q, k, v, o, lse, dout, cu_q, H, KV, causal=True, cu_k=N
     """Its gradients from the forward's o and lse: (dq, dk, dv).  Rows outside
     every sequence are left as they are."""
     dev, sq, sk, d, a = _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale)
-    dq = torch.zeros(sq, dtype=_bf16, device=q.device) if dq is None else dq
-    dk = torch.zeros(sk, dtype=_bf16, device=q.device) if dk is None else dk
-    dv = torch.zeros(sk, dtype=_bf16, device=q.device) if dv is None else dv
+    dq = _new(torch.zeros, sq, _bf16, q.device, stream) if dq is None else dq
+    dk = _new(torch.zeros, sk, _bf16, q.device, stream) if dk is None else dk
+    dv = _new(torch.zeros, sk, _bf16, q.device, stream) if dv is None else dv
     if workspace is None:
         with torch.cuda.device(dev):
-            workspace = torch.empty(
-                attention_packed_workspace_bytes(sq[0], sk[0], a.n_seq, H, KV, d),
-                dtype=torch.uint8, device=q.device)
+            n = attention_packed_workspace_bytes(sq[0], sk[0], a.n_seq, H, KV, d)
+        workspace = _new(torch.empty, n, torch.uint8, q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     _launch(dev, stream, lib().decoder_attention_packed_bwd, ctypes.byref(a), o.data_ptr(),
@@ -696,24 +705,24 @@ class GradSet:
             c.g, c.out, c.n, c.dtype = g.data_ptr(), o.data_ptr(), n, t
         self.device, self.index, self.plan = dev, index, GradPlanC()
         n = len(self.tensors)
-        self.table = torch.empty(int(lib().lora_grad_table_bytes(n)) or 16, dtype=torch.uint8,
-                                 device=dev)
+        self.table = _new(torch.empty, int(lib().lora_grad_table_bytes(n)) or 16, torch.uint8, dev,
+                          stream)
         _launch(index, stream, lambda *a: lib().lora_grad_plan(arr, n, self.table.data_ptr(),
                                                                self.table.numel(),
                                                                ctypes.byref(self.plan), *a))
-        self.workspace = self.new_workspace()
+        self.workspace = self.new_workspace(stream)
         self._ref = ctypes.byref(self.plan)
 
-    def new_workspace(self) -> torch.Tensor:
-        """A workspace for calls that may run at the same time as others on
-        this set (which otherwise share its own)."""
+    def new_workspace(self, stream=None) -> torch.Tensor:
+        """A workspace for calls on `stream` that may run at the same time as
+        others on this set (which otherwise share its own)."""
         with torch.cuda.device(self.index):
-            return torch.empty(int(lib().lora_grad_workspace(ctypes.byref(self.plan))),
-                               dtype=torch.uint8, device=self.device)
+            n = int(lib().lora_grad_workspace(ctypes.byref(self.plan)))
+        return _new(torch.empty, n, torch.uint8, self.device, stream)
 
     def _call(self, fn, args, norm, workspace, stream):
         if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=self.device)
+            norm = _new(torch.empty, (), _f32, self.device, stream)
         ws = self.workspace if workspace is None else workspace
         if workspace is not None and (ws.get_device() != self.index or not ws.is_contiguous()):
             raise ValueError(f"workspace must be a contiguous tensor on {self.device}")

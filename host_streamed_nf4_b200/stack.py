@@ -387,8 +387,6 @@ class LayerStack:
         gradients are summed."""
         if self._grad_set is None:
             self._grad_set = hsnf4.GradSet([self.grad_flat], stream=self.compute)
-        if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=self.device)
         return hsnf4.grad_clip(self._grad_set, max_norm, norm=norm, stream=self.compute)
 
     # ------------------------------------------------------------------ checks

@@ -544,8 +544,9 @@ typedef struct {
 size_t lora_grad_table_bytes(int n);
 
 /* Fill the table (device memory of table_bytes >= lora_grad_table_bytes(n),
- * 16-byte aligned) on `stream`, and the plan (host).  grads: host array of
- * n (1..65536) tensors.  Not during stream capture.  Errors: INVALID (sizes,
+ * 16-byte aligned) on `stream`, wait for it, and fill the plan (host), which
+ * calls on any stream may then use.  grads: host array of n (1..65536)
+ * tensors.  Not during stream capture.  Errors: INVALID (sizes,
  * pointers, tensors that overlap), OOM (table), STATE (capture), CUDA. */
 int lora_grad_plan(const hsnf4_grad *grads, int n, void *table, size_t table_bytes,
                    hsnf4_grad_plan *plan, void *stream);

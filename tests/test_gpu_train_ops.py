@@ -485,6 +485,35 @@ def test_grad_clip_many_small_and_repeats():
 
 # ---------------------------------------------------------------- streams and graphs
 
+def test_outputs_made_by_a_call_on_a_side_stream():
+    """Outputs and workspaces that a call makes belong to its stream: the
+    current stream, busy meanwhile, neither fills them late nor reuses them."""
+    lens, H, KV, d = [100, 33, 128], 4, 2, 128
+    q, k, v, do = _attn_inputs(lens, lens, H, KV, d, "plain", 33)
+    cu, pos = _cu(lens), torch.arange(261, dtype=torch.int32, device="cuda")
+    rope = hsnf4.Rope(d, hsnf4.rope_inv_freq(d, 1e4))
+
+    def step(stream):
+        q1, k1 = hsnf4.rope_fwd(rope, pos, q, k, stream=stream)
+        o, lse = hsnf4.attention_packed_fwd(q1, k1, v, cu, H, KV, stream=stream)
+        g = hsnf4.attention_packed_bwd(q1, k1, v, o, lse, do, cu, H, KV, stream=stream)
+        gs = hsnf4.GradSet(g, stream=stream)
+        return [q1, k1, o, lse, hsnf4.grad_clip(gs, 1.0, stream=stream), *g]
+
+    ref = step(None)
+    x = torch.zeros(4096, 4096, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(30):  # some milliseconds of work
+        x = x @ x
+    got = step(side)
+    junk = [torch.full_like(t, 3.0) for t in ref for _ in range(3)]
+    torch.cuda.synchronize()
+    assert hsnf4.device_status() == 0 and junk
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)
+
+
 def test_ops_on_a_side_stream_and_in_a_graph():
     lens, H, KV, d = [100, 33, 128], 4, 2, 128
     q, k, v, do = _attn_inputs(lens, lens, H, KV, d, "plain", 30)
