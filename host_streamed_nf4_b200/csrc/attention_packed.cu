@@ -821,12 +821,18 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
   const int per = P.KV * P.splits, kh = blockIdx.x % per / P.splits,
             split = blockIdx.x % per % P.splits;
   if (warp == 0 && lane == 0) prefetch_maps(P);
-  pdl_wait_then_release();
+  // The CTA starts while the dQ kernel ends.  That kernel let this one in after
+  // its own wait, so the call's inputs stand; only D is waited for (every CTA
+  // waits, so that this kernel never ends before that one).
+  pdl_release();
   // (before anything is set up: the grid covers the most tiles and shares)
   PackedTile x;
-  if (!find_tile(P.S, true, blockIdx.x / per, kRows, x)) return;
-  const int shares = tile_shares(P, x);
-  if (split >= shares) return;
+  const bool found = find_tile(P.S, true, blockIdx.x / per, kRows, x);
+  const int shares = found ? tile_shares(P, x) : 0;
+  if (split >= shares) {
+    pdl_wait();
+    return;
+  }
   if (threadIdx.x == 0) {
     mbar_init(&kv_full, 1);
     mbar_init(&drain, 1);
@@ -862,6 +868,7 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
   if ((smem_u32(smem) & 1023u) || tmem_slot != tmem) {
     if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
     if (warp == kMmaWarp) tmem_dealloc(tmem_slot, 512);
+    pdl_wait();
     return;
   }
 
@@ -895,6 +902,11 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
       if (i >= NA && !warp_wait(&q_empty[s], (i / NA) - 1, abort_p, kAtFlagLoad)) break;
       load(ring + s * G::kTile, &P.mq, tail ? &q_raw[s] : &q_full[s]);
       last_a = i;
+      if (i < NB) {
+        load(ring + (NA + v) * G::kTile, &P.mdo, tail ? &do_raw[v] : &do_full[v]);
+        last_b = i;
+      }
+      if (i == 0) pdl_wait();  // D
       float a[4], b[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -911,9 +923,11 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
         nD[i & 1][lane + 32 * e] = b[e];
       }
       mbar_arrive(&ld_full[i & 1]);
-      if (i >= NB && !warp_wait(&do_empty[v], (i / NB) - 1, abort_p, kAtFlagLoad)) break;
-      load(ring + (NA + v) * G::kTile, &P.mdo, tail ? &do_raw[v] : &do_full[v]);
-      last_b = i;
+      if (i >= NB) {
+        if (!warp_wait(&do_empty[v], (i / NB) - 1, abort_p, kAtFlagLoad)) break;
+        load(ring + (NA + v) * G::kTile, &P.mdo, tail ? &do_raw[v] : &do_full[v]);
+        last_b = i;
+      }
       if (++qt == qt0 + per_head) {
         qt = qt0;
         ++h;
@@ -1102,6 +1116,7 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
     }
   }
 
+  if (warp == kLoadWarp) pdl_wait();  // (a tile that no query sees has not waited)
   __syncthreads();
   if (*abort_p && warp == kLoadWarp && lane == 0) {
     volatile int never = 0;
@@ -1130,11 +1145,11 @@ template <int D>
 __global__ void __launch_bounds__(32 * kComputeWarps)
     packed_kv_reduce(const __grid_constant__ BwdTc P) {
   __shared__ __align__(16) uint8_t stage[kComputeWarps * 2048];
-  pdl_wait_then_release();
   PackedTile x;
   const int kh = blockIdx.x % P.KV, slot = blockIdx.x / P.KV;
-  if (!find_tile(P.S, true, slot, kRows, x)) return;
-  const int shares = tile_shares(P, x);
+  const bool found = find_tile(P.S, true, slot, kRows, x);  // (an input, as in the kernel above)
+  const int shares = found ? tile_shares(P, x) : 1;
+  pdl_wait_then_release();
   if (shares == 1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = warp >> 2, which = part >> 1, first = x.t * kRows + (warp & 3) * 32;

@@ -168,9 +168,13 @@ __device__ __forceinline__ bool elect_one() {
 // its first global-memory access, read or write: the wait returns once the
 // previous grid has completed and its writes are visible, exactly as plain
 // stream order would give.  Then the next kernel may be scheduled.
-__device__ __forceinline__ void pdl_wait_then_release() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait_then_release() {
+  pdl_wait();
+  pdl_release();
 }
 
 // ---------------------------------------------------------------- TMA
