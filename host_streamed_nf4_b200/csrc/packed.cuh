@@ -17,6 +17,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct PackedSeqs {
   const int32_t *cu_q, *cu_k;
   int Tq, Tk, n_seq, causal;
+  int sorted;  // key tiles in the order of their work, over all sequences (n_seq <= 128)
 };
 
 struct PackedTile {
@@ -29,6 +30,12 @@ struct PackedTile {
 // under a causal mask: query tiles from the last, key tiles from the first.
 // Whole warp, four sequences a lane at a time: up to 128 sequences cost one
 // round trip to memory.  False if there is no such tile.
+//
+// SORT, where S.sorted: the longest work of all sequences first.  Under a
+// causal mask a sequence of n tiles has tiles of the levels n, n - 1 ... 1
+// (query tiles that see them, for queries as many as keys); without one its
+// tiles all have the level of its query tiles.
+template <bool SORT = false>
 __device__ __forceinline__ bool find_tile(const PackedSeqs& S, bool keys, int slot, int rows,
                                           PackedTile& x) {
   const int lane = threadIdx.x & 31;
@@ -42,13 +49,48 @@ __device__ __forceinline__ bool find_tile(const PackedSeqs& S, bool keys, int sl
       cq[j] = __ldg(S.cu_q + i);
       ck[j] = same ? cq[j] : __ldg(S.cu_k + i);
     }
-    int n[4], sum = 0;
+    int n[4], sum = 0;  // tiles to number
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int T = keys ? S.Tk : S.Tq, c = keys ? ck[j] : cq[j], e = keys ? ck[j + 1] : cq[j + 1];
       const int len = max(min(e, T) - min(max(c, 0), T), 0);
       n[j] = (len + rows - 1) / rows;
       sum += n[j];
+    }
+    int level = 0, first[4] = {};  // sorted: of the tile; of the first tile of that level
+    if (SORT && S.sorted) {
+      int top[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int lq = max(min(cq[j + 1], S.Tq) - min(max(cq[j], 0), S.Tq), 0);
+        top[j] = n[j] == 0 ? 0 : S.causal ? n[j] : 1 + (lq + rows - 1) / rows;
+      }
+      // tiles of level v and above
+      auto count = [&](int v) {
+        int k = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k += S.causal ? max(n[j] - v + 1, 0) : top[j] >= v ? n[j] : 0;
+        return __reduce_add_sync(0xffffffffu, k);
+      };
+      if (slot >= count(1)) return false;
+      int low = 1, high = __reduce_max_sync(0xffffffffu,
+                                            max(max(top[0], top[1]), max(top[2], top[3])));
+      while (low < high) {  // the highest level that has, with those above, more than `slot`
+        const int mid = (low + high + 1) / 2;
+        if (count(mid) > slot)
+          low = mid;
+        else
+          high = mid - 1;
+      }
+      level = low;
+      before = count(level + 1);
+      sum = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        first[j] = S.causal ? n[j] - level : 0;
+        n[j] = S.causal ? n[j] >= level : top[j] == level ? n[j] : 0;
+        sum += n[j];
+      }
     }
     int inc = sum;
 #pragma unroll
@@ -64,7 +106,7 @@ __device__ __forceinline__ bool find_tile(const PackedSeqs& S, bool keys, int sl
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (at >= 0 && at < n[j]) {
-          t = keys ? at : n[j] - 1 - at;
+          t = keys ? first[j] + at : n[j] - 1 - at;
           aq = cq[j], eq = cq[j + 1], ak = ck[j], ek = ck[j + 1];
         }
         at -= n[j];

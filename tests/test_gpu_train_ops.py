@@ -258,6 +258,18 @@ def test_packed_attention(lq, lk, H, KV, causal, d, form):
         assert (o[nq:] == mark).all() and (lse[:, nq:] == mark).all()
 
 
+@pytest.mark.parametrize("lq,lk,H,KV,causal", [
+    # key tiles in the order of their work: long sequences among short and empty ones
+    ([700, 0, 5, 640, 200, 1300, 1], None, 4, 1, True),
+    ([700, 0, 5, 640, 200, 1300, 1], None, 2, 1, False), ([400, 400, 400], None, 7, 1, True),
+    ([5, 600, 300, 0, 1], [900, 100, 700, 400, 0], 4, 2, True),
+    ([5, 600, 300, 0, 1], [900, 100, 700, 400, 0], 4, 2, False),
+    ([1] * 100 + [3000] * 2 + [1] * 26, [3] * 100 + [24500] * 2 + [2] * 26, 2, 1, False),
+])
+def test_packed_attention_sorted_tiles(lq, lk, H, KV, causal):
+    test_packed_attention(lq, lk, H, KV, causal, 64, "padded")
+
+
 def test_packed_attention_large_scores():
     """Scores in the hundreds (softmax near one key) and a scale of one."""
     d, H, KV, lens = 128, 2, 1, [200, 77]
@@ -346,6 +358,18 @@ def test_packed_attention_malformed_lengths_stay_in_bounds():
     d, H, KV = 64, 2, 1
     q, k, v, do = _attn_inputs([100], [100], H, KV, d, "plain", 8)
     for cu in ([0, 400, 90], [-50, 30, 20], [90, 10, 1 << 30], [0, 0, 0]):
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        o, lse = hsnf4.attention_packed_fwd(q, k, v, cu, H, KV)
+        hsnf4.attention_packed_bwd(q, k, v, o, lse, do, cu, H, KV)
+        torch.cuda.synchronize()
+        assert hsnf4.device_status() == 0
+
+
+def test_packed_attention_malformed_lengths_of_sorted_tiles():
+    d, H, KV = 64, 4, 1
+    q, k, v, do = _attn_inputs([2000], [2000], H, KV, d, "plain", 13)
+    for cu in ([0, 1 << 30, 90, 1 << 30, 0], [-50, 1900, 20, 2000, -1], [1 << 30, 0, 700, 0, 700],
+               [0, 0, 0, 0, 0]):
         cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
         o, lse = hsnf4.attention_packed_fwd(q, k, v, cu, H, KV)
         hsnf4.attention_packed_bwd(q, k, v, o, lse, do, cu, H, KV)
