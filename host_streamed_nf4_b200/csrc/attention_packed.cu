@@ -113,6 +113,8 @@ __device__ __forceinline__ void bar_compute() {  // the computing threads
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
+constexpr int kStep = 64;  // keys of a step where a step is not a tile
+
 // 32 columns of this warp's lanes
 __device__ __forceinline__ void load_quarter(uint32_t taddr, uint32_t* r) {
   tmem_ld32_at(taddr, r);
@@ -460,6 +462,262 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
   }
 }
 
+// head_dim 64: 128 query rows of one head, the keys 64 at a time, so that S
+// and O need 128 TMEM columns and four CTAs fit an SM: with 64 columns a
+// tile's products are half as long as with 128 and the chain from scores to
+// probabilities to the next scores weighs twice as much; four chains at once
+// hide it.  A thread owns a row (no exchange between warps).
+struct Fwd64Geo {
+  static constexpr int kD = 64;
+  static constexpr int kQ = tile_bytes<kD>(), kHalf = kStep * kD * 2;  // bytes of Q; of K or V
+  static constexpr int kStages = 4;
+  static constexpr int kSmem = kQ + kStages * kHalf;
+  static constexpr int kThreads = 32 * (4 + 2);
+  static constexpr uint32_t kO = kStep, kCols = kStep + kD;
+};
+
+__global__ void __launch_bounds__(Fwd64Geo::kThreads, 4)
+    packed_fwd64_tc(const __grid_constant__ FwdTc P) {
+  using G = Fwd64Geo;
+  constexpr int D = G::kD, NS = G::kStages, kMmaWarp = 4, kLoadWarp = 5;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t q_full, kv_full[NS], kv_empty[NS], aux, s_full, p_full, o_full, drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0 && lane == 0) prefetch_maps(P);
+  pdl_wait_then_release();
+  // (before anything is set up: the grid covers the most tiles there could be)
+  PackedTile x;
+  if (!find_tile(P.S, false, blockIdx.x / P.H, kRows, x)) return;
+  if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&aux, 1);
+    mbar_init(&drain, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    mbar_init(&s_full, 1);
+    mbar_init(&p_full, 4);
+    mbar_init(&o_full, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_slot, G::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort_p = &abort_flag;
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need the alignment asked for
+    if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, G::kCols);
+    return;
+  }
+  const int h = blockIdx.x % P.H, kh = h / (P.H / P.KV), r0 = x.t * kRows;
+  const int n = (key_limit(P.S, x, min(r0 + kRows, x.lq) - 1) + kStep - 1) / kStep;
+  int last_load = -1;
+  bool q_loaded = false, mma_issued = false;
+  uint8_t* ring = smem + G::kQ;
+
+  if (warp == kLoadWarp && n) {
+    // Q, then K0 V0 K1 V1 ...
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&q_full, G::kQ);
+      tma_tile<D>(smem, &P.mq, &q_full, h * D, x.q0 + r0);
+    }
+    q_loaded = true;
+    for (int i = 0; i < 2 * n; ++i) {
+      const int s = i % NS, row = (i >> 1) * kStep;
+      if (i >= NS && !warp_wait(&kv_empty[s], (i / NS) - 1, abort_p, kAtFlagLoad)) break;
+      uint8_t* st = ring + s * G::kHalf;
+      const CUtensorMap* map = (i & 1) ? &P.mv : &P.mk;
+      // the keys behind the sequence have probability 0, their values must be
+      // finite
+      const bool tail = (i & 1) && row + kStep > x.lk;
+      uint64_t* bar = tail ? &aux : &kv_full[s];
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, G::kHalf);
+        tma_tile<D, kStep>(st, map, bar, kh * D, x.k0 + row);
+      }
+      if (tail) {
+        __syncwarp();
+        if (!tail_landed(&aux, 0, abort_p)) break;
+        zero_rows<D, kStep>(st, x.lk - row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[s]);
+      }
+      last_load = i;
+    }
+  } else if (warp == kMmaWarp && n) {
+    auto wait = [&](uint64_t* bar, int phase) {
+      return warp_wait(bar, phase, abort_p, kAtFlagMma);
+    };
+    auto stage = [&](int i) { return ring + (i % NS) * G::kHalf; };
+    bool ok = wait(&q_full, 0);
+    for (int j = 0; j <= n && ok; ++j) {
+      // O += P V of the step before, then this step's S = Q K^T, which goes
+      // over that P
+      const int i = 2 * j;
+      ok = (j == n || wait(&kv_full[i % NS], i / NS)) &&
+           (j == 0 || (wait(&kv_full[(i - 1) % NS], (i - 1) / NS) && wait(&p_full, j - 1)));
+      if (!ok) break;
+      mma_issued = true;
+      tc_fence_after();
+      if (elect_one()) {
+        if (j > 0) {
+          mma_ay_n<D, kStep, kStep>(tmem + G::kO, tmem, 0, stage(i - 1), j > 1);
+          umma_commit(&o_full);
+          umma_commit(&kv_empty[(i - 1) % NS]);
+        }
+        if (j < n) {
+          mma_xyt_n<D, kStep>(tmem, smem, stage(i));
+          umma_commit(&s_full);
+          umma_commit(&kv_empty[i % NS]);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp < kMmaWarp) {
+    const int row = r0 + threadIdx.x;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t S_r = tmem + lanes, O_r = S_r + G::kO;
+    const int limit = key_limit(P.S, x, row);
+    const uint64_t c2 = f32x2_pack(P.c, P.c);
+    float ref = 0.0f, l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      ok = warp_wait(&s_full, j, abort_p, kAtFlagCompute);
+      if (!ok) break;
+      tc_fence_after();
+      const int lim = limit - j * kStep;
+      const bool mask = __any_sync(0xffffffffu, lim < kStep);
+      auto scores = [&](int b, uint32_t* s) {  // 32 columns, read once for the maximum and again
+        load_quarter(S_r + 32 * b, s);
+        if (!mask) return;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (32 * b + e >= lim) s[e] = 0xff800000u;  // -inf
+      };
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t s[32];
+        scores(b, s);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          m4[(e >> 1) & 3] = max_nan(max_nan(m4[(e >> 1) & 3], __uint_as_float(s[e])),
+                                     __uint_as_float(s[e + 1]));
+      }
+      // (as in the kernel above: rows behind the sequence, the reference that
+      // moves by 2^8, and NaN)
+      const float mt = row < x.lq ? max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3])) * P.c
+                                  : -INFINITY;
+      if (j == 0) {
+        ref = mt == -INFINITY ? 0.0f : mt;
+      } else if (__any_sync(0xffffffffu, mt > ref + 8.0f)) {
+        ok = warp_wait(&o_full, j - 1, abort_p, kAtFlagCompute);
+        if (!ok) break;
+        tc_fence_after();
+        const float next = fmaxf(ref, mt), f = ex2(ref - next);
+        ref = next;
+        l *= f;
+        const uint64_t f2 = f32x2_pack(f, f);
+#pragma unroll 1
+        for (int b = 0; b < D / 16; ++b) {
+          uint32_t o[16];
+          tmem_ld16(O_r + 16 * b, o);
+          tmem_wait_ld();
+          tie16(o);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float lo, hi;
+            f32x2_unpack(f32x2_mul_rn(f32x2_pack_bits(o[e], o[e + 1]), f2), lo, hi);
+            o[e] = __float_as_uint(lo);
+            o[e + 1] = __float_as_uint(hi);
+          }
+          tmem_st16(O_r + 16 * b, o);
+        }
+      }
+      const uint64_t r2 = f32x2_pack(-ref, -ref);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t s[32], p[16];
+        scores(b, s);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint64_t y = f32x2_fma_rn(f32x2_pack_bits(s[2 * e], s[2 * e + 1]), c2, r2);
+          const uint64_t pr = e % kPolyOf < kPolyPart ? ex2_poly<false>(y) : ex2_pair(y);
+          sum[e & 1] = f32x2_add_rn(sum[e & 1], pr);
+          p[e] = f32x2_to_bf16x2(pr);
+        }
+        tmem_st16(S_r + 16 * b, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full);
+      float a0, a1;
+      f32x2_unpack(f32x2_add_rn(sum[0], sum[1]), a0, a1);
+      l += a0 + a1;
+      if (!(mt < INFINITY)) l = NAN;
+    }
+    if (ok && n) ok = warp_wait(&o_full, n - 1, abort_p, kAtFlagCompute);
+    if (ok) {
+      tc_fence_after();
+      const bool some = limit > 0;
+      const float inv = some ? 1.0f / l : 0.0f;
+      // the tile's Q is read: its shared memory stages the rows
+      const int first = r0 + warp * 32;
+      uint4 v[D / 8];
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) {
+        uint32_t o[32];
+        if (n) {
+          load_quarter(O_r + 32 * b, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[4 * b + c] = pack8_scaled(o + 8 * c, inv);
+      }
+      put_rows<D / 8>(smem + warp * (64 * D), v,
+                      P.out + static_cast<int64_t>(x.q0 + first) * P.os + h * D, P.os * 2,
+                      x.lq - first);
+      if (row < x.lq)
+        P.lse[static_cast<int64_t>(h) * P.S.Tq + x.q0 + row] =
+            some ? (ref + log2f(l)) / kLog2e : -INFINITY;
+    }
+  }
+
+  __syncthreads();  // every thread sees the final abort word
+  if (*abort_p && warp == kLoadWarp && lane == 0) {
+    // drain what this CTA started before its shared memory and TMEM go away
+    volatile int never = 0;
+    if (q_loaded) spin_wait(&q_full, 0, &never, kAtFlagDrain);
+    for (int i = max(0, last_load - NS + 1); i <= last_load; ++i)
+      if (!spin_wait(&kv_full[i % NS], (i / NS) & 1, &never, kAtFlagDrain)) break;
+  }
+  if (*abort_p && warp == kMmaWarp && mma_issued && elect_one()) {
+    volatile int never = 0;
+    umma_commit(&drain);
+    spin_wait(&drain, 0, &never, kAtFlagDrain);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, G::kCols);
+  }
+}
+
 // ---------------------------------------------------------------- backward
 
 struct BwdTc {
@@ -499,8 +757,6 @@ struct BwdGeo {
 // about 10000 cycles of latency, as much as eight steps.  S of the next step
 // is computed as soon as the threads have read this one's; its dP follows
 // dQ's product, which reads dS.
-constexpr int kStep = 64;  // keys of a step
-
 template <int D>
 struct DqGeo {
   static constexpr int kTile = tile_bytes<D>();  // Q, dO, O: 128 rows
@@ -1226,6 +1482,16 @@ cudaError_t fwd_tc(const FwdTc& P, cudaStream_t st) {
                     G::kSmem, st, P);
 }
 
+cudaError_t fwd64_tc(const FwdTc& P, cudaStream_t st) {
+  using G = Fwd64Geo;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(packed_fwd64_tc, G::kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = most_tiles(P.S.Tq, P.S.n_seq, kRows) * P.H;
+  return launch_pdl(packed_fwd64_tc, dim3(static_cast<unsigned>(grid)), dim3(G::kThreads),
+                    G::kSmem, st, P);
+}
+
 int sm_count() {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -1335,8 +1601,16 @@ cudaError_t launch_packed_fwd(const hsnf4_packed_attention& a, void* o, int64_t 
   memset(&P, 0, sizeof P);
   const int64_t wq = static_cast<int64_t>(a.H) * a.head_dim,
                 wk = static_cast<int64_t>(a.KV) * a.head_dim;
-  if (!map_rows(&P.mq, a.q, wq, a.Tq, a.q_stride) || !map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride) ||
-      !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride))
+  // head_dim 64: 64 keys a step and four CTAs per SM where that many come.
+  // 16/16 heads, 128 keys a step against 64: 64 sequences of 64 tokens 24.5 /
+  // 15.1 us, 23 ragged ones of 4100 25.5 / 21.7, 16 of 512 41.1 / 34.8, one of
+  // 8192 426 / 377 (no mask); with fewer CTAs the shorter chain of 128 wins,
+  // one of 512 9.9 / 12.1, one of 2048 27.4 / 35.2.
+  const bool many = a.head_dim == 64 && most_tiles(a.Tq, a.n_seq, kRows) * a.H >= 4 * sm_count();
+  const int box = many ? kStep : kRows;
+  if (!map_rows(&P.mq, a.q, wq, a.Tq, a.q_stride) ||
+      !map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride, box) ||
+      !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride, box))
     return cudaErrorInvalidValue;
   P.out = static_cast<uint16_t*>(o);
   P.os = o_stride;
@@ -1351,6 +1625,7 @@ cudaError_t launch_packed_fwd(const hsnf4_packed_attention& a, void* o, int64_t 
   // 429 / 406, one of 16384 (32/8 heads) 1940 / 1770.
   const bool two = a.Tq >= 6144 * static_cast<int64_t>(a.n_seq);
   if (a.head_dim == 128) return two ? fwd_tc<128, 2>(P, st) : fwd_tc<128, 1>(P, st);
+  if (many) return fwd64_tc(P, st);
   return two ? fwd_tc<64, 2>(P, st) : fwd_tc<64, 1>(P, st);
 }
 

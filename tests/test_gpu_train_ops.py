@@ -270,6 +270,55 @@ def test_packed_attention_sorted_tiles(lq, lk, H, KV, causal):
     test_packed_attention(lq, lk, H, KV, causal, 64, "padded")
 
 
+def _many_heads(lq):
+    """Heads that fill the device with query tiles, four per SM."""
+    tiles = sum(lq) // 128 + min(len(lq), max(sum(lq), 1))
+    n = torch.cuda.get_device_properties(0).multi_processor_count
+    return 2 * -(-2 * n // tiles)
+
+
+@pytest.mark.parametrize("lq,lk,causal", [(c[0], c[1], c[4]) for c in ATTN_CASES])
+@pytest.mark.parametrize("form", ["fused", "padded"])
+def test_packed_attention_many_heads(lq, lk, causal, form):
+    """head_dim 64 with so many tiles that the forward takes 64 keys a step."""
+    d, H, KV, lk = 64, _many_heads(lq), 2, lq if lk is None else lk
+    q, k, v, _ = _attn_inputs(lq, lk, H, KV, d, form, sum(lq))
+    nq, nk = sum(lq), sum(lk)
+    o, lse = torch.full_like(q.contiguous(), 7.0), torch.full((H, q.shape[0]), 7.0, device="cuda")
+    hsnf4.attention_packed_fwd(q, k, v, _cu(lq), H, KV, causal=causal, cu_k=_cu(lk), o=o, lse=lse)
+    torch.cuda.synchronize()
+    assert hsnf4.device_status() == 0
+    ro, rl, to = _attn_ref(q[:nq], k[:nk], v[:nk], lq, lk, H, KV, causal, d ** -0.5)
+    _within(o[:nq], ro, to + 1e-30, "o")
+    _lse_within(lse[:, :nq], rl, "lse")
+    assert (o[nq:] == 7.0).all() and (lse[:, nq:] == 7.0).all()
+
+
+def test_packed_attention_many_heads_large_scores_and_not_finite():
+    d, KV, lens = 64, 2, [70, 50, 331, 9]
+    H = _many_heads(lens)
+    q, k, v, _ = _attn_inputs(lens, lens, H, KV, d, "plain", 6)
+    cu = _cu(lens)
+    o, lse = hsnf4.attention_packed_fwd(q, k, v, cu, H, KV)
+    o4, lse4 = hsnf4.attention_packed_fwd(4 * q, k, v, cu, H, KV, scale=1.0)
+    ro, rl, _ = _attn_ref(4 * q, k, v, lens, lens, H, KV, True, 1.0)
+    # scores of deviation 32, their partial sums below 512: each of 64 additions is
+    # off by half a step of 2^-15 there, 2^-10 in all, and 2^-9 covers exp2 too
+    assert (o4.double() - ro).abs().max() <= (2 * U + 2 * 2.0 ** -9) * v.double().abs().max()
+    assert (lse4.double() - rl).abs().max() <= 2.0 ** -9
+    bad_q, bad_k, bad_v = q.clone(), k.clone(), v.clone()
+    bad_q[70:120], bad_k[70:120], bad_v[70:120] = NAN, float("inf"), NAN
+    bad_q[300, d + 3], bad_k[400, 5] = float("inf"), NAN  # head 1; KV head 0
+    o2, lse2 = hsnf4.attention_packed_fwd(bad_q, bad_k, bad_v, cu, H, KV)
+    torch.cuda.synchronize()
+    same = (o2 == o).view(460, H, d).all(2) & (lse2 == lse).T
+    want = torch.ones_like(same)
+    want[70:120], want[300, 1], want[400:451, :H // 2] = False, False, False
+    assert torch.equal(same, want)
+    assert o2[300, d:2 * d].isnan().all() and o2[400:451, :H // 2 * d].isnan().all()
+    assert lse2[1, 300].isnan() and lse2[:H // 2, 400:451].isnan().all()
+
+
 def test_packed_attention_large_scores():
     """Scores in the hundreds (softmax near one key) and a scale of one."""
     d, H, KV, lens = 128, 2, 1, [200, 77]
