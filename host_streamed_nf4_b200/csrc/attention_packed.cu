@@ -42,10 +42,6 @@ enum : unsigned int {
 
 // Of every kPolyOf pairs of exponentials, kPolyPart go to the fp32 pipe.
 constexpr int kPolyOf = 8, kPolyPart = 2;
-constexpr int kComputeWarps = 16;  // four per SM sub-partition
-constexpr int kTcThreads = 32 * (kComputeWarps + 2);
-constexpr int kMmaWarp = kComputeWarps, kLoadWarp = kComputeWarps + 1;
-constexpr int kPatchWarp = kComputeWarps + 2;  // dK/dV kernel only
 constexpr int kReduceThreads = 512;
 
 // mbar_wait with the abort word and the timer looked at every 32 polls only:
@@ -739,13 +735,23 @@ __device__ __forceinline__ void prefetch_maps(const BwdTc& P) {
   tma_prefetch_desc(&P.mdo);
 }
 
-// Two rings: the tiles that the last product of a step reads (K, or Q) are
-// held longest and get one stage more than the others (V, or dO).
-template <int D>
-struct BwdGeo {
-  static constexpr int kTile = tile_bytes<D>();
-  static constexpr int kA = D == 128 ? 3 : 5, kB = D == 128 ? 2 : 4;
-  static constexpr int kSmem = (2 + kA + kB) * kTile;
+// Geometry of the dK/dV kernel: the queries of a step are 128 with one CTA per
+// SM, or 64 with two (head_dim 64 only: a CTA has half of TMEM).  Two rings: a
+// step's last product reads Q, which is held longest and gets one stage more
+// than dO.
+template <int D, int CTAS>
+struct KvGeo {
+  static constexpr int kStep = 128 / CTAS, kParts = kStep / 32;  // queries; 32 to a thread
+  static constexpr int kWarps = 4 * kParts;                      // computing warps
+  static constexpr int kMmaWarp = kWarps, kLoadWarp = kWarps + 1, kPatchWarp = kWarps + 2;
+  static constexpr int kThreads = 32 * (kWarps + 3);
+  static constexpr int kTile = tile_bytes<D>(), kRow = kStep * D * 2;  // bytes of K, V; of Q, dO
+  static constexpr int kA = D == 128 ? 3 : 6 - CTAS, kB = kA - 1;
+  static constexpr int kSmem = 2 * kTile + (kA + kB) * kRow;
+  static constexpr uint32_t kDp = kStep, kDv = 2 * kStep, kDk = kDv + D,  // TMEM
+      kCols = 512 / CTAS;
+  static constexpr int kOut = 2 * D / kParts;  // of dV's and dK's columns: a thread's
+  static_assert(kDk + D <= kCols && kWarps * 64 * kOut <= (kA + kB) * kRow, "");
 };
 
 // dQ of 128 query rows of one head, the keys 64 at a time: S = Q K^T,
@@ -1031,9 +1037,9 @@ __global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
   }
 }
 
-// the first query tile that sees the keys of tile x
-__device__ __forceinline__ int first_query_tile(const PackedSeqs& S, const PackedTile& x) {
-  return (S.causal ? max(x.t * kRows - (x.lk - x.lq), 0) : 0) / kRows;
+// the first query that sees keys of tile x
+__device__ __forceinline__ int first_query(const PackedSeqs& S, const PackedTile& x) {
+  return S.causal ? max(x.t * kRows - (x.lk - x.lq), 0) : 0;
 }
 
 // Shares that a key tile's query heads are cut into: so many that none has
@@ -1041,7 +1047,7 @@ __device__ __forceinline__ int first_query_tile(const PackedSeqs& S, const Packe
 // long sequence among short ones would otherwise keep one CTA busy long after
 // the others (8150 tokens in 17 sequences, the longest 1855: 168 us of 350).
 __device__ __forceinline__ int tile_shares(const BwdTc& P, const PackedTile& x) {
-  const int all = max((x.lq + kRows - 1) / kRows - first_query_tile(P.S, x), 0) * (P.H / P.KV);
+  const int all = max((x.lq + kRows - 1) / kRows - first_query(P.S, x) / kRows, 0) * (P.H / P.KV);
   return min(max((all + P.limit - 1) / P.limit, 1), P.splits);
 }
 
@@ -1057,23 +1063,25 @@ __device__ __forceinline__ int64_t part_at(const BwdTc& P, int slot, int kh, int
 
 // dK, dV of 128 keys of one KV head, over one share of the group's query
 // heads and, in each, the query tiles that see the keys, in order.  The
-// scores are computed transposed (a thread owns a key row, 64 of the tile's
-// 128 queries), so that P^T and dS^T, written as bf16 over the scores they
-// came from, are the tensor-memory operands of dV += P^T dO and dK += dS^T Q.
-// TMEM: S^T, dP^T (128 columns each), dV, dK (D each).  While the threads
+// scores are computed transposed (a thread owns a key row, 32 of the step's
+// queries), so that P^T and dS^T, written as bf16 over the scores they came
+// from, are the tensor-memory operands of dV += P^T dO and dK += dS^T Q.
+// TMEM: S^T, dP^T, dV, dK.  While the threads
 // compute P^T the tensor cores run the tile before's dK product and this
 // tile's dP^T; while they compute dS^T, dV and the next S^T.
-template <int D>
-__global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __grid_constant__ BwdTc P) {
-  using G = BwdGeo<D>;
-  constexpr int NA = G::kA, NB = G::kB;  // Q, dO
+template <int D, int CTAS>
+__global__ void __launch_bounds__(KvGeo<D, CTAS>::kThreads, CTAS)
+    packed_dkdv_tc(const __grid_constant__ BwdTc P) {
+  using G = KvGeo<D, CTAS>;
+  constexpr int NA = G::kA, NB = G::kB, kStep = G::kStep;  // stages of Q, of dO; queries of a step
+  constexpr int kMmaWarp = G::kMmaWarp, kLoadWarp = G::kLoadWarp, kPatchWarp = G::kPatchWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t kv_full, q_full[NA], ld_full[2], q_empty[NA], do_full[NB], do_empty[NB], q_raw[NA],
       do_raw[NB],
       s_full, dp_full, p_full, ds_full, done, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ __align__(16) float nlse[2][kRows], nD[2][kRows];  // -lse log2(e), -D
+  __shared__ __align__(16) float nlse[2][kStep], nD[2][kStep];  // -lse log2(e), -D
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = P.KV * P.splits, kh = blockIdx.x % per / P.splits,
             split = blockIdx.x % per % P.splits;
@@ -1107,24 +1115,25 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
     mbar_init(&s_full, 1);
     mbar_init(&dp_full, 1);
     mbar_init(&done, 1);
-    mbar_init(&p_full, kComputeWarps);
-    mbar_init(&ds_full, kComputeWarps);
+    mbar_init(&p_full, G::kWarps);
+    mbar_init(&ds_full, G::kWarps);
     abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(&tmem_slot, 512);
+    tmem_alloc(&tmem_slot, G::kCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
+  // with all 512 columns this CTA's: a base known at compile time
+  const uint32_t tmem = G::kCols == 512 ? 0u : tmem_slot;
   volatile int* abort_p = &abort_flag;
   // the swizzled tiles need the alignment asked for
   if ((smem_u32(smem) & 1023u) || tmem_slot != tmem) {
     if (threadIdx.x == 0) atomicOr(&g_attn_flags, kAtFlagLoad);
-    if (warp == kMmaWarp) tmem_dealloc(tmem_slot, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem_slot, G::kCols);
     pdl_wait();
     return;
   }
@@ -1132,8 +1141,8 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
   const int grp = P.H / P.KV;
   const int h0 = kh * grp + grp * split / shares, h1 = kh * grp + grp * (split + 1) / shares;
   const int c0 = x.t * kRows;
-  const int qt0 = first_query_tile(P.S, x);
-  const int per_head = max((x.lq + kRows - 1) / kRows - qt0, 0);
+  const int qt0 = first_query(P.S, x) / kStep;  // (in steps)
+  const int per_head = max((x.lq + kStep - 1) / kStep - qt0, 0);
   const int n = per_head * (h1 - h0);
   int last_a = -1, last_b = -1;
   bool kv_loaded = false, mma_issued = false;
@@ -1148,25 +1157,25 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
     kv_loaded = true;
     int h = h0, qt = qt0;
     for (int i = 0; i < n; ++i) {
-      const int s = i % NA, v = i % NB, row = qt * kRows;
-      const bool tail = row + kRows > x.lq;  // goes through the patching warp
+      const int s = i % NA, v = i % NB, row = qt * kStep;
+      const bool tail = row + kStep > x.lq;  // goes through the patching warp
       auto load = [&](uint8_t* st, const CUtensorMap* map, uint64_t* bar) {
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar, G::kTile);
-          tma_tile<D>(st, map, bar, h * D, x.q0 + row);
+          mbar_arrive_expect_tx(bar, G::kRow);
+          tma_tile<D, kStep>(st, map, bar, h * D, x.q0 + row);
         }
       };
       if (i >= NA && !warp_wait(&q_empty[s], (i / NA) - 1, abort_p, kAtFlagLoad)) break;
-      load(ring + s * G::kTile, &P.mq, tail ? &q_raw[s] : &q_full[s]);
+      load(ring + s * G::kRow, &P.mq, tail ? &q_raw[s] : &q_full[s]);
       last_a = i;
       if (i < NB) {
-        load(ring + (NA + v) * G::kTile, &P.mdo, tail ? &do_raw[v] : &do_full[v]);
+        load(ring + (NA + v) * G::kRow, &P.mdo, tail ? &do_raw[v] : &do_full[v]);
         last_b = i;
       }
       if (i == 0) pdl_wait();  // D
-      float a[4], b[4];
+      float a[kStep / 32], b[kStep / 32];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kStep / 32; ++e) {
         const int j = lane + 32 * e;
         const int64_t at = static_cast<int64_t>(h) * P.S.Tq + x.q0 + row + j;
         a[e] = row + j < x.lq ? P.lse[at] * -kLog2e : 0.0f;
@@ -1175,14 +1184,14 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
       // their slot was last read for tile i - 2, before its dK product
       if (i >= 2 && !warp_wait(&q_empty[(i - 2) % NA], (i - 2) / NA, abort_p, kAtFlagLoad)) break;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kStep / 32; ++e) {
         nlse[i & 1][lane + 32 * e] = a[e];
         nD[i & 1][lane + 32 * e] = b[e];
       }
       mbar_arrive(&ld_full[i & 1]);
       if (i >= NB) {
         if (!warp_wait(&do_empty[v], (i / NB) - 1, abort_p, kAtFlagLoad)) break;
-        load(ring + (NA + v) * G::kTile, &P.mdo, tail ? &do_raw[v] : &do_full[v]);
+        load(ring + (NA + v) * G::kRow, &P.mdo, tail ? &do_raw[v] : &do_full[v]);
         last_b = i;
       }
       if (++qt == qt0 + per_head) {
@@ -1195,20 +1204,20 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
     // are 0 there, Q and dO must be finite.  (A warp of its own: the loader
     // would wait for every such tile instead of running ahead, 3.7 us a tile
     // where each is one.)
-    const int row = (qt0 + per_head - 1) * kRows;
+    const int row = (qt0 + per_head - 1) * kStep;
     uint32_t q_phase = 0, do_phase = 0;  // a bit per stage
-    if (row + kRows > x.lq) {
+    if (row + kStep > x.lq) {
       for (int i = per_head - 1; i < n; i += per_head) {
         const int s = i % NA, v = i % NB;
         if (!tail_landed(&q_raw[s], (q_phase >> s) & 1, abort_p)) break;
         q_phase ^= 1u << s;
-        zero_rows<D>(ring + s * G::kTile, x.lq - row);
+        zero_rows<D, kStep>(ring + s * G::kRow, x.lq - row);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[s]);
         if (!tail_landed(&do_raw[v], (do_phase >> v) & 1, abort_p)) break;
         do_phase ^= 1u << v;
-        zero_rows<D>(ring + (NA + v) * G::kTile, x.lq - row);
+        zero_rows<D, kStep>(ring + (NA + v) * G::kRow, x.lq - row);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&do_full[v]);
@@ -1220,14 +1229,14 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
     auto wait = [&](uint64_t* bar, int phase) {
       return warp_wait(bar, phase, abort_p, kAtFlagMma);
     };
-    auto Q = [&](int i) { return ring + (i % NA) * G::kTile; };
-    auto dO = [&](int i) { return ring + (NA + i % NB) * G::kTile; };
+    auto Q = [&](int i) { return ring + (i % NA) * G::kRow; };
+    auto dO = [&](int i) { return ring + (NA + i % NB) * G::kRow; };
     auto scores = [&](int i) {  // S^T = K Q^T (one thread)
-      mma_xyt<D>(tmem, smem, Q(i));
+      mma_xyt_n<D, kStep>(tmem, smem, Q(i));
       umma_commit(&s_full);
     };
     auto dprobs = [&](int i) {  // dP^T = V dO^T
-      mma_xyt<D>(tmem + 128, smem + G::kTile, dO(i));
+      mma_xyt_n<D, kStep>(tmem + G::kDp, smem + G::kTile, dO(i));
       umma_commit(&dp_full);
     };
     bool ok = wait(&kv_full, 0) && wait(&q_full[0], 0) && wait(&do_full[0], 0);
@@ -1247,7 +1256,7 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
       const bool do_in = more && warp_test(&do_full[(i + 1) % NB], (i + 1) / NB);
       tc_fence_after();
       if (elect_one()) {
-        mma_ay<D, 32>(tmem + 256, tmem, 32, dO(i), i > 0);  // dV += P^T dO
+        mma_ay_n<D, 32, kStep>(tmem + G::kDv, tmem, 32, dO(i), i > 0);  // dV += P^T dO
         umma_commit(&do_empty[i % NB]);
         if (more) scores(i + 1);
       }
@@ -1257,7 +1266,7 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
       q_in = i + 2 < n && warp_test(&q_full[(i + 2) % NA], (i + 2) / NA);
       tc_fence_after();
       if (elect_one()) {
-        mma_ay<D, 32>(tmem + 256 + D, tmem + 128, 32, Q(i), i > 0);  // dK += dS^T Q
+        mma_ay_n<D, 32, kStep>(tmem + G::kDk, tmem + G::kDp, 32, Q(i), i > 0);  // dK += dS^T Q
         umma_commit(&q_empty[i % NA]);
         if (more) dprobs(i + 1);
       }
@@ -1265,10 +1274,10 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
     }
     if (ok && elect_one()) umma_commit(&done);
     __syncwarp();
-  } else if (warp < kComputeWarps) {
+  } else if (warp < G::kWarps) {
     const int part = warp >> 2, q4 = warp & 3, key = c0 + q4 * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t S_p = tmem + part * 32 + lanes, dP_p = S_p + 128;
+    const uint32_t S_p = tmem + part * 32 + lanes, dP_p = S_p + G::kDp;
     const bool in = key < x.lk;
     // query rows of the sequence that see this key: [first, lq)
     const int first = in ? (P.S.causal ? max(key - (x.lk - x.lq), 0) : 0) : x.lq;
@@ -1278,7 +1287,7 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
     for (int i = 0; i < n; ++i) {
       const int s = i & 1;
       // bit b of keep: query b of this thread's 32 sees the key
-      const int lo = first - qt * kRows - part * 32, hi = x.lq - qt * kRows - part * 32;
+      const int lo = first - qt * kStep - part * 32, hi = x.lq - qt * kStep - part * 32;
       const uint32_t keep = (hi >= 32 ? ~0u : hi > 0 ? (1u << hi) - 1 : 0u) &
                             (lo <= 0 ? ~0u : lo < 32 ? ~0u << lo : 0u);
       const bool mask = __any_sync(0xffffffffu, keep != ~0u);
@@ -1337,14 +1346,14 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
     if (ok && n) ok = warp_wait(&done, 0, abort_p, kAtFlagCompute);
     if (ok) {
       tc_fence_after();
-      // eight warps write dV, eight dK, half of the columns each
-      const int which = part >> 1, col = (part & 1) * (D / 2);  // 1: dK
-      const uint32_t src = tmem + 256 + which * D + col + lanes;
+      // half of the warps write dV, half dK
+      const int which = part / (G::kParts / 2), col = part % (G::kParts / 2) * G::kOut;  // 1: dK
+      const uint32_t src = tmem + G::kDv + which * D + col + lanes;
       const int first = c0 + q4 * 32;
-      float4* share = P.part + part_at<D>(P, blockIdx.x / per, kh, split) + warp * (D * 4) + lane;
-      uint4 v[D / 16];
+      float4* share = P.part + part_at<D>(P, blockIdx.x / per, kh, split) + warp * (8 * G::kOut) + lane;
+      uint4 v[G::kOut / 8];
 #pragma unroll
-      for (int b = 0; b < D / 64; ++b) {
+      for (int b = 0; b < G::kOut / 32; ++b) {
         uint32_t o[32];
         if (n) {
           load_quarter(src + 32 * b, o);
@@ -1366,7 +1375,7 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
       }
       if (shares == 1) {  // all products are done: the ring stages the rows
         const int64_t pitch = which ? P.dks : P.dvs;
-        put_rows<D / 16>(ring + warp * 4096, v,
+        put_rows<G::kOut / 8>(ring + warp * (64 * G::kOut), v,
                          (which ? P.dk : P.dv) + (x.k0 + first) * pitch + kh * D + col, pitch * 2,
                          x.lk - first);
       }
@@ -1392,7 +1401,7 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, G::kCols);
   }
 }
 
@@ -1405,10 +1414,11 @@ __global__ void __launch_bounds__(kTcThreads + 32, 1) packed_dkdv_tc(const __gri
 // no work here.  With a whole tile and KV head per CTA the backward of 512
 // tokens (28/4 heads) took 40.0 us for 33.4, of 1024 tokens 65.0 for 57.9, of
 // 8150 in 17 sequences 306 for 309.
-template <int D>
+template <int D, int CTAS>
 __global__ void __launch_bounds__(kReduceThreads) packed_kv_reduce(const __grid_constant__ BwdTc P) {
   __shared__ __align__(16) uint4 stage[4][32][4];
-  constexpr int kParts = 4 * (D / 64);  // steps of a KV head
+  constexpr int kParts = KvGeo<D, CTAS>::kParts, kOut = KvGeo<D, CTAS>::kOut;
+  constexpr int kSteps = kParts * (kOut / 32);  // steps of a KV head
   PackedTile x;
   const int slot = blockIdx.x;
   const bool found = find_tile<true>(P.S, true, slot, kRows, x);  // (an input, as in the kernel above)
@@ -1417,9 +1427,10 @@ __global__ void __launch_bounds__(kReduceThreads) packed_kv_reduce(const __grid_
   if (shares == 1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = warp >> 2, piece = warp & 3;
   const int r = piece * 8 + (lane >> 2), c = lane & 3, row = x.t * kRows + q4 * 32 + r;
-  for (int u = blockIdx.y; u < P.KV * kParts; u += gridDim.y) {
-    const int kh = u / kParts, part = u % kParts / (D / 64), b = u % (D / 64), which = part >> 1;
-    const float4* p = P.part + part_at<D>(P, slot, kh, 0) + (part * 4 + q4) * (D * 4) +
+  for (int u = blockIdx.y; u < P.KV * kSteps; u += gridDim.y) {
+    const int kh = u / kSteps, part = u % kSteps / (kOut / 32), b = u % (kOut / 32),
+              which = part / (kParts / 2);
+    const float4* p = P.part + part_at<D>(P, slot, kh, 0) + (part * 4 + q4) * (8 * kOut) +
                       (8 * b + 2 * piece) * 32 + lane;
     float4 sum[2] = {};
     for (int s = 0; s < shares; s += 4) {  // four shares' loads at once
@@ -1444,7 +1455,7 @@ __global__ void __launch_bounds__(kReduceThreads) packed_kv_reduce(const __grid_
     const int64_t pitch = which ? P.dks : P.dvs;
     if (row < x.lk)
       *reinterpret_cast<uint4*>((which ? P.dk : P.dv) + (x.k0 + row) * pitch + kh * D +
-                                (part & 1) * (D / 2) + 32 * b + 8 * c) =
+                                part % (kParts / 2) * kOut + 32 * b + 8 * c) =
           stage[q4][r][c ^ ((r >> 1) & 3)];
     __syncthreads();
   }
@@ -1527,10 +1538,48 @@ bool sort_tiles(int64_t Tk, int n_seq, int splits) {
   return splits > 1 && n_seq > 1 && n_seq <= 128 && Tk >= 3 * kRows * static_cast<int64_t>(n_seq);
 }
 
+// The dK/dV kernel and the sum of its shares, after the dQ kernel with the
+// same parameters.
+template <int D, int CTAS>
+cudaError_t kv_tc(const hsnf4_packed_attention& a, const PackedBwd& b, BwdTc& P, cudaStream_t st) {
+  using G = KvGeo<D, CTAS>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(packed_dkdv_tc<D, CTAS>, G::kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t wq = static_cast<int64_t>(a.H) * D, wk = static_cast<int64_t>(a.KV) * D;
+  if (!map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride) ||
+      !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride) ||
+      !map_rows(&P.mq, a.q, wq, a.Tq, a.q_stride, G::kStep) ||
+      !map_rows(&P.mdo, b.dout, wq, a.Tq, b.do_stride, G::kStep))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = most_tiles(a.Tk, a.n_seq, kRows);
+  e = launch_pdl(packed_dkdv_tc<D, CTAS>, dim3(static_cast<unsigned>(tiles * a.KV * P.splits)),
+                 dim3(G::kThreads), G::kSmem, st, P);
+  if (e != cudaSuccess || P.splits == 1) return e;
+  const int64_t steps = a.KV * G::kParts * (G::kOut / 32);
+  const int64_t ctas = sm_count() * (2048 / kReduceThreads);
+  return launch_pdl(packed_kv_reduce<D, CTAS>,
+                    dim3(static_cast<unsigned>(tiles),
+                         static_cast<unsigned>(std::min(std::max<int64_t>(ctas / tiles, 1), steps))),
+                    dim3(kReduceThreads), 0, st, P);
+}
+
+// Whether two dK/dV CTAs share an SM (head_dim 64): where four and more come
+// per SM, or two of sequences of about a tile, and the sequences are not long.
+// One hides the other's start, end and waits, but each step takes half as many
+// queries.  One CTA per SM against two, the whole backward, 16/16 heads, no
+// mask: 64 sequences of 64 tokens 78 / 51 us, 23 ragged ones (4100 tokens) 71
+// / 62, 16 of 512 129 / 114; 28/4 heads, causal: 64 of 64 93 / 77, 16 of 512
+// 144 / 161, one of 1024 45 / 57, 25167 tokens in 20 823 / 877.
+bool two_ctas(const hsnf4_packed_attention& a) {
+  const int64_t ctas = most_tiles(a.Tk, a.n_seq, kRows) * a.KV, mean = a.Tk / a.n_seq;
+  return mean < 1024 && ctas >= (mean <= kRows ? 2 : 4) * sm_count();
+}
+
 template <int D>
 cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws,
                    cudaStream_t st) {
-  static std::atomic<uint64_t> done_q{0}, done_kv{0};
+  static std::atomic<uint64_t> done{0};
   BwdTc P;
   memset(&P, 0, sizeof P);
   const int64_t wq = static_cast<int64_t>(a.H) * D, wk = static_cast<int64_t>(a.KV) * D;
@@ -1558,25 +1607,16 @@ cudaError_t bwd_tc(const hsnf4_packed_attention& a, const PackedBwd& b, void* ws
   P.limit = share_limit(a);
   P.scale = a.scale;
   P.c = a.scale * kLog2e;
-  cudaError_t e = allow_smem(packed_dq_tc<D>, DqGeo<D>::kSmem, done_q);
-  if (e == cudaSuccess) e = allow_smem(packed_dkdv_tc<D>, BwdGeo<D>::kSmem, done_kv);
+  cudaError_t e = allow_smem(packed_dq_tc<D>, DqGeo<D>::kSmem, done);
   if (e != cudaSuccess) return e;
   e = launch_pdl(packed_dq_tc<D>,
                  dim3(static_cast<unsigned>(most_tiles(a.Tq, a.n_seq, kRows) * a.H)),
                  dim3(DqGeo<D>::kThreads), DqGeo<D>::kSmem, st, P);
   if (e != cudaSuccess) return e;
-  if (!map_rows(&P.mk, a.k, wk, a.Tk, a.k_stride) || !map_rows(&P.mv, a.v, wk, a.Tk, a.v_stride))
-    return cudaErrorInvalidValue;
-  e = launch_pdl(packed_dkdv_tc<D>, dim3(static_cast<unsigned>(most_tiles(a.Tk, a.n_seq, kRows) *
-                                                               a.KV * P.splits)),
-                 dim3(kTcThreads + 32), BwdGeo<D>::kSmem, st, P);
-  if (e != cudaSuccess || P.splits == 1) return e;
-  const int64_t tiles = most_tiles(a.Tk, a.n_seq, kRows), steps = a.KV * 4 * (D / 64);
-  const int64_t ctas = sm_count() * (2048 / kReduceThreads);
-  return launch_pdl(packed_kv_reduce<D>,
-                    dim3(static_cast<unsigned>(tiles),
-                         static_cast<unsigned>(std::min(std::max<int64_t>(ctas / tiles, 1), steps))),
-                    dim3(kReduceThreads), 0, st, P);
+  if constexpr (D == 64) {
+    if (two_ctas(a)) return kv_tc<64, 2>(a, b, P, st);
+  }
+  return kv_tc<D, 1>(a, b, P, st);
 }
 
 }  // namespace

@@ -294,6 +294,33 @@ def test_packed_attention_many_heads(lq, lk, causal, form):
     assert (o[nq:] == 7.0).all() and (lse[:, nq:] == 7.0).all()
 
 
+@pytest.mark.parametrize("lq,lk,causal", [(c[0], c[1], c[4]) for c in ATTN_CASES])
+@pytest.mark.parametrize("group", [1, 2])
+def test_packed_attention_many_kv_heads(lq, lk, causal, group):
+    """head_dim 64 with so many key tiles that two dK/dV kernels share an SM;
+    two query heads a KV head share the work out where tiles are few."""
+    d, lk = 64, lq if lk is None else lk
+    nq, nk = sum(lq), sum(lk)
+    tiles = nk // 128 + min(len(lk), max(nk, 1))
+    n = torch.cuda.get_device_properties(0).multi_processor_count
+    KV = -(-(2 if nk <= 128 * len(lk) else 4) * n // tiles)
+    group = group if group * KV <= 1024 else 1
+    H = KV * group
+    q, k, v, do = _attn_inputs(lq, lk, H, KV, d, "padded", nk)
+    cu_q, cu_k, scale = _cu(lq), _cu(lk), d ** -0.5
+    o, lse = hsnf4.attention_packed_fwd(q, k, v, cu_q, H, KV, causal=causal, cu_k=cu_k)
+    out = [torch.full(t.shape, 7.0, dtype=t.dtype, device="cuda") for t in (q, k, v)]
+    hsnf4.attention_packed_bwd(q, k, v, o, lse, do, cu_q, H, KV, causal=causal, cu_k=cu_k,
+                               dq=out[0], dk=out[1], dv=out[2])
+    torch.cuda.synchronize()
+    assert hsnf4.device_status() == 0
+    refs = _attn_ref(q[:nq], k[:nk], v[:nk], lq, lk, H, KV, causal, scale, o[:nq], lse[:, :nq],
+                     do[:nq])
+    for got, (ref, tol), rows, name in zip(out, refs, (nq, nk, nk), ("dq", "dk", "dv")):
+        _within(got[:rows], ref, tol, name)
+        assert (got[rows:] == 7.0).all(), name
+
+
 def test_packed_attention_many_heads_large_scores_and_not_finite():
     d, KV, lens = 64, 2, [70, 50, 331, 9]
     H = _many_heads(lens)
