@@ -149,11 +149,17 @@ struct FwdGeo {
   static constexpr uint32_t kO = 128 * NQ, kCols = 256 * NQ;  // TMEM: S per tile, then O per tile
 };
 
-// A CTA takes 256 query rows of one head as two tiles of 128 and walks the
-// keys 128 at a time.  Each tile has eight warps: a row belongs to two
-// threads, in two warps, 64 of the 128 keys each.  TMEM: S0 S1 (128 columns each; P overwrites its S as bf16), O0 O1.
-// The tensor cores work on one tile's products while the other tile's
-// warpgroup computes its probabilities.
+// A CTA takes NQ tiles of 128 query rows of one head and walks the keys 128 at
+// a time.  Each tile has eight warps: a row belongs to two threads, in two
+// warps, 64 of the 128 keys each.  TMEM: an S per tile (P overwrites it as
+// bf16), an O per tile.  The tensor cores work on one tile's products while
+// the warps of the other (of the other CTA) compute its probabilities.
+//
+// One causal sequence, head_dim 128: 16384 tokens of 32/8 heads 2050 us, 1070
+// TFLOP/s, where the power limit lowers the clock to about 1.64 GHz with the
+// tensor pipe 53 % busy; 4096 of 28/4 heads 119 us.  Short calls are bound by
+// the latency of a CTA's start, chain and end, 5 us and 2 us a step (nine
+// sequences of 512 tokens: 8.5 us).
 template <int D, int NQ>
 __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
     packed_fwd_tc(const __grid_constant__ FwdTc P) {
@@ -272,8 +278,8 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
       for (int part = 0; part < 2; ++part) {
         if (!wait(&p_full[t][part], j)) return false;
         if (elect_one()) {
-          mma_ay_steps<D, 64>(tmem + G::kO + t * 128, tmem + t * 128, 64, stage(2 * j + 1), 2 * part,
-                              2, j > 0 || part > 0);
+          mma_ay_steps<D, 64>(tmem + G::kO + t * 128, tmem + t * 128, 64, stage(2 * j + 1),
+                              2 * part, 2, j > 0 || part > 0);
           if (part == 1) umma_commit(&o_full[t]);
         }
         __syncwarp();
@@ -462,7 +468,9 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
 // and O need 128 TMEM columns and four CTAs fit an SM: with 64 columns a
 // tile's products are half as long as with 128 and the chain from scores to
 // probabilities to the next scores weighs twice as much; four chains at once
-// hide it.  A thread owns a row (no exchange between warps).
+// hide it.  A thread owns a row (no exchange between warps).  One sequence of
+// 8192, 16/16 heads, no mask: 377 us, 730 TFLOP/s with issue slots 58 % and the
+// special-function unit 50 % busy.
 struct Fwd64Geo {
   static constexpr int kD = 64;
   static constexpr int kQ = tile_bytes<kD>(), kHalf = kStep * kD * 2;  // bytes of Q; of K or V
@@ -567,12 +575,12 @@ __global__ void __launch_bounds__(Fwd64Geo::kThreads, 4)
       tc_fence_after();
       if (elect_one()) {
         if (j > 0) {
-          mma_ay_n<D, kStep, kStep>(tmem + G::kO, tmem, 0, stage(i - 1), j > 1);
+          mma_ay<D, kStep, kStep>(tmem + G::kO, tmem, 0, stage(i - 1), j > 1);
           umma_commit(&o_full);
           umma_commit(&kv_empty[(i - 1) % NS]);
         }
         if (j < n) {
-          mma_xyt_n<D, kStep>(tmem, smem, stage(i));
+          mma_xyt<D, kStep>(tmem, smem, stage(i));
           umma_commit(&s_full);
           umma_commit(&kv_empty[i % NS]);
         }
@@ -724,7 +732,8 @@ struct BwdTc {
   uint16_t *dq, *dk, *dv;
   int64_t dqs, dks, dvs;
   PackedSeqs S;
-  int H, KV, splits, limit;  // splits: the most shares of a KV group's heads; limit: see tile_shares
+  int H, KV;
+  int splits, limit;  // the most shares of a KV group's heads; see tile_shares
   float scale, c;  // c = scale * log2(e)
 };
 
@@ -762,7 +771,10 @@ struct KvGeo {
 // end and waits hide behind the other's products: a tile's start and end are
 // about 10000 cycles of latency, as much as eight steps.  S of the next step
 // is computed as soon as the threads have read this one's; its dP follows
-// dQ's product, which reads dS.
+// dQ's product, which reads dS.  16384 tokens of 32/8 heads of 128: 2815 us,
+// 1180 TFLOP/s of its three products at the power limit (products of 64
+// columns run at two thirds of the rate of 128); 8150 tokens in 17, 28/4 heads:
+// 145 us.
 template <int D>
 struct DqGeo {
   static constexpr int kTile = tile_bytes<D>();  // Q, dO, O: 128 rows
@@ -881,7 +893,7 @@ __global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
       mma_issued = true;
       tc_fence_after();
       if (elect_one()) {
-        mma_xyt_n<D, kStep>(tmem + G::kS, Q, Ks + (i % NK) * G::kHalf);
+        mma_xyt<D, kStep>(tmem + G::kS, Q, Ks + (i % NK) * G::kHalf);
         umma_commit(&s_full);
       }
       __syncwarp();
@@ -895,10 +907,10 @@ __global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
       tc_fence_after();
       if (elect_one()) {
         if (i > 0) {
-          mma_ay_n<D, 32, kStep>(tmem, tmem + G::kDp, 32, Ks + ((i - 1) % NK) * G::kHalf, i > 1);
+          mma_ay<D, 32, kStep>(tmem, tmem + G::kDp, 32, Ks + ((i - 1) % NK) * G::kHalf, i > 1);
           umma_commit(&k_empty[(i - 1) % NK]);
         }
-        mma_xyt_n<D, kStep>(tmem + G::kDp, dO, Vs + (i % NV) * G::kHalf);
+        mma_xyt<D, kStep>(tmem + G::kDp, dO, Vs + (i % NV) * G::kHalf);
         umma_commit(&dp_full);
         umma_commit(&v_empty[i % NV]);
       }
@@ -908,7 +920,7 @@ __global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
     ok = ok && wait(&ds_full, n - 1);
     tc_fence_after();
     if (ok && elect_one()) {
-      mma_ay_n<D, 32, kStep>(tmem, tmem + G::kDp, 32, Ks + ((n - 1) % NK) * G::kHalf, n > 1);
+      mma_ay<D, 32, kStep>(tmem, tmem + G::kDp, 32, Ks + ((n - 1) % NK) * G::kHalf, n > 1);
       umma_commit(&done);
     }
     __syncwarp();
@@ -1066,7 +1078,10 @@ __device__ __forceinline__ int64_t part_at(const BwdTc& P, int slot, int kh, int
 // scores are computed transposed (a thread owns a key row, 32 of the step's
 // queries), so that P^T and dS^T, written as bf16 over the scores they came
 // from, are the tensor-memory operands of dV += P^T dO and dK += dS^T Q.
-// TMEM: S^T, dP^T, dV, dK.  While the threads
+// TMEM: S^T, dP^T, dV, dK.  16384 tokens of 32/8 heads of 128: 3280 us, 1357
+// TFLOP/s of its four products, 0.97 of a library product's rate under the same
+// power limit; 8150 tokens in 17, 28/4 heads: 145 us, 1.7 us a step and 9 us of
+// a CTA's start and end.  While the threads
 // compute P^T the tensor cores run the tile before's dK product and this
 // tile's dP^T; while they compute dS^T, dV and the next S^T.
 template <int D, int CTAS>
@@ -1076,9 +1091,8 @@ __global__ void __launch_bounds__(KvGeo<D, CTAS>::kThreads, CTAS)
   constexpr int NA = G::kA, NB = G::kB, kStep = G::kStep;  // stages of Q, of dO; queries of a step
   constexpr int kMmaWarp = G::kMmaWarp, kLoadWarp = G::kLoadWarp, kPatchWarp = G::kPatchWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ uint64_t kv_full, q_full[NA], ld_full[2], q_empty[NA], do_full[NB], do_empty[NB], q_raw[NA],
-      do_raw[NB],
-      s_full, dp_full, p_full, ds_full, done, drain;
+  __shared__ uint64_t kv_full, q_full[NA], q_raw[NA], q_empty[NA], ld_full[2], do_full[NB],
+      do_raw[NB], do_empty[NB], s_full, dp_full, p_full, ds_full, done, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ __align__(16) float nlse[2][kStep], nD[2][kStep];  // -lse log2(e), -D
@@ -1232,11 +1246,11 @@ __global__ void __launch_bounds__(KvGeo<D, CTAS>::kThreads, CTAS)
     auto Q = [&](int i) { return ring + (i % NA) * G::kRow; };
     auto dO = [&](int i) { return ring + (NA + i % NB) * G::kRow; };
     auto scores = [&](int i) {  // S^T = K Q^T (one thread)
-      mma_xyt_n<D, kStep>(tmem, smem, Q(i));
+      mma_xyt<D, kStep>(tmem, smem, Q(i));
       umma_commit(&s_full);
     };
     auto dprobs = [&](int i) {  // dP^T = V dO^T
-      mma_xyt_n<D, kStep>(tmem + G::kDp, smem + G::kTile, dO(i));
+      mma_xyt<D, kStep>(tmem + G::kDp, smem + G::kTile, dO(i));
       umma_commit(&dp_full);
     };
     bool ok = wait(&kv_full, 0) && wait(&q_full[0], 0) && wait(&do_full[0], 0);
@@ -1256,7 +1270,7 @@ __global__ void __launch_bounds__(KvGeo<D, CTAS>::kThreads, CTAS)
       const bool do_in = more && warp_test(&do_full[(i + 1) % NB], (i + 1) / NB);
       tc_fence_after();
       if (elect_one()) {
-        mma_ay_n<D, 32, kStep>(tmem + G::kDv, tmem, 32, dO(i), i > 0);  // dV += P^T dO
+        mma_ay<D, 32, kStep>(tmem + G::kDv, tmem, 32, dO(i), i > 0);  // dV += P^T dO
         umma_commit(&do_empty[i % NB]);
         if (more) scores(i + 1);
       }
@@ -1266,7 +1280,7 @@ __global__ void __launch_bounds__(KvGeo<D, CTAS>::kThreads, CTAS)
       q_in = i + 2 < n && warp_test(&q_full[(i + 2) % NA], (i + 2) / NA);
       tc_fence_after();
       if (elect_one()) {
-        mma_ay_n<D, 32, kStep>(tmem + G::kDk, tmem + G::kDp, 32, Q(i), i > 0);  // dK += dS^T Q
+        mma_ay<D, 32, kStep>(tmem + G::kDk, tmem + G::kDp, 32, Q(i), i > 0);  // dK += dS^T Q
         umma_commit(&q_empty[i % NA]);
         if (more) dprobs(i + 1);
       }
@@ -1350,7 +1364,8 @@ __global__ void __launch_bounds__(KvGeo<D, CTAS>::kThreads, CTAS)
       const int which = part / (G::kParts / 2), col = part % (G::kParts / 2) * G::kOut;  // 1: dK
       const uint32_t src = tmem + G::kDv + which * D + col + lanes;
       const int first = c0 + q4 * 32;
-      float4* share = P.part + part_at<D>(P, blockIdx.x / per, kh, split) + warp * (8 * G::kOut) + lane;
+      float4* share =
+          P.part + part_at<D>(P, blockIdx.x / per, kh, split) + warp * (8 * G::kOut) + lane;
       uint4 v[G::kOut / 8];
 #pragma unroll
       for (int b = 0; b < G::kOut / 32; ++b) {
@@ -1415,13 +1430,15 @@ __global__ void __launch_bounds__(KvGeo<D, CTAS>::kThreads, CTAS)
 // tokens (28/4 heads) took 40.0 us for 33.4, of 1024 tokens 65.0 for 57.9, of
 // 8150 in 17 sequences 306 for 309.
 template <int D, int CTAS>
-__global__ void __launch_bounds__(kReduceThreads) packed_kv_reduce(const __grid_constant__ BwdTc P) {
+__global__ void __launch_bounds__(kReduceThreads)
+    packed_kv_reduce(const __grid_constant__ BwdTc P) {
   __shared__ __align__(16) uint4 stage[4][32][4];
   constexpr int kParts = KvGeo<D, CTAS>::kParts, kOut = KvGeo<D, CTAS>::kOut;
   constexpr int kSteps = kParts * (kOut / 32);  // steps of a KV head
   PackedTile x;
   const int slot = blockIdx.x;
-  const bool found = find_tile<true>(P.S, true, slot, kRows, x);  // (an input, as in the kernel above)
+  // (the lengths are an input, as in the kernel above)
+  const bool found = find_tile<true>(P.S, true, slot, kRows, x);
   const int shares = found ? tile_shares(P, x) : 1;
   pdl_wait_then_release();
   if (shares == 1) return;
@@ -1480,7 +1497,9 @@ bool map_rows(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-int64_t most_tiles(int64_t T, int n_seq, int rows) { return T / rows + std::min<int64_t>(n_seq, T); }
+int64_t most_tiles(int64_t T, int n_seq, int rows) {
+  return T / rows + std::min<int64_t>(n_seq, T);
+}
 
 template <int D, int NQ>
 cudaError_t fwd_tc(const FwdTc& P, cudaStream_t st) {
@@ -1558,9 +1577,9 @@ cudaError_t kv_tc(const hsnf4_packed_attention& a, const PackedBwd& b, BwdTc& P,
   if (e != cudaSuccess || P.splits == 1) return e;
   const int64_t steps = a.KV * G::kParts * (G::kOut / 32);
   const int64_t ctas = sm_count() * (2048 / kReduceThreads);
+  const int64_t ways = std::min(std::max<int64_t>(ctas / tiles, 1), steps);
   return launch_pdl(packed_kv_reduce<D, CTAS>,
-                    dim3(static_cast<unsigned>(tiles),
-                         static_cast<unsigned>(std::min(std::max<int64_t>(ctas / tiles, 1), steps))),
+                    dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(ways)),
                     dim3(kReduceThreads), 0, st, P);
 }
 

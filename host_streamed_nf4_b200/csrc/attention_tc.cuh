@@ -21,7 +21,7 @@ constexpr int tile_bytes() {
   return D / 64 * kBoxBytes;
 }
 
-// N: the tile's tokens, and the rows of a box of `map`
+// N: the tile's tokens, and the rows of a box of `map` (64 rows: boxes of 8 KiB)
 template <int D, int N = kRows>
 __device__ __forceinline__ void tma_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
                                          int col, int row) {
@@ -40,37 +40,10 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from) {
   }
 }
 
-// d[128 x 128] = X Y^T over the D columns of two tiles (one thread issues)
-template <int D>
+// d[128 x N] = X Y^T over the D columns of two tiles, Y of N tokens (one
+// thread issues)
+template <int D, int N = kRows>
 __device__ __forceinline__ void mma_xyt(uint32_t d, const uint8_t* X, const uint8_t* Y) {
-  const uint64_t x0 = make_sdesc(smem_u32(X), 16, 1024, kLayoutSw128);
-  const uint64_t y0 = make_sdesc(smem_u32(Y), 16, 1024, kLayoutSw128);
-  constexpr uint32_t idesc = make_idesc_bf16(kRows, kRows, 0, 0);
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k) {
-    const uint64_t off = ((k / 4) * kBoxBytes + (k % 4) * 32) >> 4;
-    umma_bf16(d, x0 + off, y0 + off, idesc, k > 0 ? 1u : 0u);
-  }
-}
-
-// d[128 x D] (+)= A Y over the 128 tokens of tile Y; A is bf16 in tensor
-// memory, 16 tokens to 8 columns, in groups of GROUP tokens `stride` columns
-// apart.
-template <int D, int GROUP>
-__device__ __forceinline__ void mma_ay(uint32_t d, uint32_t a, uint32_t stride, const uint8_t* Y,
-                                       bool accumulate) {
-  const uint64_t y0 = make_sdesc(smem_u32(Y), kBoxBytes, 1024, kLayoutSw128);
-  constexpr uint32_t idesc = make_idesc_bf16(kRows, D, 0, 1);
-#pragma unroll
-  for (int k = 0; k < kRows / 16; ++k)
-    umma_bf16_ta(d, a + (k * 16 / GROUP) * stride + (k * 16 % GROUP) / 2,
-                 y0 + ((k * 2048) >> 4), idesc, accumulate || k > 0 ? 1u : 0u);
-}
-
-// The two products with a tile of N tokens (boxes of N rows) as the right
-// operand: d[128 x N] = X Y^T, and d[128 x D] (+)= A Y with A as in mma_ay.
-template <int D, int N>
-__device__ __forceinline__ void mma_xyt_n(uint32_t d, const uint8_t* X, const uint8_t* Y) {
   const uint64_t x0 = make_sdesc(smem_u32(X), 16, 1024, kLayoutSw128);
   const uint64_t y0 = make_sdesc(smem_u32(Y), 16, 1024, kLayoutSw128);
   constexpr uint32_t idesc = make_idesc_bf16(kRows, N, 0, 0);
@@ -80,9 +53,11 @@ __device__ __forceinline__ void mma_xyt_n(uint32_t d, const uint8_t* X, const ui
               y0 + (((k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc, k > 0 ? 1u : 0u);
 }
 
-template <int D, int GROUP, int N>
-__device__ __forceinline__ void mma_ay_n(uint32_t d, uint32_t a, uint32_t stride, const uint8_t* Y,
-                                         bool accumulate) {
+// d[128 x D] (+)= A Y over the N tokens of tile Y; A is bf16 in tensor memory,
+// 16 tokens to 8 columns, in groups of GROUP tokens `stride` columns apart.
+template <int D, int GROUP, int N = kRows>
+__device__ __forceinline__ void mma_ay(uint32_t d, uint32_t a, uint32_t stride, const uint8_t* Y,
+                                       bool accumulate) {
   const uint64_t y0 = make_sdesc(smem_u32(Y), N * 128, 1024, kLayoutSw128);
   constexpr uint32_t idesc = make_idesc_bf16(kRows, D, 0, 1);
 #pragma unroll

@@ -95,6 +95,19 @@ def test_rope(T, H, KV, d, half, sections, pairing, way, form):
             assert torch.equal(x, x0)
 
 
+@pytest.mark.parametrize("T,H,KV,d,half,sections,pairing", [
+    # several tokens and turns a CTA, the last one's partly behind the end
+    (40001, 2, 1, 64, 32, [10, 11, 11], "half"), (9000, 1, 1, 256, 128, None, "adjacent"),
+    (70003, 1, 0, 16, 8, None, "half"), (11111, 28, 4, 128, 64, None, "half")])
+def test_rope_long(T, H, KV, d, half, sections, pairing):
+    if KV:
+        return test_rope(T, H, KV, d, half, sections, pairing, "fwd", "in_place")
+    rope = hsnf4.Rope(d, hsnf4.rope_inv_freq(2 * half, 1e4), sections, pairing=pairing)
+    pos, q = torch.arange(T, dtype=torch.int32, device="cuda"), _normal((T, H * d), _gen(T))
+    ref, mag = _rope_ref(rope, pos, q, H, 1)
+    _within(hsnf4.rope_fwd(rope, pos, q), ref, U * ref.abs() + ROPE_W * mag, "rope")
+
+
 def test_rope_far_positions_and_ends():
     """Positions at the ends of int32 keep their angle, position 0 turns
     nothing, and the backward undoes the forward to rounding."""
