@@ -598,6 +598,46 @@ def test_grad_clip_many_small_and_repeats():
 
 # ---------------------------------------------------------------- streams and graphs
 
+def test_offsets_beyond_32_bits():
+    """Rope, attention with its gradients and clipping at the end of tensors
+    of more than 2^31 elements: the last sequence against 64 bits, rows
+    before it zero."""
+    H, KV, d, n = 64, 1, 128, 128
+    lens = [n] * 2100 + [77]
+    T, a = sum(lens), n * 2100
+    assert a * H * d > 2 ** 31
+    g = _gen(40)
+    q, do = (torch.zeros(T, H * d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.zeros(T, KV * d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for t in (q, k, v, do):
+        t[a:] = _normal((77, t.shape[1]), g)
+    rope = hsnf4.Rope(d, hsnf4.rope_inv_freq(d, 1e4))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    ref, mag = _rope_ref(rope, pos[a:].contiguous(), q[a:], H, 1)
+    hsnf4.rope_fwd(rope, pos, q, k, q, k)
+    _within(q[a:], ref, U * ref.abs() + ROPE_W * mag, "rope")
+    cu = _cu(lens)
+    o, lse = hsnf4.attention_packed_fwd(q, k, v, cu, H, KV)
+    args = ([77], [77], H, KV, True, d ** -0.5)
+    ro, rl, to = _attn_ref(q[a:], k[a:], v[a:], *args)
+    _within(o[a:], ro, to + 1e-30, "o")
+    _lse_within(lse[:, a:], rl, "lse")
+    dq, dk, dv = hsnf4.attention_packed_bwd(q, k, v, o, lse, do, cu, H, KV)
+    refs = _attn_ref(q[a:], k[a:], v[a:], *args, o[a:], lse[:, a:].contiguous(), do[a:])
+    for got, (r, tol), name in zip((dq, dk, dv), refs, ("dq", "dk", "dv")):
+        _within(got[a:], r, tol, name)
+    for t in (q, o, dq, dk, dv):
+        assert not t[:a].any()
+    gs = hsnf4.GradSet([dq])
+    want = dq[a:].double().norm()
+    before = dq[a:].clone()
+    norm = hsnf4.grad_clip(gs, 0.5 * float(want))
+    assert abs(float(norm) - float(want)) <= 2.0 ** -22 * float(want)
+    c = 0.5 * float(want) / (float(norm) + 1e-6)
+    assert ((dq[a:].double() - before.double() * c).abs()
+            <= (U + 2.0 ** -20) * before.double().abs() * c + 1e-38).all()
+
+
 def test_outputs_made_by_a_call_on_a_side_stream():
     """Outputs and workspaces that a call makes belong to its stream: the
     current stream, busy meanwhile, neither fills them late nor reuses them."""
