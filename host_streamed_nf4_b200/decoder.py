@@ -48,7 +48,9 @@ class DecoderStack(LayerStack):
                  seq_lens=None, **kw):
         """rope: an hsnf4.Rope of the family's head_dim; positions: int32
         [n_axes, T] on the device (default: each sequence counts from 0, on
-        every axis).  seq_lens: lengths of the packed sequences, T together."""
+        every axis).  seq_lens: lengths of the packed sequences, T together.
+        `positions` and `cu` (the sequences' starts and T) may be filled anew
+        between steps."""
         if family.head_dim != 128:
             raise ValueError("the attention kernels take head_dim 128")
         kw.setdefault("grouping", "decoder")
@@ -60,6 +62,9 @@ class DecoderStack(LayerStack):
         self.H, self.KV = H, KV
         if rope is not None and rope.head_dim != d:
             raise ValueError(f"rope has head_dim {rope.head_dim}, the family {d}")
+        if positions is not None and (rope is None or
+                                      tuple(positions.shape) != (rope.n_axes, T)):
+            raise ValueError("positions must be [rope.n_axes, T], with a rope")
         lens = [T] if seq_lens is None else [int(n) for n in seq_lens]
         if sum(lens) != T or min(lens) < 0:
             raise ValueError(f"seq_lens {lens} do not add up to T = {T}")

@@ -575,6 +575,8 @@ def _rope(fn, rope, pos, q, k, q_out, k_out, stream):
     T, wq = shape
     if wq % d:
         raise ValueError(f"q has {wq} columns, not a multiple of {d}")
+    if pos.shape != (rope.n_axes, T) and (rope.n_axes > 1 or pos.shape != (T,)):
+        _bad(pos, "pos", pos.dtype, pos.get_device(), f"[{rope.n_axes}, {T}]")
     p = _plain(pos, "pos", dev, _i32, rope.n_axes * T)
     if q_out is None:
         q_out = _new(torch.empty, shape, _bf16, q.device, stream)
@@ -641,6 +643,8 @@ def attention_packed_fwd(q, k, v, cu_q, H, KV, causal=True, cu_k=None, scale=Non
         o = _new(torch.zeros, sq, _bf16, q.device, stream)
     if lse is None:
         lse = _new(torch.zeros, (H, Tq), _f32, q.device, stream)
+    elif lse.shape != (H, Tq):
+        _bad(lse, "lse", lse.dtype, lse.get_device(), f"[{H}, {Tq}]")
     _launch(dev, stream, lib().decoder_attention_packed_fwd, ctypes.byref(a), o.data_ptr(),
             _rows(o, "o", dev, sq), _plain(lse, "lse", dev, _f32, H * Tq))
     return o, lse
@@ -658,6 +662,8 @@ def attention_packed_bwd(q, k, v, o, lse, dout, cu_q, H, KV, causal=True, cu_k=N
     """Its gradients from the forward's o and lse: (dq, dk, dv).  Rows outside
     every sequence are left as they are."""
     dev, sq, sk, d, a = _packed(q, k, v, cu_q, cu_k, H, KV, causal, scale)
+    if lse.shape != (H, sq[0]):
+        _bad(lse, "lse", lse.dtype, lse.get_device(), f"[{H}, {sq[0]}]")
     dq = _new(torch.zeros, sq, _bf16, q.device, stream) if dq is None else dq
     dk = _new(torch.zeros, sk, _bf16, q.device, stream) if dk is None else dk
     dv = _new(torch.zeros, sk, _bf16, q.device, stream) if dv is None else dv

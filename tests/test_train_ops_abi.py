@@ -17,6 +17,20 @@ def _refused(rc, status, *words):
         assert w in hsnf4.last_error(), hsnf4.last_error()
 
 
+def test_transposed_positions_and_lse_are_refused():
+    """As many values in another shape would be read in the wrong order."""
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    rope = hsnf4.Rope(64, hsnf4.rope_inv_freq(64, 1e4), [8, 12, 12])
+    pos, cu = torch.zeros(5, 3, dtype=torch.int32), torch.tensor([0, 5], dtype=torch.int32)
+    with pytest.raises(ValueError, match="pos must be"):
+        hsnf4.rope_fwd(rope, pos, bf(5, 64))
+    lse, t = torch.zeros(5, 2), bf(5, 128)
+    with pytest.raises(ValueError, match="lse must be"):
+        hsnf4.attention_packed_fwd(t, t, t, cu, 2, 2, o=bf(5, 128), lse=lse)
+    with pytest.raises(ValueError, match="lse must be"):
+        hsnf4.attention_packed_bwd(t, t, t, t, lse, t, cu, 2, 2)
+
+
 def test_rows_that_overlap_are_refused():
     """An expanded tensor has row stride 0, which the library reads as
     contiguous rows: it would leave the tensor's memory."""
