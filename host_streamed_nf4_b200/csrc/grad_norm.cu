@@ -9,10 +9,12 @@
 // launch serves any number of tensors); each CTA takes an equal contiguous
 // range of chunks, and the scaling pass walks its range from the end, where
 // the norm pass has just been, so that what the L2 still holds is not read
-// again from HBM.  The second launch is a programmatic dependent one.  1120
-// fp32 tensors of 842 MB: 419 us, 6.0 TB/s over the three passes; 448 bf16 ones
-// of odd sizes, 84 MB: 47 us (44 if they are aligned); 14 of 5.8 MB: 8.8 us, of
-// which the two launches are 6.
+// again from HBM.  The second launch is a programmatic dependent one.  The next
+// chunk's loads (16 KiB) are in flight while one is worked on, and three
+// CTAs per SM: 1120 fp32 tensors of 842 MB 406 us, 6.2 TB/s over the three
+// passes (418 with four CTAs and one chunk each); 448 bf16 ones of odd sizes,
+// 84 MB: 47 us (42 if they are aligned); 14 of 5.8 MB: 8.5 us, of which the two
+// launches are 6.
 //
 // Squares are added in fp32 over one 16-byte load, then in double; a load
 // whose fp32 sum leaves the safe range (overflow, underflow, NaN) is squared
@@ -35,7 +37,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunkBytes = 16384;
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 3;
 constexpr double kEps = 1e-6;
 
 struct Entry {  // one tensor, in the device table
@@ -227,17 +229,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_norm_kernel(const N
   double sum = 0.0;
   if (c0 < c1) {
     Cursor k = locate(P, c0);
+    uint4 next[kLoads];
+    load_chunk(k.x, Piece(k.x, c0), next);
     for (int64_t c = c0; c < c1; ++c) {
-      move_to(P, k, c);
-      const Piece p(k.x, c);
+      const Cursor k0 = k;  // of this chunk; the next one's loads are in flight meanwhile
+      const Piece p(k0.x, c);
       uint4 v[kLoads];
-      load_chunk(k.x, p, v);
-      if (k.x.dtype == HSNF4_F32)
-        sum += squares<HSNF4_F32>(k.x, p, v);
-      else if (k.x.dtype == HSNF4_BF16)
-        sum += squares<HSNF4_BF16>(k.x, p, v);
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) v[j] = next[j];
+      if (c + 1 < c1) {
+        move_to(P, k, c + 1);
+        load_chunk(k.x, Piece(k.x, c + 1), next);
+      }
+      if (k0.x.dtype == HSNF4_F32)
+        sum += squares<HSNF4_F32>(k0.x, p, v);
+      else if (k0.x.dtype == HSNF4_BF16)
+        sum += squares<HSNF4_BF16>(k0.x, p, v);
       else
-        sum += squares<HSNF4_F16>(k.x, p, v);
+        sum += squares<HSNF4_F16>(k0.x, p, v);
     }
   }
   sum = block_sum(sum, red);
@@ -267,16 +276,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const 
   if (f > 1.0) f = 1.0;
   const float coef = static_cast<float>(f);
   for (int64_t c = c1 - 1; c >= c0; --c) {
-    move_to(P, k, c);
-    if (coef == 1.0f && k.x.g == k.x.out) continue;  // nothing to clip, in place
-    const Piece p(k.x, c);
-    if (c < c1 - 1) load_chunk(k.x, p, v);
-    if (k.x.dtype == HSNF4_F32)
-      scale_chunk<HSNF4_F32>(k.x, p, v, coef);
-    else if (k.x.dtype == HSNF4_BF16)
-      scale_chunk<HSNF4_BF16>(k.x, p, v, coef);
+    const Cursor k0 = k;
+    const Piece p(k0.x, c);
+    uint4 now[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) now[j] = v[j];
+    if (c > c0) {
+      move_to(P, k, c - 1);
+      // (nothing to clip, in place: not read)
+      if (coef != 1.0f || k.x.g != k.x.out) load_chunk(k.x, Piece(k.x, c - 1), v);
+    }
+    if (coef == 1.0f && k0.x.g == k0.x.out) continue;
+    if (k0.x.dtype == HSNF4_F32)
+      scale_chunk<HSNF4_F32>(k0.x, p, now, coef);
+    else if (k0.x.dtype == HSNF4_BF16)
+      scale_chunk<HSNF4_BF16>(k0.x, p, now, coef);
     else
-      scale_chunk<HSNF4_F16>(k.x, p, v, coef);
+      scale_chunk<HSNF4_F16>(k0.x, p, now, coef);
   }
 }
 
