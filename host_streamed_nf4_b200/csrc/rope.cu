@@ -17,7 +17,7 @@
 // more (as many as 32 KiB hold the cos and sin of) and computes those once.
 // A thread keeps its place in the head and walks the heads and tokens, its
 // first loads in flight while the angles are computed.  8191 tokens of 64/8
-// heads of 128: 55.6 us, 5.4 TB/s; 16000 of 16/16 heads of 64: 25.5 us, 29.0
+// heads of 128: 51.4 us, 5.9 TB/s; 16000 of 16/16 heads of 64: 25.5 us, 29.0
 // with at most 16 tokens a CTA; with few heads a token the angles are the time
 // (32768 tokens of 2/1 heads of 128: 17.8 us, 2.8 TB/s).
 #include <cuda_bf16.h>
@@ -200,8 +200,8 @@ cudaError_t launch_rope(const hsnf4_rope& R, const RopeTensors& t, int64_t T, in
     P.axis[i] = R.axis[i];
   }
   // several tokens at once if all their heads fit the threads, else the heads
-  // of one in equal passes; and, in a long sequence, more tokens in turn, so
-  // that each SM gets its CTAs once
+  // of one in equal passes, two or three of them at once; and, in a long
+  // sequence, more tokens in turn, so that each SM gets its CTAs once
   const int heads = H + KV, per_token = heads * P.per_head;
   const int max_tokens = kMaxAngles / P.half;
   P.par = std::min(std::max(kThreads / per_token, 1), max_tokens);
@@ -213,13 +213,26 @@ cudaError_t launch_rope(const hsnf4_rope& R, const RopeTensors& t, int64_t T, in
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t slots = static_cast<int64_t>(sms) * (passes == 1 ? 5 : 4);
-  const int64_t turns = (T + slots * P.par - 1) / (slots * P.par);
+  // As many CTAs per SM as fit, unless fewer share the turns out more evenly
+  // (8191 tokens of 72 heads of 128: four with 14 turns 51.4 us, five with 12
+  // 55.2; 9000 of 40 heads: four with 16 38.2, six with 11 35.8).
+  const int fit = 65536 / ((passes == 1 ? 48 : 64) * threads);
+  int64_t turns = 1, least = 0;
+  for (int c = std::min(fit, 8); c >= 4; --c) {
+    const int64_t n = (T + int64_t(sms) * c * P.par - 1) / (int64_t(sms) * c * P.par);
+    const int64_t ctas = (T + n * P.par - 1) / (n * P.par), per_sm = (ctas + sms - 1) / sms * n;
+    if (least == 0 || per_sm * 20 < least * 19) turns = n, least = per_sm;
+  }
   P.tokens = P.par * static_cast<int>(std::min<int64_t>(turns, std::max(1, max_tokens / P.par)));
   const int64_t grid = (T + P.tokens - 1) / P.tokens;
   const size_t smem = static_cast<size_t>(P.tokens) * P.half * sizeof(float2);
-  const auto kernel = half ? (passes == 1 ? rope_kernel<true, 1> : rope_kernel<true, 2>)
-                           : (passes == 1 ? rope_kernel<false, 1> : rope_kernel<false, 2>);
+  const int batch = passes == 1 ? 1 : passes == 2 || passes == 4 ? 2 : 3;
+  const auto kernel = half ? (batch == 1   ? rope_kernel<true, 1>
+                              : batch == 2 ? rope_kernel<true, 2>
+                                           : rope_kernel<true, 3>)
+                           : (batch == 1   ? rope_kernel<false, 1>
+                              : batch == 2 ? rope_kernel<false, 2>
+                                           : rope_kernel<false, 3>);
   count_launch();
   kernel<<<static_cast<unsigned>(grid), threads, smem, st>>>(P);
   return cudaGetLastError();
