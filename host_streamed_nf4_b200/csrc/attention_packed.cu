@@ -1102,7 +1102,9 @@ __global__ void __launch_bounds__(KvGeo<D, CTAS>::kThreads, CTAS)
   if (warp == 0 && lane == 0) prefetch_maps(P);
   // The CTA starts while the dQ kernel ends.  That kernel let this one in after
   // its own wait, so the call's inputs stand; only D is waited for (every CTA
-  // waits, so that this kernel never ends before that one).
+  // waits, so that this kernel never ends before that one).  It holds TMEM
+  // meanwhile: no more than two of its and the dQ kernel's CTAs fit an SM's
+  // shared memory, and two have TMEM enough, so no dQ CTA waits for it there.
   pdl_release();
   // (before anything is set up: the grid covers the most tiles and shares)
   PackedTile x;

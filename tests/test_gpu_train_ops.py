@@ -638,6 +638,47 @@ def test_offsets_beyond_32_bits():
             <= (U + 2.0 ** -20) * before.double().abs() * c + 1e-38).all()
 
 
+def test_calls_at_once():
+    """Steps of different sizes and head dimensions on three streams at once,
+    each with its own workspaces, repeat what they give alone."""
+    steps = []
+    for lens, H, KV, d, causal in (([512] * 8, 28, 4, 128, True), ([64] * 40, 16, 16, 64, False),
+                                   ([900, 3, 700], 40, 20, 64, True)):
+        q, k, v, do = _attn_inputs(lens, lens, H, KV, d, "fused", 50 + d)
+        cu, pos = _cu(lens), torch.arange(sum(lens), dtype=torch.int32, device="cuda")
+        rope = hsnf4.Rope(d, hsnf4.rope_inv_freq(d, 1e4))
+        o, lse = hsnf4.attention_packed_fwd(q, k, v, cu, H, KV, causal=causal)
+        g = hsnf4.attention_packed_bwd(q, k, v, o, lse, do, cu, H, KV, causal=causal)
+        ws = torch.empty(hsnf4.attention_packed_workspace_bytes(sum(lens), sum(lens), len(lens),
+                                                                H, KV, d),
+                         dtype=torch.uint8, device="cuda")
+        q1, k1 = torch.empty_like(do), torch.empty_like(g[1])
+        out = [torch.empty_like(t) for t in g]
+        gs = hsnf4.GradSet(g, outs=out)
+
+        def step(stream=None, a=(q, k, v, do, cu, H, KV, causal, pos, rope, ws, o, lse, g, gs, q1,
+                                 k1)):
+            q, k, v, do, cu, H, KV, causal, pos, rope, ws, o, lse, g, gs, q1, k1 = a
+            hsnf4.rope_fwd(rope, pos, q, k, q1, k1, stream=stream)
+            hsnf4.attention_packed_fwd(q1, k1, v, cu, H, KV, causal=causal, o=o, lse=lse,
+                                       stream=stream)
+            hsnf4.attention_packed_bwd(q1, k1, v, o, lse, do, cu, H, KV, causal=causal, dq=g[0],
+                                       dk=g[1], dv=g[2], workspace=ws, stream=stream)
+            hsnf4.grad_clip(gs, 1.0, stream=stream)
+
+        step()
+        torch.cuda.synchronize()
+        outs = [q1, k1, o, lse, *g, *out]
+        steps.append((step, outs, [t.clone() for t in outs], torch.cuda.Stream()))
+    for _ in range(20):
+        for step, *_, stream in steps:
+            step(stream)
+    torch.cuda.synchronize()
+    assert hsnf4.device_status() == 0
+    for _, outs, want, _ in steps:
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
 def test_outputs_made_by_a_call_on_a_side_stream():
     """Outputs and workspaces that a call makes belong to its stream: the
     current stream, busy meanwhile, neither fills them late nor reuses them."""
