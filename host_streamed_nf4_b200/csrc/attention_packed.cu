@@ -224,11 +224,15 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
 
   if (warp == kLoadWarp && n) {
     // ---------------------------------------------- TMA: Q, then K0 V0 K1 V1 ...
-    const bool two = NQ == 2 && r0 + kRows < x.lq;
+    // (of a tile that sees no key only the output's zeros are staged there,
+    // without a wait: no copy may be on its way)
     if (lane == 0) {
-      mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * G::kTile);
-      tma_tile<D>(smem, &P.mq, &q_full, h * D, x.q0 + r0);
-      if (two) tma_tile<D>(smem + G::kTile, &P.mq, &q_full, h * D, x.q0 + r0 + kRows);
+      int tiles = 0;
+      for (int t = 0; t < NQ; ++t) tiles += nt[t] > 0;
+      mbar_arrive_expect_tx(&q_full, tiles * G::kTile);
+      for (int t = 0; t < NQ; ++t)
+        if (nt[t])
+          tma_tile<D>(smem + t * G::kTile, &P.mq, &q_full, h * D, x.q0 + r0 + t * kRows);
     }
     q_loaded = true;
     for (int i = 0; i < 2 * n; ++i) {

@@ -1,0 +1,37 @@
+"""Rotary positions, packed attention and gradient clipping in calls at the
+edges of what the header allows: two query tiles per CTA, queries without a
+key beside values that are not finite, memory around the tensors, streams.
+
+Tolerances are those of the operators' other tests, with their reasons."""
+import pytest
+import torch
+
+import test_gpu_train_ops as ops
+from host_streamed_nf4_b200 import hsnf4
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- packed attention
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lq,lk", [(6400, 100), (7000, 900), (8192, 7000)])
+def test_first_query_tile_of_a_pair_without_keys(d, lq, lk):
+    """One long sequence (two query tiles per CTA) whose queries outnumber the
+    keys so that the causal mask leaves a pair's first tile nothing and its
+    second one something: the first one's rows are 0, -inf."""
+    H, KV = 2, 1
+    assert 128 < (lq - lk) % 256 < 256
+    q, k, v, do = ops._attn_inputs([lq], [lk], H, KV, d, "padded", lk)
+    o = torch.full_like(do, 7.0)
+    lse = torch.full((H, q.shape[0]), 7.0, device="cuda")
+    cu_q, cu_k = ops._cu([lq]), ops._cu([lk])
+    ref, rl, tol = ops._attn_ref(q[:lq], k[:lk], v[:lk], [lq], [lk], H, KV, True, d ** -0.5)
+    for _ in range(8):
+        hsnf4.attention_packed_fwd(q, k, v, cu_q, H, KV, cu_k=cu_k, o=o, lse=lse)
+        torch.cuda.synchronize()
+        assert hsnf4.device_status() == 0
+        assert not o[:lq - lk].any() and torch.isneginf(lse[:, :lq - lk]).all()
+        ops._within(o[:lq], ref, tol + 1e-30, "o")
+        ops._lse_within(lse[:, :lq], rl, "lse")
+        assert (o[lq:] == 7.0).all() and (lse[:, lq:] == 7.0).all()
