@@ -429,9 +429,8 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
 #pragma unroll
       for (int b = 0; b < D / 64; ++b) {
         uint32_t o[32];
-        if (nt[t]) {
-          load_quarter(O_h + 32 * b, o);
-        } else {
+        if (nt[t]) load_quarter(O_h + 32 * b, o);
+        if (!nt[t] || !some) {  // (also where 0 times a value that is not finite was added)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
@@ -687,9 +686,8 @@ __global__ void __launch_bounds__(Fwd64Geo::kThreads, 4)
 #pragma unroll
       for (int b = 0; b < D / 32; ++b) {
         uint32_t o[32];
-        if (n) {
-          load_quarter(O_r + 32 * b, o);
-        } else {
+        if (n) load_quarter(O_r + 32 * b, o);
+        if (!n || !some) {  // (as above)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
@@ -1012,9 +1010,8 @@ __global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
 #pragma unroll
       for (int b = 0; b < D / 64; ++b) {
         uint32_t o[32];
-        if (n) {
-          load_quarter(tmem + part * (D / 2) + 32 * b + lanes, o);
-        } else {
+        if (n) load_quarter(tmem + part * (D / 2) + 32 * b + lanes, o);
+        if (limit <= 0) {  // no key (also where 0 times a key that is not finite was added)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }

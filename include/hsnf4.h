@@ -472,7 +472,8 @@ int decoder_rope_bwd(const hsnf4_rope *rope, const int32_t *pos, int64_t T, int 
  * bf16 as operands); softmax statistics are fp32.  A value that is not finite
  * reaches every result that the formulas give it a part in, and may reach
  * others of its own sequence and KV head (a causal mask makes factors 0, and
- * 0 times it is NaN), never those of another sequence or KV head. */
+ * 0 times it is NaN), never those of another sequence or KV head, nor of a
+ * query that sees no key. */
 typedef struct {
   const void *q, *k, *v;  /* bf16; heads contiguous within a token */
   int64_t q_stride, k_stride, v_stride; /* elements between tokens (multiples

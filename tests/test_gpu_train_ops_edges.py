@@ -35,3 +35,21 @@ def test_first_query_tile_of_a_pair_without_keys(d, lq, lk):
         ops._within(o[:lq], ref, tol + 1e-30, "o")
         ops._lse_within(lse[:, :lq], rl, "lse")
         assert (o[lq:] == 7.0).all() and (lse[:, lq:] == 7.0).all()
+
+
+@pytest.mark.parametrize("d,H,KV,lq,lk", [
+    (64, 2, 1, 200, 30), (128, 2, 1, 200, 30), (64, 2, 1, 6300, 30), (128, 2, 1, 6300, 30),
+    (64, 1000, 2, 200, 30)])  # (so many heads take 64 keys a step)
+@pytest.mark.parametrize("value", [ops.NAN, float("inf")])
+def test_queries_without_keys_beside_values_that_are_not_finite(d, H, KV, lq, lk, value):
+    """A query that sees no key gives 0, -inf and no gradient whatever its
+    sequence's keys and values hold, in the tile of queries that see some too."""
+    q, k, v, do = ops._attn_inputs([lq], [lk], H, KV, d, "plain", d)
+    k[3, 5], v[7, 9] = value, value
+    cu_q, cu_k, none = ops._cu([lq]), ops._cu([lk]), lq - lk
+    o, lse = hsnf4.attention_packed_fwd(q, k, v, cu_q, H, KV, cu_k=cu_k)
+    dq, _, _ = hsnf4.attention_packed_bwd(q, k, v, o, lse, do, cu_q, H, KV, cu_k=cu_k)
+    torch.cuda.synchronize()
+    assert hsnf4.device_status() == 0
+    assert not o[:none].any() and torch.isneginf(lse[:, :none]).all() and not dq[:none].any()
+    assert torch.isfinite(lse[:, none:none + 3]).all()  # these see finite keys alone
