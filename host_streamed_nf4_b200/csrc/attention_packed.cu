@@ -43,6 +43,9 @@ enum : unsigned int {
 // Of every kPolyOf pairs of exponentials, kPolyPart go to the fp32 pipe.
 constexpr int kPolyOf = 8, kPolyPart = 2;
 constexpr int kReduceThreads = 512;
+// The least reference of a row's exponentials, of a row whose first keys'
+// scores are all -inf: with any more, later scores far below it would be lost.
+constexpr float kLowRef = -3.402823466e38f;
 
 // mbar_wait with the abort word and the timer looked at every 32 polls only:
 // reading the timer takes hundreds of cycles, by which each wait ended late.
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
         pair_sync(pair);
         const float m = fmaxf(mt, row_x[half ^ 1][t][tid]);
         if (j == 0) {
-          ref = m == -INFINITY ? 0.0f : m;  // a row without a key: all 0
+          ref = fmaxf(m, kLowRef);
         } else {
           ok = pair_all(pair, warp_wait(&o_full[t], (j - 1), abort_p, kAtFlagCompute));
           if (!ok) break;
@@ -626,7 +629,7 @@ __global__ void __launch_bounds__(Fwd64Geo::kThreads, 4)
       const float mt = row < x.lq ? max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3])) * P.c
                                   : -INFINITY;
       if (j == 0) {
-        ref = mt == -INFINITY ? 0.0f : mt;
+        ref = fmaxf(mt, kLowRef);
       } else if (__any_sync(0xffffffffu, mt > ref + 8.0f)) {
         ok = warp_wait(&o_full, j - 1, abort_p, kAtFlagCompute);
         if (!ok) break;

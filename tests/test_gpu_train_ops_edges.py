@@ -53,3 +53,24 @@ def test_queries_without_keys_beside_values_that_are_not_finite(d, H, KV, lq, lk
     assert hsnf4.device_status() == 0
     assert not o[:none].any() and torch.isneginf(lse[:, :none]).all() and not dq[:none].any()
     assert torch.isfinite(lse[:, none:none + 3]).all()  # these see finite keys alone
+
+
+@pytest.mark.parametrize("d,H,KV,lq", [(64, 2, 1, 150), (128, 2, 1, 150), (64, 2, 1, 6200),
+                                       (128, 2, 1, 6200), (64, 1000, 2, 150)])
+def test_first_keys_with_scores_of_minus_infinity(d, H, KV, lq):
+    """130 keys whose scores are -inf in every query, then keys with scores
+    near -256: the softmax of those, as without the first ones.  Whole numbers, so that
+    the scores are exact."""
+    lk, g = 300, ops._gen(lq + d)
+    small = lambda t, n: torch.randint(-1, 2, (t, n, d), generator=g, device="cuda").bfloat16()
+    q, k = small(lq, H), small(lk, KV)
+    q[..., 0], q[..., 1], k[..., 1] = 1, 32, -32
+    k[:130, :, 0] = -float("inf")
+    q, k, v = q.flatten(1), k.flatten(1), ops._normal((lk, KV * d), g)
+    o, lse = hsnf4.attention_packed_fwd(q, k, v, ops._cu([lq]), H, KV, causal=False,
+                                        cu_k=ops._cu([lk]), scale=0.25)
+    torch.cuda.synchronize()
+    assert hsnf4.device_status() == 0
+    ref, rl, tol = ops._attn_ref(q, k, v, [lq], [lk], H, KV, False, 0.25)
+    ops._within(o, ref, tol + 1e-30, "o")
+    ops._lse_within(lse, rl, "lse")
