@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
   __shared__ float row_x[2][NQ][kRows];  // [half][tile][row]: exchanged between two warps
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0 && lane == 0) prefetch_maps(P);
-  pdl_wait_then_release();
+  pdl_wait();
   // (before anything is set up: the grid covers the most tiles there could be)
   PackedTile x;
   if (!find_tile(P.S, false, blockIdx.x / P.H, NQ * kRows, x)) return;
@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_release();  // (after the allocation)
   // with two tiles all 512 columns are this CTA's: a base known at compile time
   const uint32_t tmem = NQ == 2 ? 0u : tmem_slot;
   volatile int* abort_p = &abort_flag;
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(Fwd64Geo::kThreads, 4)
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0 && lane == 0) prefetch_maps(P);
-  pdl_wait_then_release();
+  pdl_wait();
   // (before anything is set up: the grid covers the most tiles there could be)
   PackedTile x;
   if (!find_tile(P.S, false, blockIdx.x / P.H, kRows, x)) return;
@@ -521,6 +522,7 @@ __global__ void __launch_bounds__(Fwd64Geo::kThreads, 4)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_release();  // (after the allocation)
   const uint32_t tmem = tmem_slot;
   volatile int* abort_p = &abort_flag;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need the alignment asked for
@@ -803,7 +805,7 @@ __global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
   __shared__ float row_x[kRows];  // dO . O, exchanged between the two threads of a row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0 && lane == 0) prefetch_maps(P);
-  pdl_wait_then_release();
+  pdl_wait();
   // (before anything is set up: the grid covers the most tiles there could be)
   PackedTile x;
   if (!find_tile(P.S, false, blockIdx.x / P.H, kRows, x)) return;
@@ -836,6 +838,7 @@ __global__ void __launch_bounds__(DqGeo<D>::kThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_release();  // (after the allocation)
   const uint32_t tmem = tmem_slot;
   volatile int* abort_p = &abort_flag;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need the alignment asked for
@@ -1107,9 +1110,7 @@ __global__ void __launch_bounds__(KvGeo<D, CTAS>::kThreads, CTAS)
   // The CTA starts while the dQ kernel ends.  That kernel let this one in after
   // its own wait, so the call's inputs stand; only D is waited for (every CTA
   // waits, so that this kernel never ends before that one).  It holds TMEM
-  // meanwhile: no more than two of its and the dQ kernel's CTAs fit an SM's
-  // shared memory, and two have TMEM enough, so no dQ CTA waits for it there.
-  pdl_release();
+  // meanwhile, which no dQ CTA waits for: they have theirs before they let it in.
   // (before anything is set up: the grid covers the most tiles and shares)
   PackedTile x;
   const bool found = find_tile<true>(P.S, true, blockIdx.x / per, kRows, x);
@@ -1147,6 +1148,7 @@ __global__ void __launch_bounds__(KvGeo<D, CTAS>::kThreads, CTAS)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_release();  // (after the allocation)
   // with all 512 columns this CTA's: a base known at compile time
   const uint32_t tmem = G::kCols == 512 ? 0u : tmem_slot;
   volatile int* abort_p = &abort_flag;

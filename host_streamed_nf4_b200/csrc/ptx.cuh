@@ -168,6 +168,11 @@ __device__ __forceinline__ bool elect_one() {
 // its first global-memory access, read or write: the wait returns once the
 // previous grid has completed and its writes are visible, exactly as plain
 // stream order would give.  Then the next kernel may be scheduled.
+//
+// A kernel that allocates TMEM releases the next one only behind its own
+// allocation (or the CTA's end): the next kernel may allocate before its wait
+// and hold the columns until this grid has ended, and an allocation waits
+// without a limit.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
