@@ -56,18 +56,24 @@ class DecoderStack(LayerStack):
         kw.setdefault("grouping", "decoder")
         if kw["grouping"] != "decoder":
             raise ValueError("a decoder layer runs its projections in decoder grouping")
-        super().__init__(family, n_layers, T, **kw)
-        dev, f = self.device, family
-        h, I, H, KV, d = f.hidden, f.inter, f.heads, f.kv_heads, f.head_dim
-        self.H, self.KV = H, KV
-        if rope is not None and rope.head_dim != d:
-            raise ValueError(f"rope has head_dim {rope.head_dim}, the family {d}")
-        if positions is not None and (rope is None or
-                                      tuple(positions.shape) != (rope.n_axes, T)):
-            raise ValueError("positions must be [rope.n_axes, T], with a rope")
+        if rope is not None and rope.head_dim != family.head_dim:
+            raise ValueError(f"rope has head_dim {rope.head_dim}, the family {family.head_dim}")
+        if positions is not None:
+            if rope is None or tuple(positions.shape) != (rope.n_axes, T):
+                raise ValueError("positions must be [rope.n_axes, T], with a rope")
+            if positions.dtype is not torch.int32:
+                raise TypeError(f"positions must be an int32 tensor, got {positions.dtype}")
+            if not positions.is_cuda or not positions.is_contiguous():
+                raise ValueError("positions must be a contiguous tensor on the stack's device")
         lens = [T] if seq_lens is None else [int(n) for n in seq_lens]
         if sum(lens) != T or min(lens) < 0:
             raise ValueError(f"seq_lens {lens} do not add up to T = {T}")
+        super().__init__(family, n_layers, T, **kw)
+        dev, f = self.device, family
+        if positions is not None and positions.device != self.grad_flat.device:
+            raise ValueError(f"positions are on {positions.device}, the stack on {dev}")
+        h, I, H, KV, d = f.hidden, f.inter, f.heads, f.kv_heads, f.head_dim
+        self.H, self.KV = H, KV
         self.rope, self.positions, self.cu = rope, positions, None
         if rope is not None and positions is None:
             count = torch.cat([torch.arange(n, dtype=torch.int32) for n in lens])
