@@ -173,7 +173,8 @@ class LayerStack:
         self.ws_f = torch.empty(ws_f, dtype=torch.uint8, device=dev)
         self.ws_b = torch.empty(ws_b, dtype=torch.uint8, device=dev)
         self._prefetched = False
-        self._grad_set = None
+        # (here: making a set waits for the device and is refused during capture)
+        self._grad_set = hsnf4.GradSet([self.grad_flat], stream=self.compute)
         torch.cuda.synchronize(dev)
 
     # ------------------------------------------------------------------ setup
@@ -385,8 +386,6 @@ class LayerStack:
         (their global norm + 1e-6)), on the compute stream; returns the norm
         before that (a device scalar).  With several ranks, after their
         gradients are summed."""
-        if self._grad_set is None:
-            self._grad_set = hsnf4.GradSet([self.grad_flat], stream=self.compute)
         return hsnf4.grad_clip(self._grad_set, max_norm, norm=norm, stream=self.compute)
 
     # ------------------------------------------------------------------ checks
