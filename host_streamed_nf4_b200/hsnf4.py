@@ -687,7 +687,8 @@ class GradSet:
     """A fixed list of gradient tensors (fp32, bf16 or fp16, contiguous, any
     mix) for grad_norm and grad_clip.  outs: where clipped gradients go, each
     of its gradient's type and size (default: in place).  The set keeps the
-    tensors' addresses, so their memory must not be replaced."""
+    tensors' addresses, so their memory must not be replaced, and a graph that
+    captured a call needs the set for as long as it is replayed."""
 
     def __init__(self, tensors, outs=None, stream=None):
         self.tensors = list(tensors)
@@ -718,6 +719,8 @@ class GradSet:
                                                                ctypes.byref(self.plan), *a))
         self.workspace = self.new_workspace(stream)
         self._ref = ctypes.byref(self.plan)
+        # the streams that the table's and workspace's memory is known to be used on
+        self._streams = {_raw_stream(index) if stream is None else stream.cuda_stream}
 
     def new_workspace(self, stream=None) -> torch.Tensor:
         """A workspace for calls on `stream` that may run at the same time as
@@ -732,6 +735,12 @@ class GradSet:
         ws = self.workspace if workspace is None else workspace
         if workspace is not None and (ws.get_device() != self.index or not ws.is_contiguous()):
             raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        at = _raw_stream(self.index) if stream is None else stream.cuda_stream
+        if at not in self._streams:  # else a set dropped after the call frees them too early
+            used = torch.cuda.current_stream(self.index) if stream is None else stream
+            self.table.record_stream(used)
+            self.workspace.record_stream(used)
+            self._streams.add(at)
         _launch(self.index, stream, fn, self._ref, *args,
                 _plain(norm, "norm", self.index, _f32, 1), ws.data_ptr(), ws.nbytes)
         return norm

@@ -74,3 +74,36 @@ def test_first_keys_with_scores_of_minus_infinity(d, H, KV, lq):
     ref, rl, tol = ops._attn_ref(q, k, v, [lq], [lk], H, KV, False, 0.25)
     ops._within(o, ref, tol + 1e-30, "o")
     ops._lse_within(lse, rl, "lse")
+
+
+# ---------------------------------------------------------------- gradient norm
+
+@pytest.mark.parametrize("given", [True, False])
+def test_set_dropped_while_another_stream_uses_it(given):
+    """The table of addresses and the workspace stay the set's until a call
+    on another stream has ended, though nothing refers to the set any more."""
+    grads = [torch.ones(n, device="cuda") for n in (5, 4096, 77)]
+    norm, x = torch.zeros((), device="cuda"), torch.zeros(4096, 4096, device="cuda")
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    hsnf4.grad_clip(hsnf4.GradSet(grads), 1.0, norm=norm)  # (loading code waits for the device)
+    x = x @ x
+    gs = hsnf4.GradSet(grads)
+    mine = {gs.table.data_ptr(), gs.workspace.data_ptr()}
+    sizes = (gs.table.nbytes, gs.workspace.nbytes)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(60):  # some tens of milliseconds
+            x = x @ x
+    if given:
+        hsnf4.grad_clip(gs, 1.0, norm=norm, stream=side)
+    else:
+        with torch.cuda.stream(side):
+            hsnf4.grad_clip(gs, 1.0, norm=norm)
+    done.record(side)
+    del gs
+    later = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(8)]
+    assert not done.query()  # the call is still to come
+    assert not mine & {t.data_ptr() for t in later}
+    torch.cuda.synchronize()
+    # the call before left a norm of 1 / (1 + 1e-6 / norm)
+    assert abs(float(norm) - 1.0) <= 2.0 ** -20
