@@ -803,6 +803,11 @@ static int check_packed(const char* fn, hsnf4_packed_attention* a) {
   return rc;
 }
 
+// the cumulative lengths, as one row of 16-bit words
+static Rows cu_rows(const hsnf4_packed_attention& a, const int32_t* cu, const char* name) {
+  return {cu, 0, 2 * (static_cast<int64_t>(a.n_seq) + 1), 1, name};
+}
+
 int decoder_attention_packed_fwd(const hsnf4_packed_attention* args, void* o, int64_t o_stride,
                                  float* lse, void* stream) {
   static const char* fn = "decoder_attention_packed_fwd";
@@ -816,9 +821,10 @@ int decoder_attention_packed_fwd(const hsnf4_packed_attention* args, void* o, in
   if (rc) return rc;
   const Rows q = {a.q, a.q_stride, wq, a.Tq, "q"}, k = {a.k, a.k_stride, wk, a.Tk, "k"},
              v = {a.v, a.v_stride, wk, a.Tk, "v"}, ro = {o, o_stride, wq, a.Tq, "o"},
-             rl = {lse, 0, 2 * a.H * a.Tq, 1, "lse"};
-  rc = check_disjoint(fn, ro, {q, k, v, rl});
-  if (!rc) rc = check_disjoint(fn, rl, {q, k, v});
+             rl = {lse, 0, 2 * a.H * a.Tq, 1, "lse"}, cq = cu_rows(a, a.cu_q, "cu_q"),
+             ck = cu_rows(a, a.cu_k, "cu_k");
+  rc = check_disjoint(fn, ro, {q, k, v, rl, cq, ck});
+  if (!rc) rc = check_disjoint(fn, rl, {q, k, v, cq, ck});
   if (rc) return rc;
   return cuda_status(launch_packed_fwd(a, o, o_stride, lse, static_cast<cudaStream_t>(stream)),
                      "decoder_attention_packed_fwd launch");
@@ -860,7 +866,10 @@ int decoder_attention_packed_bwd(const hsnf4_packed_attention* args, const void*
                      {o, o_stride, wq, a.Tq, "o"},
                      {dout, dout_stride, wq, a.Tq, "dout"},
                      {lse, 0, 2 * a.H * a.Tq, 1, "lse"},
+                     cu_rows(a, a.cu_q, "cu_q"),
+                     cu_rows(a, a.cu_k, "cu_k"),
                      {workspace, 0, static_cast<int64_t>(need / 2), 1, "workspace"}};
+  constexpr int kIn = sizeof in / sizeof in[0];  // the last of them is written too
   const Rows out[] = {{dq, dq_stride, wq, a.Tq, "dq"},
                       {dk, dk_stride, wk, a.Tk, "dk"},
                       {dv, dv_stride, wk, a.Tk, "dv"}};
@@ -870,8 +879,8 @@ int decoder_attention_packed_bwd(const hsnf4_packed_attention* args, const void*
     for (int j = 0; j < i; ++j)
       if ((rc = check_disjoint(fn, out[i], {out[j]}))) return rc;
   }
-  for (int j = 0; j < 6; ++j)
-    if ((rc = check_disjoint(fn, in[6], {in[j]}))) return rc;
+  for (int j = 0; j + 1 < kIn; ++j)
+    if ((rc = check_disjoint(fn, in[kIn - 1], {in[j]}))) return rc;
   const PackedBwd b = {o, lse, dout, dq, dk, dv, o_stride, dout_stride, dq_stride, dk_stride,
                        dv_stride};
   return cuda_status(launch_packed_bwd(a, b, workspace, static_cast<cudaStream_t>(stream)),

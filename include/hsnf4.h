@@ -490,7 +490,7 @@ typedef struct {
 } hsnf4_packed_attention;
 
 /* o bf16 [Tq, H, head_dim] (o_stride as above), lse fp32 [H, Tq].  o and
- * lse may not overlap the inputs.  Errors: INVALID (sizes, strides,
+ * lse may not overlap the inputs (cu_q and cu_k among them).  Errors: INVALID (sizes, strides,
  * pointers), CUDA. */
 int decoder_attention_packed_fwd(const hsnf4_packed_attention *a, void *o, int64_t o_stride,
                                  float *lse, void *stream);

@@ -1,5 +1,6 @@
 """CPU checks of the training operators: what their kernels' sources have to
 keep to, and refusals beyond those of single arguments."""
+import ctypes
 import glob
 import os
 import re
@@ -52,3 +53,33 @@ def test_stack_refuses_lengths_and_ropes_when_it_is_made():
                dict(positions=torch.zeros(1, 64, dtype=torch.int32))):
         with pytest.raises(ValueError):
             DecoderStack(TINY, 1, 64, streamed=False, **kw)
+
+
+FAKE = 0x10000  # never dereferenced: validation fails first
+
+
+def _refused(rc, *words):
+    assert rc == hsnf4.ERR_INVALID, (rc, hsnf4.last_error())
+    for w in words:
+        assert w in hsnf4.last_error(), hsnf4.last_error()
+
+
+@pytest.mark.parametrize("name,at", [("cu_q", FAKE * 64), ("cu_k", FAKE * 80)])
+def test_attention_outputs_on_the_lengths_are_refused(name, at):
+    """Lengths that an earlier CTA or kernel of the call has overwritten."""
+    L = hsnf4.lib()
+    a = hsnf4.PackedAttentionC(FAKE, FAKE * 16, FAKE * 32, 0, 0, 0, FAKE * 64, FAKE * 80, 8, 8, 2,
+                               4, 2, 128, 1, 0.1)
+    r, near = ctypes.byref(a), at - 16  # (three lengths: 12 bytes)
+    _refused(L.decoder_attention_packed_fwd(r, near, 0, FAKE * 256, None), "o overlaps", name)
+    _refused(L.decoder_attention_packed_fwd(r, FAKE * 128, 0, near, None), "lse overlaps", name)
+    need = hsnf4.attention_packed_workspace_bytes(8, 8, 2, 4, 2, 128)
+
+    def bwd(dq=FAKE * 400, dk=FAKE * 500, dv=FAKE * 600, ws=FAKE * 1024):
+        return L.decoder_attention_packed_bwd(r, FAKE * 128, 0, FAKE * 256, FAKE * 300, 0, dq, 0, dk,
+                                              0, dv, 0, ws, need, None)
+
+    _refused(bwd(dq=near), "dq overlaps", name)
+    _refused(bwd(dk=near), "dk overlaps", name)
+    _refused(bwd(dv=near), "dv overlaps", name)
+    _refused(bwd(ws=at), "workspace overlaps", name)
