@@ -927,6 +927,11 @@ int lora_grad_plan(const hsnf4_grad* grads, int n, void* table, size_t table_byt
     r[m++] = {a, a + size * static_cast<uintptr_t>(g.n), i, a == o};
     if (a != o) r[m++] = {o, o + size * static_cast<uintptr_t>(g.n), i, true};
   }
+  // the table is written now, and later calls trust its addresses
+  const uintptr_t ta = reinterpret_cast<uintptr_t>(table), tb = ta + grad_table_bytes(n);
+  for (int j = 0; j < m; ++j)
+    if (r[j].a < tb && ta < r[j].b)
+      return fail(HSNF4_ERR_INVALID, "%s: the table overlaps tensor %d", fn, r[j].i);
   // in order of their starts, a range that is written meets another exactly
   // when it meets the furthest-reaching range before it, or the furthest
   // written one does
@@ -968,7 +973,14 @@ static int grad_call(const char* fn, const hsnf4_grad_plan* plan, float max_norm
                 static_cast<double>(max_norm));
   if (!norm || (reinterpret_cast<uintptr_t>(norm) & 3))
     return fail(HSNF4_ERR_INVALID, "%s: norm is NULL or not 4-byte aligned", fn);
-  int rc = check_workspace(fn, ws, ws_bytes, grad_workspace_bytes(plan->chunks));
+  const size_t need = grad_workspace_bytes(plan->chunks);
+  int rc = check_workspace(fn, ws, ws_bytes, need);
+  if (rc) return rc;
+  const int64_t table_bytes = static_cast<int64_t>(grad_table_bytes(plan->n));
+  const Rows rw = {ws, 0, static_cast<int64_t>(need / 2), 1, "workspace"}, rn = {norm, 0, 2, 1, "norm"},
+             rt = {plan->table, 0, table_bytes / 2, 1, "the plan's table"};
+  rc = check_disjoint(fn, rw, {rt, rn});
+  if (!rc) rc = check_disjoint(fn, rn, {rt});
   if (rc) return rc;
   return cuda_status(launch_grad_norm(plan->table, plan->n, plan->chunks, max_norm, scale, norm,
                                       ws, static_cast<cudaStream_t>(stream)),

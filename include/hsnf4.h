@@ -547,13 +547,15 @@ size_t lora_grad_table_bytes(int n);
 /* Fill the table (device memory of table_bytes >= lora_grad_table_bytes(n),
  * 16-byte aligned) on `stream`, wait for it, and fill the plan (host), which
  * calls on any stream may then use.  grads: host array of n (1..65536)
- * tensors.  Not during stream capture.  Errors: INVALID (sizes,
- * pointers, tensors that overlap), OOM (table), STATE (capture), CUDA. */
+ * tensors, none of them over the table.  Not during stream capture.  Errors:
+ * INVALID (sizes, pointers, overlaps), OOM (table), STATE (capture), CUDA. */
 int lora_grad_plan(const hsnf4_grad *grads, int n, void *table, size_t table_bytes,
                    hsnf4_grad_plan *plan, void *stream);
 
 /* Workspace bytes of the two calls below (at least 256; depends on the
- * device's SM count). */
+ * device's SM count).  Their workspace and norm may not overlap each other,
+ * the table or the tensors (the last is not checked: a plan's addresses are
+ * on the device). */
 size_t lora_grad_workspace(const hsnf4_grad_plan *plan);
 
 /* *norm (device fp32) = sqrt(sum g^2) over every tensor of the plan, the

@@ -83,3 +83,21 @@ def test_attention_outputs_on_the_lengths_are_refused(name, at):
     _refused(bwd(dk=near), "dk overlaps", name)
     _refused(bwd(dv=near), "dv overlaps", name)
     _refused(bwd(ws=at), "workspace overlaps", name)
+
+
+def test_gradient_table_workspace_and_norm_apart():
+    """The table holds addresses that kernels write to: nothing else may."""
+    L = hsnf4.lib()
+    size = int(L.lora_grad_table_bytes(2))
+    grads = (hsnf4.GradC * 2)(hsnf4.GradC(FAKE, FAKE * 2, 100, 0, 0),
+                              hsnf4.GradC(FAKE * 4, FAKE * 4, 100, 1, 0))
+    plan = hsnf4.GradPlanC()
+    for table, i in ((FAKE + 384, 0), (FAKE * 2 - size + 16, 0), (FAKE * 4 + 192, 1)):
+        _refused(L.lora_grad_plan(grads, 2, table, size, ctypes.byref(plan), None), "the table",
+                 f"tensor {i}")
+    plan = hsnf4.GradPlanC(FAKE, 3, 100, 2, 0)
+    p, need = ctypes.byref(plan), int(L.lora_grad_workspace(ctypes.byref(plan)))
+    for call in (L.lora_grad_norm, lambda p, *a: L.lora_grad_clip(p, 1.0, *a)):
+        _refused(call(p, FAKE * 2, FAKE, need, None), "workspace overlaps the plan's table")
+        _refused(call(p, FAKE + size - 4, FAKE * 2, need, None), "norm overlaps the plan's table")
+        _refused(call(p, FAKE * 2 + 4, FAKE * 2, need, None), "workspace overlaps norm")
