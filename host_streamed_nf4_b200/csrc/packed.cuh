@@ -25,6 +25,17 @@ struct PackedTile {
   int t;               // tile of the sequence (of its queries or of its keys)
 };
 
+// The tokens of [start, end) that a tensor of T has, from any two values.  Both
+// are clamped before they are subtracted: from one that is not the difference
+// of two int32 may wrap around to a length far beyond the tensor.
+struct Span {
+  int at, len;
+};
+__host__ __device__ __forceinline__ Span span_of(int start, int end, int T) {
+  const int a = start < 0 ? 0 : start > T ? T : start, b = end < 0 ? 0 : end > T ? T : end;
+  return {a, b > a ? b - a : 0};
+}
+
 // Tile number `slot` over all sequences in order, tiles of `rows` tokens of
 // the queries (or keys).  Within a sequence the longest work comes first
 // under a causal mask: query tiles from the last, key tiles from the first.
@@ -52,8 +63,8 @@ __device__ __forceinline__ bool find_tile(const PackedSeqs& S, bool keys, int sl
     int n[4], sum = 0;  // tiles to number
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int T = keys ? S.Tk : S.Tq, c = keys ? ck[j] : cq[j], e = keys ? ck[j + 1] : cq[j + 1];
-      const int len = max(min(e, T) - min(max(c, 0), T), 0);
+      const int len =
+          keys ? span_of(ck[j], ck[j + 1], S.Tk).len : span_of(cq[j], cq[j + 1], S.Tq).len;
       n[j] = (len + rows - 1) / rows;
       sum += n[j];
     }
@@ -62,7 +73,7 @@ __device__ __forceinline__ bool find_tile(const PackedSeqs& S, bool keys, int sl
       int top[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int lq = max(min(cq[j + 1], S.Tq) - min(max(cq[j], 0), S.Tq), 0);
+        const int lq = span_of(cq[j], cq[j + 1], S.Tq).len;
         top[j] = n[j] == 0 ? 0 : S.causal ? n[j] : 1 + (lq + rows - 1) / rows;
       }
       // tiles of level v and above
@@ -112,10 +123,11 @@ __device__ __forceinline__ bool find_tile(const PackedSeqs& S, bool keys, int sl
         at -= n[j];
       }
       x.t = __shfl_sync(0xffffffffu, t, src);
-      x.q0 = min(max(__shfl_sync(0xffffffffu, aq, src), 0), S.Tq);
-      x.lq = max(min(__shfl_sync(0xffffffffu, eq, src), S.Tq) - x.q0, 0);
-      x.k0 = min(max(__shfl_sync(0xffffffffu, ak, src), 0), S.Tk);
-      x.lk = max(min(__shfl_sync(0xffffffffu, ek, src), S.Tk) - x.k0, 0);
+      const Span q = span_of(__shfl_sync(0xffffffffu, aq, src), __shfl_sync(0xffffffffu, eq, src),
+                             S.Tq);
+      const Span k = span_of(__shfl_sync(0xffffffffu, ak, src), __shfl_sync(0xffffffffu, ek, src),
+                             S.Tk);
+      x = {q.at, q.len, k.at, k.len, __shfl_sync(0xffffffffu, t, src)};
       return true;
     }
     before = __shfl_sync(0xffffffffu, before + inc, 31);

@@ -76,6 +76,53 @@ def test_first_keys_with_scores_of_minus_infinity(d, H, KV, lq):
     ops._lse_within(lse, rl, "lse")
 
 
+def _guarded(rows, cols, mark, lead=8):
+    """A [rows, cols] bf16 tensor inside a larger one, and that."""
+    whole = torch.full((rows + 2 * lead, cols), mark, dtype=torch.bfloat16, device="cuda")
+    return whole[lead:lead + rows], whole
+
+
+MALFORMED = [[0, 400, 90], [-50, 30, 20], [90, 10, 1 << 30], [0, 0, 0], [0, 1 << 30, 90, 1 << 30, 0],
+             [-50, 1900, 20, 2000, -1], [1 << 30, 0, 700, 0, 700], [0, 0, 0, 0, 0],
+             [-(1 << 31), (1 << 31) - 1], [(1 << 31) - 1, -(1 << 31)]]
+
+
+@pytest.mark.parametrize("T", [100, 2000])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_malformed_lengths_write_nothing_outside(T, d, causal):
+    """Every tensor lies inside a larger one whose values stay as they are;
+    sequences that are all empty change nothing at all."""
+    H, KV, mark = 4, 1, 7.0
+    g = ops._gen(T + d)
+    ins = [_guarded(T, n * d, ops.NAN) for n in (H, KV, KV, H)]
+    for t, _ in ins:
+        t.copy_(ops._normal(t.shape, g))
+    q, k, v, do = (t for t, _ in ins)
+    for cu in MALFORMED:
+        n_seq = len(cu) - 1
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        outs = [_guarded(T, n * d, mark) for n in (H, H, KV, KV)]
+        flat = torch.full((H * T + 128,), mark, device="cuda")
+        lse = flat[64:64 + H * T].view(H, T)
+        need = hsnf4.attention_packed_workspace_bytes(T, T, n_seq, H, KV, d)
+        scratch = torch.full((need + 1024,), 0x5A, dtype=torch.uint8, device="cuda")
+        o, dq, dk, dv = (t for t, _ in outs)
+        hsnf4.attention_packed_fwd(q, k, v, cu, H, KV, causal=causal, o=o, lse=lse)
+        hsnf4.attention_packed_bwd(q, k, v, o, lse, do, cu, H, KV, causal=causal, dq=dq, dk=dk,
+                                   dv=dv, workspace=scratch[512:512 + need])
+        torch.cuda.synchronize()
+        assert hsnf4.device_status() == 0
+        for t, whole in outs:
+            assert (whole[:8] == mark).all() and (whole[8 + T:] == mark).all()
+            if not cu.any():
+                assert (t == mark).all()
+        assert (flat[:64] == mark).all() and (flat[64 + H * T:] == mark).all()
+        assert (scratch[:512] == 0x5A).all() and (scratch[512 + need:] == 0x5A).all()
+        if not cu.any():
+            assert (lse == mark).all()
+
+
 # ---------------------------------------------------------------- gradient norm
 
 @pytest.mark.parametrize("given", [True, False])

@@ -4,6 +4,7 @@ import ctypes
 import glob
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -101,3 +102,31 @@ def test_gradient_table_workspace_and_norm_apart():
         _refused(call(p, FAKE * 2, FAKE, need, None), "workspace overlaps the plan's table")
         _refused(call(p, FAKE + size - 4, FAKE * 2, need, None), "norm overlaps the plan's table")
         _refused(call(p, FAKE * 2 + 4, FAKE * 2, need, None), "workspace overlaps norm")
+
+
+def test_lengths_of_any_int32_stay_inside_the_tensor(tmp_path):
+    """The kernels' clamping of cumulative lengths, run on the CPU: the ends
+    of int32 among them, whose difference is none."""
+    src = tmp_path / "span.cu"
+    src.write_text("""
+#include <stdio.h>
+#include "packed.cuh"
+int main() {
+  int start, end, T;
+  while (scanf("%d %d %d", &start, &end, &T) == 3) {
+    const hsnf4::Span s = hsnf4::span_of(start, end, T);
+    printf("%d %d\\n", s.at, s.len);
+  }
+}
+""")
+    exe = tmp_path / "span"
+    subprocess.run([build.NVCC, *build.ARCH, *build.CFLAGS, str(src), "-o", str(exe)], check=True,
+                   capture_output=True)
+    ends = [-2 ** 31, -2 ** 31 + 1, -50, -1, 0, 1, 99, 100, 101, 400, 1 << 24, 1 << 30, 2 ** 31 - 1]
+    cases = [(a, b, T) for a in ends for b in ends for T in (1, 100, 2000, 1 << 24)]
+    out = subprocess.run([str(exe)], input="\n".join("%d %d %d" % c for c in cases), check=True,
+                         capture_output=True, text=True).stdout.split()
+    assert len(out) == 2 * len(cases)
+    for (a, b, T), at, n in zip(cases, out[::2], out[1::2]):
+        lo, hi = min(max(a, 0), T), min(max(b, 0), T)
+        assert (int(at), int(n)) == (lo, max(hi - lo, 0)), (a, b, T)
