@@ -76,6 +76,44 @@ def test_first_keys_with_scores_of_minus_infinity(d, H, KV, lq):
     ops._lse_within(lse, rl, "lse")
 
 
+@pytest.mark.parametrize("lq,lk,causal", [
+    # (6144 queries a sequence and more: two query tiles per CTA)
+    ([6144], None, True), ([6145], None, True), ([6273], None, False),  # a last pair of 1, of 129
+    ([6200], [6500], True), ([6300], [4000], True), ([6300], [133], False),
+    ([12200, 150], None, True)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_two_query_tiles_per_cta(lq, lk, causal, d):
+    ops.test_packed_attention(lq, lk, 2, 1, causal, d, "padded")
+
+
+@pytest.mark.parametrize("d,causal", [(64, True), (128, True), (64, False), (128, False)])
+def test_two_query_tiles_and_a_maximum_that_moves(d, causal):
+    """Keys that grow along the sequence: late tiles pass the maximum so far
+    by far, and the sums are scaled anew."""
+    n, H, KV = 6500, 2, 1
+    q, k, v, do = ops._attn_inputs([n], [n], H, KV, d, "fused", 60 + d)
+    k *= torch.linspace(0.02, 3.0, n, device="cuda")[:, None].bfloat16()
+    cu, scale = ops._cu([n]), d ** -0.5
+    o, lse = hsnf4.attention_packed_fwd(q, k, v, cu, H, KV, causal=causal)
+    grads = hsnf4.attention_packed_bwd(q, k, v, o, lse, do, cu, H, KV, causal=causal)
+    torch.cuda.synchronize()
+    assert hsnf4.device_status() == 0
+    args = ([n], [n], H, KV, causal, scale)
+    ref, rl, tol = ops._attn_ref(q, k, v, *args)
+    ops._within(o, ref, tol + 1e-30, "o")
+    ops._lse_within(lse, rl, "lse")
+    for got, (r, t), name in zip(grads, ops._attn_ref(q, k, v, *args, o, lse, do),
+                                 ("dq", "dk", "dv")):
+        ops._within(got, r, t, name)
+
+
+@pytest.mark.parametrize("H,KV,d,causal", [(4, 2, 128, True), (7, 1, 64, True),
+                                           (16, 16, 64, False)])
+def test_one_long_sequence_among_short_ones(H, KV, d, causal):
+    """The kernels are chosen by the mean length, which hides it."""
+    ops.test_packed_attention([50] * 20 + [3000] + [50] * 20, None, H, KV, causal, d, "padded")
+
+
 def _guarded(rows, cols, mark, lead=8):
     """A [rows, cols] bf16 tensor inside a larger one, and that."""
     whole = torch.full((rows + 2 * lead, cols), mark, dtype=torch.bfloat16, device="cuda")
@@ -121,6 +159,20 @@ def test_malformed_lengths_write_nothing_outside(T, d, causal):
         assert (scratch[:512] == 0x5A).all() and (scratch[512 + need:] == 0x5A).all()
         if not cu.any():
             assert (lse == mark).all()
+
+
+# ---------------------------------------------------------------- rotary positions
+
+@pytest.mark.parametrize("T,H,KV,d,half,sections,pairing", [
+    # a token's heads in two and four passes of the threads, also uneven ones
+    (37, 32, 8, 128, 64, None, "half"), (64, 40, 8, 128, 64, [16, 24, 24], "half"),
+    (33, 33, 2, 128, 64, None, "half"), (50, 28, 4, 128, 64, [16, 24, 24], "adjacent"),
+    (29, 56, 8, 128, 64, None, "adjacent"), (41, 31, 2, 128, 64, None, "adjacent"),
+    (9001, 32, 8, 128, 64, [16, 24, 24], "half"), (70, 17, 8, 256, 64, None, "half")])
+@pytest.mark.parametrize("way", ["fwd", "bwd"])
+@pytest.mark.parametrize("form", ["plain", "fused", "in_place"])
+def test_rope_of_more_heads_than_threads(T, H, KV, d, half, sections, pairing, way, form):
+    ops.test_rope(T, H, KV, d, half, sections, pairing, way, form)
 
 
 # ---------------------------------------------------------------- gradient norm
