@@ -48,9 +48,16 @@ class DecoderStack(LayerStack):
                  seq_lens=None, **kw):
         """rope: an hsnf4.Rope of the family's head_dim; positions: int32
         [n_axes, T] on the device (default: each sequence counts from 0, on
-        every axis).  seq_lens: lengths of the packed sequences, T together.
-        `positions` and `cu` (the sequences' starts and T) may be filled anew
-        between steps."""
+        every axis).  seq_lens: lengths of the packed sequences, T together
+        (0 among them); None: one sequence, on the mma.sync attention kernels,
+        whose roundings differ from those that [T] takes (tcgen05, faster).
+
+        `positions` and `cu` (the sequences' starts, and T) may be filled anew
+        between steps, for as many sequences.  `cu` has to start at 0 and end
+        at T: attention leaves rows outside every sequence as they are, and the
+        projections around it would read what an earlier step left there.  So
+        padding is a sequence of its own, the last one say, with zeros in
+        its rows of `dh_top`: then it adds nothing to any gradient."""
         if family.head_dim != 128:
             raise ValueError("the attention kernels take head_dim 128")
         kw.setdefault("grouping", "decoder")
