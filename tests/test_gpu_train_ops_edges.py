@@ -114,6 +114,46 @@ def test_one_long_sequence_among_short_ones(H, KV, d, causal):
     ops.test_packed_attention([50] * 20 + [3000] + [50] * 20, None, H, KV, causal, d, "padded")
 
 
+@pytest.mark.parametrize("d,H,KV,lens", [(128, 28, 4, [300, 1, 211]), (64, 6, 6, [40] * 9),
+                                         (64, 8, 2, [700])])
+def test_every_tensor_a_part_of_wider_rows(d, H, KV, lens):
+    """q, k, v and their gradients as columns of one tensor each, turned in
+    place there, o and its gradient in rows with room beside them: bit for
+    bit what separate tensors give, and the rest stays as it was."""
+    T, g, w = sum(lens), ops._gen(d + H), (H + 2 * KV) * d
+    cu, pos = ops._cu(lens), torch.arange(T, dtype=torch.int32, device="cuda")
+    rope = hsnf4.Rope(d, hsnf4.rope_inv_freq(d, 1e4))
+
+    def parts(buf):
+        return buf[:, :H * d], buf[:, H * d:(H + KV) * d], buf[:, (H + KV) * d:w]
+
+    x, do = ops._normal((T, w), g), ops._normal((T, H * d), g)
+    q, k, v = (t.contiguous() for t in parts(x))
+    q, k = hsnf4.rope_fwd(rope, pos, q, k)
+    o, lse = hsnf4.attention_packed_fwd(q, k, v, cu, H, KV)
+    dq, dk, dv = hsnf4.attention_packed_bwd(q, k, v, o, lse, do, cu, H, KV)
+    want = [q, k, v, o, *hsnf4.rope_bwd(rope, pos, dq, dk), dv]
+
+    wide = torch.full((T, w + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, :w] = x
+    grad = torch.full((T, w + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((T, 2 * H * d + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    o, dout = out[:, 8:8 + H * d], out[:, 16 + H * d:]
+    dout.copy_(do)
+    q, k, v = parts(wide)
+    dq, dk, dv = parts(grad)
+    hsnf4.rope_fwd(rope, pos, q, k, q, k)
+    _, lse2 = hsnf4.attention_packed_fwd(q, k, v, cu, H, KV, o=o)
+    hsnf4.attention_packed_bwd(q, k, v, o, lse2, dout, cu, H, KV, dq=dq, dk=dk, dv=dv)
+    hsnf4.rope_bwd(rope, pos, dq, dk, dq, dk)
+    torch.cuda.synchronize()
+    assert hsnf4.device_status() == 0 and torch.equal(lse, lse2)
+    for got, ref in zip((q, k, v, o, dq, dk, dv), want):
+        assert torch.equal(got, ref)
+    assert torch.equal(dout, do) and (wide[:, w:] == 7).all() and (grad[:, w:] == 7).all()
+    assert (out[:, :8] == 7).all() and (out[:, 8 + H * d:16 + H * d] == 7).all()
+
+
 def _guarded(rows, cols, mark, lead=8):
     """A [rows, cols] bf16 tensor inside a larger one, and that."""
     whole = torch.full((rows + 2 * lead, cols), mark, dtype=torch.bfloat16, device="cuda")
