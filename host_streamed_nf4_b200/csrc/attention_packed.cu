@@ -158,11 +158,11 @@ struct FwdGeo {
 // bf16), an O per tile.  The tensor cores work on one tile's products while
 // the warps of the other (of the other CTA) compute its probabilities.
 //
-// One causal sequence, head_dim 128: 16384 tokens of 32/8 heads 2050 us, 1070
-// TFLOP/s, where the power limit lowers the clock to about 1.64 GHz with the
-// tensor pipe 53 % busy; 4096 of 28/4 heads 119 us.  Short calls are bound by
-// the latency of a CTA's start, chain and end, 5 us and 2 us a step (nine
-// sequences of 512 tokens: 8.5 us).
+// One causal sequence, head_dim 128: 16384 tokens of 32/8 heads 2115 us, 1040
+// TFLOP/s, in a loop, where the power limit lowers the clock to about 1.64 GHz
+// with the tensor pipe 53 % busy (a call from rest: 1890); 4096 of 28/4 heads
+// 119 us.  Short calls are bound by the latency of a CTA's start, chain and
+// end, 5 us and 2 us a step (nine sequences of 512 tokens: 8.6 us).
 template <int D, int NQ>
 __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
     packed_fwd_tc(const __grid_constant__ FwdTc P) {
@@ -476,8 +476,9 @@ __global__ void __launch_bounds__(FwdGeo<D, NQ>::kThreads, 3 - NQ)
 // tile's products are half as long as with 128 and the chain from scores to
 // probabilities to the next scores weighs twice as much; four chains at once
 // hide it.  A thread owns a row (no exchange between warps).  One sequence of
-// 8192, 16/16 heads, no mask: 377 us, 730 TFLOP/s with issue slots 58 % and the
-// special-function unit 50 % busy.
+// 8192, 16/16 heads, no mask: 377 us, 730 TFLOP/s, in a short burst with issue
+// slots 58 % and the special-function unit 50 % busy; 465 us in a loop at the
+// power limit.
 struct Fwd64Geo {
   static constexpr int kD = 64;
   static constexpr int kQ = tile_bytes<kD>(), kHalf = kStep * kD * 2;  // bytes of Q; of K or V
@@ -778,10 +779,10 @@ struct KvGeo {
 // end and waits hide behind the other's products: a tile's start and end are
 // about 10000 cycles of latency, as much as eight steps.  S of the next step
 // is computed as soon as the threads have read this one's; its dP follows
-// dQ's product, which reads dS.  16384 tokens of 32/8 heads of 128: 2815 us,
-// 1180 TFLOP/s of its three products at the power limit (products of 64
-// columns run at two thirds of the rate of 128); 8150 tokens in 17, 28/4 heads:
-// 145 us.
+// dQ's product, which reads dS.  16384 tokens of 32/8 heads of 128: 3080 us,
+// 1070 TFLOP/s of its three products, in a loop at the power limit (products
+// of 64 columns run at two thirds of the rate of 128), 2740 from rest; 8150
+// tokens in 17, 28/4 heads: 145 us.
 template <int D>
 struct DqGeo {
   static constexpr int kTile = tile_bytes<D>();  // Q, dO, O: 128 rows
@@ -1085,10 +1086,10 @@ __device__ __forceinline__ int64_t part_at(const BwdTc& P, int slot, int kh, int
 // scores are computed transposed (a thread owns a key row, 32 of the step's
 // queries), so that P^T and dS^T, written as bf16 over the scores they came
 // from, are the tensor-memory operands of dV += P^T dO and dK += dS^T Q.
-// TMEM: S^T, dP^T, dV, dK.  16384 tokens of 32/8 heads of 128: 3280 us, 1357
-// TFLOP/s of its four products, 0.97 of a library product's rate under the same
-// power limit; 8150 tokens in 17, 28/4 heads: 145 us, 1.7 us a step and 9 us of
-// a CTA's start and end.  While the threads
+// TMEM: S^T, dP^T, dV, dK.  16384 tokens of 32/8 heads of 128: 3520 us, 1250
+// TFLOP/s of its four products, in a loop at the power limit, 0.90 of a library
+// product's rate under it (3340 us from rest); 8150 tokens in 17, 28/4 heads:
+// 149 us, 1.7 us a step and 9 us of a CTA's start and end.  While the threads
 // compute P^T the tensor cores run the tile before's dK product and this
 // tile's dP^T; while they compute dS^T, dV and the next S^T.
 template <int D, int CTAS>
@@ -1505,6 +1506,10 @@ bool map_rows(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The host knows the sequences' number and tokens, not their lengths: this and
+// the rules below go by the mean.  One of 8000 tokens among 40 of 50 takes the
+// kernels for short ones: 446 us forward and 1469 backward (28/4 heads of 128,
+// causal), the two parts alone 410 + 33 and 1340 + 96.
 int64_t most_tiles(int64_t T, int n_seq, int rows) {
   return T / rows + std::min<int64_t>(n_seq, T);
 }
@@ -1687,9 +1692,9 @@ cudaError_t launch_packed_fwd(const hsnf4_packed_attention& a, void* o, int64_t 
   P.KV = a.KV;
   P.c = a.scale * kLog2e;
   // One query tile per CTA unless the sequences are long on average.  28/4
-  // heads, head_dim 128, causal, one tile against two: 64 sequences of 64
-  // tokens 49 / 99 us, 16 of 512 70 / 84, one of 4096 117 / 118, one of 8192
-  // 429 / 406, one of 16384 (32/8 heads) 1940 / 1770.
+  // heads, head_dim 128, causal, one tile against two, short bursts from rest:
+  // 64 sequences of 64 tokens 48 / 88 us, 16 of 512 70 / 83, one of 4096 119 /
+  // 122, one of 8192 438 / 417, one of 16384 (32/8 heads) 1935 / 1820 to 1875.
   const bool two = a.Tq >= 6144 * static_cast<int64_t>(a.n_seq);
   if (a.head_dim == 128) return two ? fwd_tc<128, 2>(P, st) : fwd_tc<128, 1>(P, st);
   if (many) return fwd64_tc(P, st);

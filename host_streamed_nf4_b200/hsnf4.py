@@ -688,7 +688,11 @@ class GradSet:
     mix) for grad_norm and grad_clip.  outs: where clipped gradients go, each
     of its gradient's type and size (default: in place).  The set keeps the
     tensors' addresses, so their memory must not be replaced, and a graph that
-    captured a call needs the set for as long as it is replayed."""
+    captured a call needs the set for as long as it is replayed.
+
+    Make it once, for gradients that stay where they are: it fills a table on
+    the device and waits for that, 0.04 to 0.1 ms for 14 tensors, 0.9 to 1.7 ms
+    for 1120, as long as plain torch operations take to clip them."""
 
     def __init__(self, tensors, outs=None, stream=None):
         self.tensors = list(tensors)

@@ -496,7 +496,9 @@ int decoder_attention_packed_fwd(const hsnf4_packed_attention *a, void *o, int64
                                  float *lse, void *stream);
 
 /* Workspace bytes of the backward (depends on the device's SM count); 0 for
- * sizes that it refuses. */
+ * sizes that it refuses.  4 H Tq, and where key tiles are few the fp32 parts of
+ * dK and dV: at most about 310 MB with 148 SMs and head_dim 128 (169 MB for 8150
+ * tokens in 17 sequences, 28/4 heads). */
 size_t decoder_attention_packed_workspace(int64_t Tq, int64_t Tk, int n_seq, int H, int KV,
                                           int head_dim);
 
@@ -519,7 +521,9 @@ int decoder_attention_packed_bwd(const hsnf4_packed_attention *a, const void *o,
 /* Gradient norm and clipping over many tensors (a stack has 14 adapter
  * gradients a layer).  Describe the tensors once, then clip every step:
  * the plan keeps their addresses in a table in caller-owned device memory,
- * so they must stay where they are while the plan is used. */
+ * so they must stay where they are while the plan is used.  Making one costs
+ * host time and a wait, 0.04 to 0.1 ms for 14 tensors and 0.9 to 1.7 ms for 1120
+ * from Python, so gradients that are new tensors every step gain little. */
 #define HSNF4_F32 0
 #define HSNF4_BF16 1
 #define HSNF4_F16 2
@@ -565,7 +569,7 @@ int lora_grad_norm(const hsnf4_grad_plan *plan, float *norm, void *workspace, si
                    void *stream);
 
 /* *norm as above, then out = round(g * c), c = min(1, max_norm / (norm +
- * 1e-6)), for every tensor.  max_norm >= 0, infinity: c = 1.  A norm that
+ * 1e-6)) rounded to fp32, for every tensor.  max_norm >= 0, infinity: c = 1.  A norm that
  * is not finite gives c = 0 (infinite) or NaN, as the formula does.  In
  * place, a tensor that c = 1 would leave alone is not written.  workspace:
  * device scratch, 256-byte aligned, one per call that may run at the same
