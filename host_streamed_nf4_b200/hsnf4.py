@@ -470,6 +470,8 @@ _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _cur_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or \
+    torch.cuda.is_current_stream_capturing
 
 
 def _launch(index: int, stream, fn, *args):
@@ -723,28 +725,43 @@ class GradSet:
                                                                ctypes.byref(self.plan), *a))
         self.workspace = self.new_workspace(stream)
         self._ref = ctypes.byref(self.plan)
-        # the streams that the table's and workspace's memory is known to be used on
-        self._streams = {_raw_stream(index) if stream is None else stream.cuda_stream}
+        # a workspace per stream that calls were made on
+        self._spaces = {_raw_stream(index) if stream is None else stream.cuda_stream:
+                        self.workspace}
 
     def new_workspace(self, stream=None) -> torch.Tensor:
-        """A workspace for calls on `stream` that may run at the same time as
-        others on this set (which otherwise share its own)."""
+        """A workspace for calls on `stream`.  Without one, the calls on a
+        stream share the set's for that stream, and a captured call has one of
+        its graph, so that streams and graphs may run at the same time."""
         with torch.cuda.device(self.index):
             n = int(lib().lora_grad_workspace(ctypes.byref(self.plan)))
         return _new(torch.empty, n, torch.uint8, self.device, stream)
 
+    def _first_call_on(self, stream, at):
+        if stream is not None and stream.device.index != self.index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+        used = torch.cuda.current_stream(self.index) if stream is None else stream
+        # else a set dropped after the call would give its table back too early
+        self.table.record_stream(used)
+        self.workspace.record_stream(used)
+        if _capturing():  # the stream's memory is the graph's now; a later call makes the set's
+            return None
+        ws = self._spaces[at] = self.new_workspace(stream)
+        return ws
+
     def _call(self, fn, args, norm, workspace, stream):
         if norm is None:
             norm = _new(torch.empty, (), _f32, self.device, stream)
-        ws = self.workspace if workspace is None else workspace
-        if workspace is not None and (ws.get_device() != self.index or not ws.is_contiguous()):
-            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
         at = _raw_stream(self.index) if stream is None else stream.cuda_stream
-        if at not in self._streams:  # else a set dropped after the call frees them too early
-            used = torch.cuda.current_stream(self.index) if stream is None else stream
-            self.table.record_stream(used)
-            self.workspace.record_stream(used)
-            self._streams.add(at)
+        ws = self._spaces.get(at)
+        if ws is None:
+            ws = self._first_call_on(stream, at)
+        if workspace is not None:
+            ws = workspace
+            if ws.get_device() != self.index or not ws.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        elif _capturing():
+            ws = self.new_workspace(stream)
         _launch(self.index, stream, fn, self._ref, *args,
                 _plain(norm, "norm", self.index, _f32, 1), ws.data_ptr(), ws.nbytes)
         return norm

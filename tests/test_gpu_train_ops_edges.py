@@ -246,3 +246,32 @@ def test_set_dropped_while_another_stream_uses_it(given):
     torch.cuda.synchronize()
     # the call before left a norm of 1 / (1 + 1e-6 / norm)
     assert abs(float(norm) - 1.0) <= 2.0 ** -20
+
+
+def test_streams_and_graphs_of_one_set_have_a_workspace_each():
+    """Norms of one set on two streams and in two graphs at once: none of
+    them writes where another one's sums are."""
+    g = ops._gen(70)
+    grads = [ops._normal((n,), g, torch.float32) for n in (5, 3_000_000, 4097)]
+    gs = hsnf4.GradSet(grads)
+    want = hsnf4.grad_norm(gs)
+    graphs, norms = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            norms.append([hsnf4.grad_norm(gs) for _ in range(20)])
+        graphs.append(graph)
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    gs.workspace.fill_(0xFF)  # of the calls on this stream: no other may touch it
+    torch.cuda.synchronize()
+    eager = []
+    for graph, stream in zip(graphs, side):
+        with torch.cuda.stream(stream):
+            graph.replay()
+            eager += [hsnf4.grad_norm(gs) for _ in range(20)]
+        eager += [hsnf4.grad_norm(gs, stream=stream) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert (gs.workspace == 0xFF).all()
+    for got in eager + norms[0] + norms[1]:
+        assert torch.equal(got, want)
+    assert torch.equal(hsnf4.grad_norm(gs), want)
